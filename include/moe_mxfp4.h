@@ -380,6 +380,163 @@ int moe_matvec_mxfp4(const void* w_packed, int n_out, int d_in, const int8_t* q,
 int moe_debug_block_dots(const void* w_packed, int n_out, int d_in, const int8_t* q,
                          int64_t ld_q, int rows, int32_t* dots, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The operators around the routed experts: a decoder block's norms, gates
+ * and residual, its router's scoring rule, and its dense projections in int8.
+ *
+ * Element types of the calls below. */
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
+
+/* Which int8 codes a norm writes beside its rows: none; a scale per
+ * 32-element block, as moe_quant_act_q8 (what the routed experts read); a
+ * scale per row, as moe_quant_row_q8 (what moe_linear_q8 reads). */
+#define MOE_QUANT_NONE 0
+#define MOE_QUANT_BLOCK 1
+#define MOE_QUANT_ROW 2
+
+/* Norms before and after a block.  With rms(v) = v / sqrt(mean(v^2) + eps)
+ * over a row:
+ *   before the block   h = rms(x) * pre_w
+ *   after the block    out = residual_scale * residual + gate * b,
+ *                      b = rms(y) * post_w  (post_norm = 1)  or  y  (0)
+ * pre_w, post_w f32 [d_model] (device; NULL: ones).  1 <= d_model <= 16384,
+ * eps > 0, residual_scale finite. */
+typedef struct moe_norm {
+  int d_model;
+  int post_norm; /* 0 or 1: whether moe_norm_post normalises the block's output */
+  float eps;
+  float residual_scale;
+  const float* pre_w;
+  const float* post_w;
+} moe_norm_t;
+
+/* Before the block: h = rms(x) * pre_w, one pass over x.
+ *   x   f32/bf16 [rows][ld_x] (device)
+ *   h   f32/bf16 [rows][ld_h] (device, out), or NULL where only codes are
+ *       wanted; may be x itself (same type and leading dimension)
+ *   quant, q, ld_q, qs, ld_qs   codes of the row as it is written (of its
+ *       bf16 values where h is bf16; in f32 where h is NULL):
+ *       MOE_QUANT_BLOCK  d_model % 32 == 0, qs f32 [rows][ld_qs]
+ *       MOE_QUANT_ROW    qs f32 [rows], row r's scale at qs[r * ld_qs]
+ *       q int8 [rows][ld_q], 8-byte aligned, ld_q % 8 == 0; bytes of a row
+ *       past d_model are left alone.  MOE_QUANT_NONE: q and qs are not read.
+ * h or codes (or both) must be asked for.  Squares are summed in fp32 in an
+ * order set by d_model alone, so a row's bits do not depend on the rows that
+ * share a call, on strides or on alignment; |x| up to 2^56 does not
+ * overflow.  A row with an infinity or a NaN gives what the formula gives,
+ * for that row alone.  Rows need no alignment beyond their elements' (16
+ * bytes and d_model % 8 == 0 are the fast form).  rows == 0 is a no-op. */
+int moe_norm_pre(const moe_norm_t* N, const void* x, int x_type, int64_t ld_x, int rows,
+                 void* h, int h_type, int64_t ld_h, int quant, int8_t* q, int64_t ld_q,
+                 float* qs, int64_t ld_qs, void* stream);
+
+/* After the block: out as above, and in the same pass, with `next` set, the
+ * next block's h = rms(out) * next->pre_w (and its codes).
+ *   y    f32/bf16 [rows][ld_y] (device) the block's output
+ *   res  f32/bf16 [rows][ld_res] (device) the residual stream
+ *   gate f32/bf16 (device) or NULL (1): element (t, d) is
+ *        gate[t * gate_row + d * gate_col]; gate_row >= 0, gate_col 0 or 1
+ *        (0 and 0: one number; 0 and 1: per channel; gate_row and 0: per
+ *        token; gate_row and 1: per element)
+ *   out  of res's type [rows][ld_out] (device, out); may be res itself, or y
+ *        where its type is the same (with the same leading dimension)
+ *   next, h .. ld_qs  as for moe_norm_pre, of `out` as it is stored (rounded
+ *        to bf16 where it is bf16), so the result has the bits of
+ *        moe_norm_pre(next, out); next == NULL: not read.  next->d_model
+ *        must be N->d_model.
+ * Each output buffer is distinct from the others. */
+int moe_norm_post(const moe_norm_t* N, const void* y, int y_type, int64_t ld_y,
+                  const void* res, int res_type, int64_t ld_res, const void* gate,
+                  int gate_type, int64_t gate_row, int64_t gate_col, int rows, void* out,
+                  int64_t ld_out, const moe_norm_t* next, void* h, int h_type, int64_t ld_h,
+                  int quant, int8_t* q, int64_t ld_q, float* qs, int64_t ld_qs, void* stream);
+
+/* Router with a scoring rule, for checkpoints whose router is not the plain
+ * one of moe_route_group.  Per row, for the experts whose logit is neither
+ * NaN nor -infinity (-infinity takes an expert out of the row's reach):
+ *   s      = softmax of the row's logits (MOE_SCORE_SOFTMAX) or the sigmoid
+ *            of each (MOE_SCORE_SIGMOID), fp32
+ *   key    = s + bias[e]                  (bias NULL: s)
+ *   groups of n_experts / n_groups consecutive experts are ranked by their
+ *            largest key (MOE_GROUP_MAX) or the sum of their two largest
+ *            (MOE_GROUP_TOP2); only the best top_groups stay
+ *   picks  = the top_k largest keys left, in that order; ties, here and among
+ *            groups, go to the lower index
+ *   w      = s of the pick (without the bias), divided by the picks' sum
+ *            (added in slot order) if renorm and the sum is not 0, times scale
+ * Where fewer than top_k experts are left, the remaining slots hold id -1
+ * and w 0 and are absent from sorted, as a route that the device does not own
+ * is in moe_route_group.  A row whose largest logit is +infinity shares the
+ * softmax among the experts that hold it. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2 1
+typedef struct moe_router_rule {
+  int n_experts;   /* 1..512 */
+  int top_k;       /* 1..min(MOE_MAX_TOP_K, top_groups * n_experts / n_groups) */
+  int n_groups;    /* 1..64, divides n_experts */
+  int top_groups;  /* 1..n_groups */
+  int score;       /* MOE_SCORE_* */
+  int group_score; /* MOE_GROUP_* (not read with one group) */
+  int renorm;      /* 0 or 1 */
+  float scale;     /* finite */
+  const float* bias; /* f32 [n_experts] (device), finite, or NULL */
+} moe_router_rule_t;
+
+/* Bytes of workspace moe_route_scored needs for `rows` rows (0 for decode
+ * rows; 0 as well for a rule that it rejects). */
+size_t moe_route_scored_workspace_bytes(const moe_router_rule_t* R, int rows);
+
+/*   logits f32/bf16 [rows][ld_l] (device), ld_l >= n_experts
+ *   ids .. sorted (device, out)  as moe_route_group's; positions of sorted
+ *          from offsets[n_experts] on hold -1
+ *   ws     workspace (device, 16-byte aligned; NULL where 0 bytes are needed)
+ * rows*top_k <= 2^24; rows == 0 writes zero counts and offsets. */
+int moe_route_scored(const moe_router_rule_t* R, const void* logits, int l_type, int64_t ld_l,
+                     int rows, int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
+                     int32_t* sorted, void* ws, size_t ws_bytes, void* stream);
+
+/* int8 codes with one scale per row: of activations per token, or of a
+ * weight matrix [n_out][d_in] per output channel.
+ *   amax = max |x| over the row, d = amax / 127 (fp32, correctly rounded),
+ *   q = clamp(rint(x / d), -127, 127) (fp32 division, ties to even);
+ *   an all-zero row gives d = 0 and q = 0.
+ *   x      f32/bf16 [rows][ld_x] (device)
+ *   q      int8 [rows][ld_q] (device, 8-byte aligned, ld_q % 8 == 0)
+ *   scales f32 [rows] (device)
+ * cols >= 1; rows == 0 is a no-op.  NaN/Inf inputs are outside the contract. */
+int moe_quant_row_q8(const void* x, int x_type, int64_t ld_x, int rows, int cols, int8_t* q,
+                     int64_t ld_q, float* scales, void* stream);
+
+/* Dense projection of int8 codes:
+ *   y[t][n] = qs[t] * w_scales[n] * sum_k q[t][k] * w[n][k]  (+ bias[n])
+ * The sum is exact in int32 (so the result does not depend on tiles, splits
+ * or the rows that share a call), then one conversion and two products in
+ * fp32: fl(fl(sum * qs) * w_scales), then + bias, then one rounding to y's
+ * type. */
+typedef struct moe_linear {
+  int n_out, d_in;       /* n_out >= 1, 1 <= d_in <= 65536 */
+  const int8_t* w;       /* [n_out][ld_w] (device), row-major as stored; 16-byte aligned */
+  int64_t ld_w;          /* >= d_in, % 16 == 0; the bytes past d_in are not used */
+  const float* w_scales; /* f32 [n_out] (device) */
+  const float* bias;     /* f32 [n_out] (device) or NULL */
+} moe_linear_t;
+
+/* Bytes of workspace moe_linear_q8 needs for `rows` rows (can be 0). */
+size_t moe_linear_q8_workspace_bytes(const moe_linear_t* L, int rows);
+
+/*   q  int8 [rows][ld_q] (device, 16-byte aligned, ld_q % 16 == 0), any codes
+ *      -128..127; bytes past d_in are not used
+ *   qs f32 [rows] (device)
+ *   y  f32/bf16 [rows][ld_y] (device, out), ld_y >= n_out
+ *   ws workspace (device, 16-byte aligned; NULL where 0 bytes are needed)
+ * rows >= 0 (0: a no-op), from one decoded token to prefill chunks. */
+int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_q, const float* qs,
+                  int rows, void* y, int y_type, int64_t ld_y, void* ws, size_t ws_bytes,
+                  void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* moe_status_string(int status);
 

@@ -13,6 +13,12 @@ import os
 
 import torch
 
+from . import block
+from .block import (  # noqa: F401
+    Linear, Norm, RouterRule, codes_buffer, moe_linear_q8, moe_linear_q8_workspace_bytes,
+    moe_norm_post, moe_norm_pre, moe_quant_row_q8, moe_route_scored,
+    moe_route_scored_workspace_bytes, route_outputs)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_mxfp4.so")
 
@@ -27,7 +33,7 @@ EXPORTS = [
     "moe_ffn_stages",
     "moe_matvec_mxfp4",
     "moe_debug_block_dots", "moe_status_string",
-]
+] + block.EXPORTS
 
 MOE_STAGE_GATE_UP, MOE_STAGE_DOWN, MOE_STAGE_ALL, MOE_STAGE_REUSE_ACTS = 1, 2, 3, 4
 
@@ -90,6 +96,7 @@ def lib():
         for f in EXPORTS:
             if f not in ("moe_packed_bytes", "moe_ffn_workspace_bytes", "moe_status_string"):
                 getattr(L, f).restype = I
+        block.declare(L)
         _lib = L
     return _lib
 

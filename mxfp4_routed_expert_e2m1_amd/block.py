@@ -1,0 +1,324 @@
+"""The operators around the routed experts: block norms with gate and
+residual, scored routing, int8 linear layers.
+
+Like the rest of the binding, every function has the name of the C entry point
+it calls and only marshals arguments; a non-zero status raises MoeError.
+Element types and devices, which the C side cannot see, are checked here and
+raise TypeError or ValueError.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+P, I, I64, SZ, F = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float
+
+EXPORTS = ["moe_norm_pre", "moe_norm_post", "moe_route_scored",
+           "moe_route_scored_workspace_bytes", "moe_quant_row_q8", "moe_linear_q8",
+           "moe_linear_q8_workspace_bytes"]
+
+MOE_TYPE_F32, MOE_TYPE_BF16 = 0, 1
+MOE_QUANT_NONE, MOE_QUANT_BLOCK, MOE_QUANT_ROW = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+
+_TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
+_QUANT = {None: MOE_QUANT_NONE, "block": MOE_QUANT_BLOCK, "row": MOE_QUANT_ROW}
+_SCORE = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_GROUP = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
+
+
+class moe_norm_t(C.Structure):
+    _fields_ = [("d_model", I), ("post_norm", I), ("eps", F), ("residual_scale", F),
+                ("pre_w", P), ("post_w", P)]
+
+
+class moe_router_rule_t(C.Structure):
+    _fields_ = [("n_experts", I), ("top_k", I), ("n_groups", I), ("top_groups", I),
+                ("score", I), ("group_score", I), ("renorm", I), ("scale", F), ("bias", P)]
+
+
+class moe_linear_t(C.Structure):
+    _fields_ = [("n_out", I), ("d_in", I), ("w", P), ("ld_w", I64), ("w_scales", P),
+                ("bias", P)]
+
+
+def declare(L):
+    """Argument types of this module's entry points on the loaded library."""
+    norm, rule, lin = C.POINTER(moe_norm_t), C.POINTER(moe_router_rule_t), C.POINTER(moe_linear_t)
+    out = [P, I, I64, I, P, I64, P, I64]
+    L.moe_norm_pre.argtypes = [norm, P, I, I64, I] + out + [P]
+    L.moe_norm_post.argtypes = ([norm, P, I, I64, P, I, I64, P, I, I64, I64, I, P, I64, norm]
+                                + out + [P])
+    L.moe_route_scored_workspace_bytes.argtypes = [rule, I]
+    L.moe_route_scored.argtypes = [rule, P, I, I64, I, P, P, P, P, P, P, SZ, P]
+    L.moe_quant_row_q8.argtypes = [P, I, I64, I, I, P, I64, P, P]
+    L.moe_linear_q8_workspace_bytes.argtypes = [lin, I]
+    L.moe_linear_q8.argtypes = [lin, P, I64, P, I, P, I, I64, P, SZ, P]
+    for f in EXPORTS:
+        getattr(L, f).restype = SZ if f.endswith("_bytes") else I
+
+
+def _pkg():
+    import mxfp4_routed_expert_e2m1_amd as m
+    return m
+
+
+def _call(fn, *args):
+    m = _pkg()
+    rc = getattr(m._lib or m.lib(), fn)(*args)
+    if rc != 0:
+        raise m.MoeError(fn, rc)
+
+
+def _stream(stream, device):
+    return (stream or torch.cuda.current_stream(device)).cuda_stream
+
+
+def _rows(name, t, dtypes=_TYPES, shape=None):
+    """A 2-d tensor of contiguous rows on the GPU (row-strided views are fine)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype} is not one of {[str(d) for d in dtypes]}")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (shape and t.shape != shape):
+        raise ValueError(f"{name}: need contiguous rows {shape or '[rows][cols]'}, "
+                         f"got {tuple(t.shape)} with strides {t.stride()}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a GPU tensor")
+    return t.data_ptr()
+
+
+def _vec(name, t, n, dtype=torch.float32, least=False):
+    """A contiguous 1-d tensor of n (or, with `least`, at least n) elements, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, need {dtype}")
+    if not t.is_cuda or not t.is_contiguous() or (t.numel() < n if least else t.numel() != n):
+        raise ValueError(f"{name}: need {n} contiguous elements on the GPU")
+    return t.data_ptr()
+
+
+def _ld(t):
+    """Leading dimension (of a single row, which needs none: any aligned one)."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+# --------------------------------------------------------------------- norms
+class Norm:
+    """moe_norm_t with its weights (f32 [d_model] or None): pre_w of the norm
+    before a block, post_w and post_norm of the norm after one."""
+
+    def __init__(self, d_model, pre_w=None, post_w=None, post_norm=True, eps=1e-6,
+                 residual_scale=1.0):
+        self.tensors = (pre_w, post_w)  # keep alive
+        self.d_model = d_model
+        self.c = moe_norm_t(d_model, int(post_norm), eps, residual_scale,
+                            _vec("pre_w", pre_w, d_model), _vec("post_w", post_w, d_model))
+        self.ref = C.byref(self.c)
+
+
+def _norm_out(like, rows, cols, h, h_dtype, quant, q, qs):
+    """Output buffers of a norm and their C arguments."""
+    if quant not in _QUANT:
+        raise ValueError(f"quant: {quant!r} is not one of {list(_QUANT)}")
+    if h is None:
+        h = torch.empty((rows, cols), dtype=h_dtype or like.dtype, device=like.device)
+    if h is False:
+        h, ha = None, (None, 0, 0)
+    else:
+        ha = (_rows("h", h, shape=(rows, cols)), _TYPES[h.dtype], _ld(h))
+    if quant is None:
+        return h, None, None, ha + (0, None, 0, None, 0)
+    if q is None:
+        q = codes_buffer(rows, cols, like.device)
+    n = cols // 32 if quant == "block" else 1
+    if qs is None:
+        qs = torch.empty((rows, n) if quant == "block" else rows, device=like.device)
+    if quant == "block":
+        qa = (_rows("qs", qs, (torch.float32,), (rows, n)), _ld(qs))
+    else:
+        qa = (_vec("qs", qs, rows), 1)
+    ha += (_QUANT[quant], _rows("q", q, (torch.int8,), (rows, cols)), _ld(q)) + qa
+    return h, q, qs, ha
+
+
+def moe_norm_pre(norm, x, h=None, h_dtype=None, quant=None, q=None, qs=None, stream=None):
+    """h = rms(x) * pre_w of x [rows][d_model] (f32 or bf16).  h: the tensor to
+    fill, None (allocated; h_dtype, by default x's type) or False (codes
+    only).  quant: None, "block" (codes as moe_quant_act_q8's, for the routed
+    experts) or "row" (as moe_quant_row_q8's, for moe_linear_q8).  Returns h,
+    or (h, q, qs) with quant."""
+    xp = _rows("x", x)
+    rows, cols = x.shape
+    if cols != norm.d_model:
+        raise ValueError(f"x: {cols} columns, the norm has d_model {norm.d_model}")
+    h, q, qs, out = _norm_out(x, rows, cols, h, h_dtype, quant, q, qs)
+    _call("moe_norm_pre", norm.ref, xp, _TYPES[x.dtype], _ld(x), rows, *out,
+          _stream(stream, x.device))
+    return h if quant is None else (h, q, qs)
+
+
+def _gate_args(gate, rows, cols):
+    if gate is None:
+        return None, 0, 0, 0
+    if gate.dtype not in _TYPES:
+        raise TypeError(f"gate: {gate.dtype} is not one of {[str(d) for d in _TYPES]}")
+    if not gate.is_cuda:
+        raise ValueError("gate: not a GPU tensor")
+    shape, st = gate.shape, gate.stride()
+    if len(shape) < 2:
+        shape, st = (1,) * (2 - len(shape)) + tuple(shape), (0,) * (2 - len(st)) + tuple(st)
+    if len(shape) != 2 or shape[0] not in (1, rows) or shape[1] not in (1, cols):
+        raise ValueError(f"gate: {tuple(gate.shape)} does not broadcast to ({rows}, {cols})")
+    row, col = (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
+    return gate.data_ptr(), _TYPES[gate.dtype], row, col
+
+
+def moe_norm_post(norm, y, residual, gate=None, out=None, next_norm=None, h=None, h_dtype=None,
+                  quant=None, q=None, qs=None, stream=None):
+    """out = residual_scale * residual + gate * b, b = rms(y) * post_w (or y
+    without post_norm).  gate: None or f32/bf16 that broadcasts to
+    [rows][d_model] (a number, per channel, per token or per element).  out is
+    of residual's type and may be residual itself.  With next_norm, also the
+    next block's h = rms(out) * pre_w in the same pass; h, h_dtype (default:
+    residual's type), quant, q, qs as for moe_norm_pre.  Returns out, (out, h)
+    with next_norm, (out, h, q, qs) with quant too."""
+    yp, rp = _rows("y", y), _rows("residual", residual, shape=y.shape)
+    rows, cols = y.shape
+    if cols != norm.d_model:
+        raise ValueError(f"y: {cols} columns, the norm has d_model {norm.d_model}")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=residual.dtype, device=y.device)
+    op = _rows("out", out, (residual.dtype,), y.shape)
+    if next_norm is None:
+        if quant is not None or (h is not None and h is not False):
+            raise ValueError("h and codes belong to next_norm, which is None")
+        nx, nargs = None, (None, 0, 0, 0, None, 0, None, 0)
+    else:
+        h, q, qs, nargs = _norm_out(residual, rows, cols, h, h_dtype, quant, q, qs)
+        nx = next_norm.ref
+    _call("moe_norm_post", norm.ref, yp, _TYPES[y.dtype], _ld(y), rp, _TYPES[residual.dtype],
+          _ld(residual), *_gate_args(gate, rows, cols), rows, op, _ld(out), nx, *nargs,
+          _stream(stream, y.device))
+    if next_norm is None:
+        return out
+    return (out, h) if quant is None else (out, h, q, qs)
+
+
+# ------------------------------------------------------------------- routing
+class RouterRule:
+    """moe_router_rule_t: score "softmax" or "sigmoid", bias f32 [n_experts]
+    or None (added for the choice, not in the weights), group_score "max" or
+    "top2", renorm and scale of the weights."""
+
+    def __init__(self, n_experts, top_k, score="sigmoid", bias=None, n_groups=1, top_groups=None,
+                 group_score="top2", renorm=True, scale=1.0):
+        if score not in _SCORE or group_score not in _GROUP:
+            raise ValueError(f"score {score!r} / group_score {group_score!r}: need one of "
+                             f"{list(_SCORE)} / {list(_GROUP)}")
+        self.tensors = (bias,)  # keep alive
+        self.n_experts, self.top_k = n_experts, top_k
+        self.c = moe_router_rule_t(n_experts, top_k, n_groups,
+                                   n_groups if top_groups is None else top_groups, _SCORE[score],
+                                   _GROUP[group_score], int(renorm), scale,
+                                   _vec("bias", bias, n_experts))
+        self.ref = C.byref(self.c)
+
+
+def route_outputs(rows, n_experts, top_k, device="cuda"):
+    """Buffers (ids, w, counts, offsets, sorted) of a routing call."""
+    i32 = torch.int32
+    return (torch.empty((rows, top_k), dtype=i32, device=device),
+            torch.empty((rows, top_k), dtype=torch.float32, device=device),
+            torch.empty(n_experts, dtype=i32, device=device),
+            torch.empty(n_experts + 1, dtype=i32, device=device),
+            torch.empty(rows * top_k, dtype=i32, device=device))
+
+
+def moe_route_scored_workspace_bytes(rule, rows):
+    m = _pkg()
+    return int(m.lib().moe_route_scored_workspace_bytes(rule.ref, rows))
+
+
+def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
+    """Picks, weights and grouping of logits [rows][n_experts] (f32 or bf16)
+    under a RouterRule.  Returns (ids, w, counts, offsets, sorted), as
+    moe_route_group does; a slot without an expert holds id -1 and weight 0."""
+    lp = _rows("logits", logits)
+    rows, E, k = logits.shape[0], rule.n_experts, rule.top_k
+    if logits.shape[1] != E:
+        raise ValueError(f"logits: {logits.shape[1]} columns, the rule has {E} experts")
+    if out is None:
+        out = route_outputs(rows, E, k, logits.device)
+    ids, w, counts, offsets, srt = out
+    i32, n = torch.int32, rows * k
+    ptrs = (_vec("ids", ids, n, i32), _vec("w", w, n), _vec("counts", counts, E, i32),
+            _vec("offsets", offsets, E + 1, i32), _vec("sorted", srt, n, i32, least=True))
+    if ws is None:
+        ws = torch.empty(moe_route_scored_workspace_bytes(rule, rows), dtype=torch.uint8,
+                         device=logits.device)
+    _call("moe_route_scored", rule.ref, lp, _TYPES[logits.dtype], _ld(logits), rows, *ptrs,
+          ws.data_ptr(), ws.numel(), _stream(stream, logits.device))
+    return out
+
+
+# ------------------------------------------------------------- linear layers
+def codes_buffer(rows, cols, device="cuda"):
+    """int8 [rows][cols] whose rows start 16-byte aligned, as the int8 calls need."""
+    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8,
+                       device=device)[:, :cols]
+
+
+def moe_quant_row_q8(x, q=None, scales=None, stream=None):
+    """int8 codes and one scale per row of x [rows][cols] (f32 or bf16): of
+    activations per token, or of weights [n_out][d_in] per channel.  Returns
+    (q, scales); a q allocated here has 16-byte-aligned rows."""
+    xp = _rows("x", x)
+    rows, cols = x.shape
+    if q is None:
+        q = codes_buffer(rows, cols, x.device)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _call("moe_quant_row_q8", xp, _TYPES[x.dtype], _ld(x), rows, cols,
+          _rows("q", q, (torch.int8,), (rows, cols)), _ld(q), _vec("scales", scales, rows),
+          _stream(stream, x.device))
+    return q, scales
+
+
+class Linear:
+    """moe_linear_t: int8 codes w [n_out][d_in] (16-byte-aligned rows, e.g.
+    from moe_quant_row_q8 of the weights), w_scales f32 [n_out], bias f32
+    [n_out] or None."""
+
+    def __init__(self, w, w_scales, bias=None):
+        self.tensors = (w, w_scales, bias)  # keep alive
+        self.n_out, self.d_in = w.shape
+        self.c = moe_linear_t(self.n_out, self.d_in, _rows("w", w, (torch.int8,)), _ld(w),
+                              _vec("w_scales", w_scales, self.n_out),
+                              _vec("bias", bias, self.n_out))
+        self.ref = C.byref(self.c)
+
+
+def moe_linear_q8_workspace_bytes(linear, rows):
+    m = _pkg()
+    return int(m.lib().moe_linear_q8_workspace_bytes(linear.ref, rows))
+
+
+def moe_linear_q8(linear, q, qs, y=None, dtype=torch.bfloat16, ws=None, stream=None):
+    """y[t][n] = qs[t] w_scales[n] sum_k q[t][k] w[n][k] (+ bias[n]) of int8
+    codes q [rows][d_in] (16-byte-aligned rows) and their row scales.  y: the
+    f32 or bf16 tensor to fill, or None (allocated with `dtype`)."""
+    qp = _rows("q", q, (torch.int8,))
+    rows = q.shape[0]
+    if q.shape[1] != linear.d_in:
+        raise ValueError(f"q: {q.shape[1]} columns, the layer has d_in {linear.d_in}")
+    if y is None:
+        y = torch.empty((rows, linear.n_out), dtype=dtype, device=q.device)
+    if ws is None:
+        ws = torch.empty(moe_linear_q8_workspace_bytes(linear, rows), dtype=torch.uint8,
+                         device=q.device)
+    _call("moe_linear_q8", linear.ref, qp, _ld(q), _vec("qs", qs, rows), rows,
+          _rows("y", y, shape=(rows, linear.n_out)), _TYPES[y.dtype], _ld(y), ws.data_ptr(),
+          ws.numel(), _stream(stream, q.device))
+    return y

@@ -11,14 +11,15 @@ LIB = os.path.join(HERE, "libmoe_mxfp4.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["status.cpp", "pack.hip", "quant.hip", "route.hip", "ffn.hip", "stream.hip",
-           "prefill.hip", "down_rows.hip", "router.hip"]
+           "prefill.hip", "down_rows.hip", "router.hip", "block/norm.hip",
+           "block/route_scored.hip", "block/linear_q8.hip"]
 # Packed-fp32 VALU ops are disabled: only scalar fp32 FMAs are emitted.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 
 def _compile(src: str) -> str:
-    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0].replace("/", "_") + ".o")
     cmd = [HIPCC, *FLAGS, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -1,0 +1,438 @@
+// route_scored.hip -- routing by a scoring rule: softmax or sigmoid scores, a
+// balance bias for the choice alone, expert groups, top-k, weights, and the
+// stable grouping by expert.
+//
+// One wave per row.  Expert e sits in lane e % 64, slot e / 64, as an
+// order-preserving integer key (0: out of reach or already picked), so the
+// choice is a wave maximum per round and the lowest lane of the lowest slot
+// holding it, which is the lowest expert among equals.
+//
+// Grouping.  An expert takes a row at most once, so the rows that chose it are
+// a bit set: an assignment's place among its expert's is the number of
+// earlier rows in the set.  The sets are built with LDS ORs, whose order does
+// not matter, and the result is the unique stable one.  Decode-sized calls do
+// all of it in one workgroup.  Larger ones take two launches: the first
+// counts each expert in every run of rows, the second turns the counts of the
+// earlier runs into first positions and places its own rows, 64 at a time.
+#include "block.h"
+
+#include <math.h>
+
+namespace moe {
+
+constexpr int kRuleMaxExperts = 512;
+constexpr int kRuleMaxGroups = 64;
+constexpr int kRouteThreads = 1024;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kRunRows = kRouteWaves;  // rows a workgroup chooses for at once
+
+struct RuleArgs {
+  const void* logits;
+  int l_type;
+  int64_t ld_l;
+  int rows, n_experts, top_k, n_groups, top_groups, group_size, score, group_score, renorm;
+  uint32_t group_inv;  // ceil(2^20 / group_size): e / group_size = e * group_inv >> 20
+  int lanes_log2;      // lanes that share a group's reduction
+  float scale;
+  const float* bias;
+  int32_t* ids;
+  float* w;
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* sorted;
+};
+
+// The picks of one row: lane s < top_k gets pick s (-1: none left) and its
+// weight.  `lds` holds 64 * PER_LANE words of this wave.
+template <int PER_LANE>
+__device__ inline void choose_row(const RuleArgs& p, int row, uint32_t* lds, int* my_id,
+                                  float* my_w) {
+  const int lane = lane_id(), E = p.n_experts;
+  float l[PER_LANE], s[PER_LANE], b[PER_LANE];
+  if (p.l_type == MOE_TYPE_F32) {
+    const float* r = (const float*)p.logits + (int64_t)row * p.ld_l;
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j) l[j] = r[min(lane + 64 * j, E - 1)];
+  } else {
+    const __bf16* r = (const __bf16*)p.logits + (int64_t)row * p.ld_l;
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j) l[j] = (float)r[min(lane + 64 * j, E - 1)];
+  }
+#pragma unroll
+  for (int j = 0; j < PER_LANE; ++j)
+    b[j] = p.bias ? p.bias[min(lane + 64 * j, E - 1)] : 0.f;
+  bool in[PER_LANE];
+#pragma unroll
+  for (int j = 0; j < PER_LANE; ++j)
+    in[j] = lane + 64 * j < E && l[j] > -__builtin_inff();  // not NaN either
+  if (p.score == MOE_SCORE_SOFTMAX) {
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j)
+      if (in[j]) m = fmaxf(m, l[j]);
+    m = wave_max(m);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j) {
+      // (an infinite maximum: its holders share, the others get 0)
+      s[j] = !in[j] ? 0.f : l[j] == m ? 1.f : exp_rows(l[j] - m);
+      sum += s[j];
+    }
+    sum = wave_sum(sum);
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j) s[j] = in[j] ? s[j] / sum : 0.f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j) s[j] = in[j] ? 1.0f / (1.0f + exp_rows(-l[j])) : 0.f;
+  }
+  uint32_t k[PER_LANE];
+#pragma unroll
+  for (int j = 0; j < PER_LANE; ++j) k[j] = in[j] ? logit_key(s[j] + b[j]) : 0u;
+
+  if (p.n_groups > 1 && p.top_groups < p.n_groups) {
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j) lds[lane + 64 * j] = k[j];
+    __builtin_amdgcn_wave_barrier();
+    // group g's lanes are g << lanes_log2 on; each reads every 2^lanes_log2-th
+    // member, then the lanes' two largest are merged
+    const int P = 1 << p.lanes_log2, g = lane >> p.lanes_log2;
+    uint32_t k1 = 0, k2 = 0;
+    if (g < p.n_groups)
+      for (int i = lane & (P - 1); i < p.group_size; i += P) {
+        const uint32_t v = lds[g * p.group_size + i];
+        k2 = max(k2, min(k1, v));
+        k1 = max(k1, v);
+      }
+    for (int m = 1; m < P; m <<= 1) {
+      const uint32_t o1 = __shfl_xor(k1, m, 64), o2 = __shfl_xor(k2, m, 64);
+      k2 = max(min(k1, o1), max(k2, o2));
+      k1 = max(k1, o1);
+    }
+    uint32_t gk = k1;
+    if (p.group_score == MOE_GROUP_TOP2 && k2 != 0)
+      gk = logit_key(logit_of_key(k1) + logit_of_key(k2));
+    // a group stays if fewer than top_groups groups come before it
+    int before = 0;
+    for (int h = 0; h < p.n_groups; ++h) {
+      const uint32_t v = (uint32_t)__builtin_amdgcn_readlane((int)gk, h << p.lanes_log2);
+      before += (v > gk || (v == gk && h < g)) ? 1 : 0;
+    }
+    const uint64_t stays = __ballot(g < p.n_groups && gk != 0 && before < p.top_groups);
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j) {
+      const uint32_t mine = ((uint32_t)(lane + 64 * j) * p.group_inv) >> 20;
+      if (mine >= (uint32_t)p.n_groups || !((stays >> (mine << p.lanes_log2)) & 1)) k[j] = 0u;
+    }
+  }
+
+  int id = -1;
+  float w = 0.f;
+  for (int r = 0; r < p.top_k; ++r) {
+    uint32_t lm = k[0];
+#pragma unroll
+    for (int j = 1; j < PER_LANE; ++j) lm = max(lm, k[j]);
+    const uint32_t bk = wave_max_u32(lm);
+    if (bk == 0u) break;  // none left: the remaining slots keep -1
+    int be = 0;
+    float bs = 0.f;
+#pragma unroll
+    for (int j = PER_LANE - 1; j >= 0; --j) {
+      const uint64_t m = __ballot(k[j] == bk);
+      if (m != 0ull) {
+        be = 64 * j + (__ffsll((unsigned long long)m) - 1);
+        bs = s[j];
+      }
+    }
+    bs = __builtin_bit_cast(float,
+                            __builtin_amdgcn_readlane(__builtin_bit_cast(int, bs), be & 63));
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j)
+      if (lane + 64 * j == be) k[j] = 0u;
+    if (lane == r) {
+      id = be;
+      w = bs;
+    }
+  }
+  if (p.renorm) {
+    float sum = 0.f;
+    for (int r = 0; r < p.top_k; ++r)
+      sum += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), r));
+    if (sum > 0.f) w = w / sum;
+  }
+  *my_id = id;
+  *my_w = w * p.scale;
+}
+
+// Exclusive scan over the experts of `c` (thread e < n_experts holds expert
+// e's count) in a workgroup of kRouteThreads; returns this thread's, and the
+// total.  `slots` is LDS of one int per wave.
+__device__ inline int expert_scan(int c, int* slots, int* total) {
+  const int incl = wave_incl_scan(c), wave = threadIdx.x >> 6;
+  if (lane_id() == 63) slots[wave] = incl;
+  __syncthreads();
+  int base = 0, all = 0;
+  for (int i = 0; i < kRouteWaves; ++i) {
+    const int t = slots[i];
+    base += i < wave ? t : 0;
+    all += t;
+  }
+  *total = all;
+  return base + incl - c;
+}
+
+// Up to kRunRows rows (decode): choice and grouping in one workgroup.
+template <int PER_LANE>
+__global__ __launch_bounds__(kRouteThreads) void route_small_kernel(RuleArgs p) {
+  __shared__ uint32_t keys[kRouteWaves][64 * PER_LANE];
+  __shared__ int ids[kRunRows * MOE_MAX_TOP_K];
+  __shared__ uint32_t rows_of[kRuleMaxExperts];
+  __shared__ int first[kRuleMaxExperts];
+  __shared__ int slots[kRouteWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = p.rows * p.top_k;
+  if (tid < p.n_experts) rows_of[tid] = 0;
+  if (wave < p.rows) {
+    int id;
+    float w;
+    choose_row<PER_LANE>(p, wave, keys[wave], &id, &w);
+    if (lane < p.top_k) {
+      const int a = wave * p.top_k + lane;
+      p.ids[a] = id;
+      p.w[a] = w;
+      ids[a] = id;
+    }
+  }
+  __syncthreads();
+  const int e = tid < n ? ids[tid] : -1, row = tid / p.top_k;
+  if (e >= 0) atomicOr(&rows_of[e], 1u << row);
+  __syncthreads();
+  const int c = tid < p.n_experts ? __popc(rows_of[tid]) : 0;
+  int total;
+  const int at = expert_scan(c, slots, &total);
+  if (tid < p.n_experts) {
+    p.counts[tid] = c;
+    p.offsets[tid] = at;
+    first[tid] = at;
+  }
+  if (tid == 0) p.offsets[p.n_experts] = total;
+  __syncthreads();
+  if (e >= 0) p.sorted[first[e] + __popc(rows_of[e] & ((1u << row) - 1))] = tid;
+  if (tid >= total && tid < n) p.sorted[tid] = -1;
+}
+
+// More rows, launch 1: run b (rows b*run_rows on) writes its rows' picks and
+// how many of them chose each expert, hist[b][e].
+template <int PER_LANE>
+__global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RuleArgs p, int run_rows,
+                                                                     uint16_t* hist,
+                                                                     int hist_ld) {
+  __shared__ uint32_t keys[kRouteWaves][64 * PER_LANE];
+  __shared__ int count[kRuleMaxExperts];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < hist_ld; e += kRouteThreads) count[e] = 0;
+  __syncthreads();
+  const int r1 = min(p.rows, ((int)blockIdx.x + 1) * run_rows);
+  for (int row = blockIdx.x * run_rows + wave; row < r1; row += kRouteWaves) {
+    int id;
+    float w;
+    choose_row<PER_LANE>(p, row, keys[wave], &id, &w);
+    if (lane < p.top_k) {
+      p.ids[(int64_t)row * p.top_k + lane] = id;
+      p.w[(int64_t)row * p.top_k + lane] = w;
+      if (id >= 0) atomicAdd(&count[id], 1);
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < hist_ld; e += kRouteThreads)
+    hist[(int64_t)blockIdx.x * hist_ld + e] = (uint16_t)count[e];
+}
+
+// Launch 2: workgroup g places the rows of runs [g * group_runs, ..).
+__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(
+    RuleArgs p, int run_rows, int n_runs, int group_runs, const uint16_t* __restrict__ hist,
+    int hist_ld) {
+  __shared__ int total_of[kRuleMaxExperts], next[kRuleMaxExperts];
+  __shared__ unsigned long long rows_of[kRuleMaxExperts];
+  __shared__ int slots[kRouteWaves];
+  const int tid = threadIdx.x;
+  const int run0 = blockIdx.x * group_runs;
+  for (int e = tid; e < kRuleMaxExperts; e += kRouteThreads) total_of[e] = next[e] = 0;
+  __syncthreads();
+  // counts over all runs and over the runs before this workgroup's, two
+  // experts per thread
+  const int pairs = hist_ld / 2, strips = kRouteThreads / pairs;
+  const int col = tid % pairs, strip = tid / pairs;
+  if (strip < strips) {
+    int t0 = 0, t1 = 0, b0 = 0, b1 = 0;
+    for (int r = strip; r < n_runs; r += strips) {
+      const uint32_t v = ((const uint32_t*)hist)[(int64_t)r * pairs + col];
+      const int lo = v & 0xFFFF, hi = v >> 16;
+      t0 += lo;
+      t1 += hi;
+      b0 += r < run0 ? lo : 0;
+      b1 += r < run0 ? hi : 0;
+    }
+    atomicAdd(&total_of[2 * col], t0);
+    atomicAdd(&total_of[2 * col + 1], t1);
+    atomicAdd(&next[2 * col], b0);
+    atomicAdd(&next[2 * col + 1], b1);
+  }
+  __syncthreads();
+  const int c = tid < p.n_experts ? total_of[tid] : 0;
+  int total;
+  const int at = expert_scan(c, slots, &total);
+  if (tid < p.n_experts) {
+    next[tid] += at;
+    rows_of[tid] = 0;
+    if (blockIdx.x == 0) {
+      p.counts[tid] = c;
+      p.offsets[tid] = at;
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) p.offsets[p.n_experts] = total;
+  __syncthreads();
+  const int r0 = run0 * run_rows, r1 = min(p.rows, (run0 + group_runs) * run_rows);
+  for (int rb = r0; rb < r1; rb += 64) {
+    // one thread per assignment of 64 rows: at most 64 * MOE_MAX_TOP_K
+    const int row = rb + tid / p.top_k;
+    const bool mine = tid < 64 * p.top_k && row < r1;
+    const int64_t a = (int64_t)rb * p.top_k + tid;
+    const int e = mine ? p.ids[a] : -1;
+    if (e >= 0) atomicOr(&rows_of[e], 1ull << (row - rb));
+    __syncthreads();
+    if (e >= 0)
+      p.sorted[next[e] + __popcll(rows_of[e] & ((1ull << (row - rb)) - 1))] = (int)a;
+    if (mine && a >= total) p.sorted[a] = -1;
+    __syncthreads();
+    if (tid < p.n_experts) {
+      next[tid] += __popcll(rows_of[tid]);
+      rows_of[tid] = 0;
+    }
+    __syncthreads();
+  }
+}
+
+__global__ void route_none_kernel(int n_experts, int32_t* counts, int32_t* offsets) {
+  for (int e = threadIdx.x; e <= n_experts; e += blockDim.x) {
+    if (e < n_experts) counts[e] = 0;
+    offsets[e] = 0;
+  }
+}
+
+// ------------------------------------------------------------- host side
+static int rule_check(const moe_router_rule_t* R) {
+  if (!R) return MOE_ERR_INVALID_ARG;
+  if (R->n_experts < 1 || R->n_experts > kRuleMaxExperts) return MOE_ERR_SHAPE;
+  if (R->n_groups < 1 || R->n_groups > kRuleMaxGroups || R->n_experts % R->n_groups != 0 ||
+      R->top_groups < 1 || R->top_groups > R->n_groups)
+    return MOE_ERR_SHAPE;
+  if (R->top_k < 1 || R->top_k > MOE_MAX_TOP_K ||
+      R->top_k > R->top_groups * (R->n_experts / R->n_groups))
+    return MOE_ERR_SHAPE;
+  if ((R->score != MOE_SCORE_SOFTMAX && R->score != MOE_SCORE_SIGMOID) ||
+      (R->group_score != MOE_GROUP_MAX && R->group_score != MOE_GROUP_TOP2) ||
+      (R->renorm != 0 && R->renorm != 1) || !isfinite(R->scale))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(R->bias, 4)) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+// Runs of launch 1: kRunRows rows each up to 8192 rows, longer beyond, so
+// that there are never more than 512 (a run's count of an expert, at most
+// 2^24 / 512 rows, fits 16 bits).  Launch 2 takes four runs per workgroup.
+struct RouteShape {
+  int run_rows, n_runs, hist_ld;
+};
+static RouteShape route_shape(int n_experts, int rows) {
+  const int m = (rows + 512 * kRunRows - 1) / (512 * kRunRows);
+  RouteShape s;
+  s.run_rows = kRunRows * (m < 1 ? 1 : m);
+  s.n_runs = (rows + s.run_rows - 1) / s.run_rows;
+  s.hist_ld = (n_experts + 1) / 2 * 2;
+  return s;
+}
+constexpr int kGroupRuns = 4;
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_route_scored_workspace_bytes(const moe_router_rule_t* R, int rows) {
+  if (rule_check(R) != MOE_OK || rows <= kRunRows) return 0;
+  const RouteShape s = route_shape(R->n_experts, rows);
+  return (size_t)s.n_runs * s.hist_ld * sizeof(uint16_t);
+}
+
+extern "C" int moe_route_scored(const moe_router_rule_t* R, const void* logits, int l_type,
+                                int64_t ld_l, int rows, int32_t* ids, float* w, int32_t* counts,
+                                int32_t* offsets, int32_t* sorted, void* ws, size_t ws_bytes,
+                                void* stream) {
+  const int rc = rule_check(R);
+  if (rc != MOE_OK) return rc;
+  if (rows < 0 || !type_ok(l_type) || !counts || !offsets) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!logits || !ids || !w || !sorted)) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)rows * R->top_k > (1 << 24)) return MOE_ERR_SHAPE;
+  if (rows > 0 && ld_l < R->n_experts) return MOE_ERR_STRIDE;
+  if (!aligned(counts, 4) || !aligned(offsets, 4) ||
+      (rows > 0 && (!aligned(logits, type_size(l_type)) || !aligned(ids, 4) || !aligned(w, 4) ||
+                    !aligned(sorted, 4))))
+    return MOE_ERR_ALIGNMENT;
+  const size_t need = moe_route_scored_workspace_bytes(R, rows);
+  if (need > 0) {
+    if (!ws) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
+  }
+  if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
+  hipStream_t s = (hipStream_t)stream;
+  if (rows == 0) {
+    hipLaunchKernelGGL(route_none_kernel, dim3(1), dim3(256), 0, s, R->n_experts, counts,
+                       offsets);
+    return launch_status();
+  }
+  RuleArgs p{};
+  p.logits = logits;
+  p.l_type = l_type;
+  p.ld_l = ld_l;
+  p.rows = rows;
+  p.n_experts = R->n_experts;
+  p.top_k = R->top_k;
+  p.n_groups = R->n_groups;
+  p.top_groups = R->top_groups;
+  p.group_size = R->n_experts / R->n_groups;
+  p.score = R->score;
+  p.group_score = R->group_score;
+  p.renorm = R->renorm;
+  p.group_inv = (uint32_t)(((1 << 20) + p.group_size - 1) / p.group_size);
+  p.lanes_log2 = 0;
+  while ((R->n_groups << (p.lanes_log2 + 1)) <= 64) ++p.lanes_log2;
+  p.scale = R->scale;
+  p.bias = R->bias;
+  p.ids = ids;
+  p.w = w;
+  p.counts = counts;
+  p.offsets = offsets;
+  p.sorted = sorted;
+  const int per_lane = (R->n_experts + 63) / 64;
+  if (rows <= kRunRows) {
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(1), dim3(kRouteThreads), 0, s, p);
+    };
+    if (per_lane <= 2) go(route_small_kernel<2>);
+    else if (per_lane <= 4) go(route_small_kernel<4>);
+    else go(route_small_kernel<8>);
+    return launch_status();
+  }
+  const RouteShape sh = route_shape(R->n_experts, rows);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(sh.n_runs), dim3(kRouteThreads), 0, s, p, sh.run_rows,
+                       (uint16_t*)ws, sh.hist_ld);
+  };
+  if (per_lane <= 2) go(route_choose_kernel<2>);
+  else if (per_lane <= 4) go(route_choose_kernel<4>);
+  else go(route_choose_kernel<8>);
+  hipLaunchKernelGGL(route_place_kernel, dim3((sh.n_runs + kGroupRuns - 1) / kGroupRuns),
+                     dim3(kRouteThreads), 0, s, p, sh.run_rows, sh.n_runs, kGroupRuns,
+                     (const uint16_t*)ws, sh.hist_ld);
+  return launch_status();
+}
