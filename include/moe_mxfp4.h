@@ -515,11 +515,13 @@ int moe_quant_row_q8(const void* x, int x_type, int64_t ld_x, int rows, int cols
  * The sum is exact in int32 (so the result does not depend on tiles, splits
  * or the rows that share a call), then one conversion and two products in
  * fp32: fl(fl(sum * qs) * w_scales), then + bias, then one rounding to y's
- * type. */
+ * type.  Rows of w and q are read up to the next multiple of 16 codes (so the
+ * last row has to be readable that far); what lies past d_in changes
+ * nothing. */
 typedef struct moe_linear {
   int n_out, d_in;       /* n_out >= 1, 1 <= d_in <= 65536 */
   const int8_t* w;       /* [n_out][ld_w] (device), row-major as stored; 16-byte aligned */
-  int64_t ld_w;          /* >= d_in, % 16 == 0; the bytes past d_in are not used */
+  int64_t ld_w;          /* >= d_in, % 16 == 0, <= 2^22 */
   const float* w_scales; /* f32 [n_out] (device) */
   const float* bias;     /* f32 [n_out] (device) or NULL */
 } moe_linear_t;
@@ -527,10 +529,10 @@ typedef struct moe_linear {
 /* Bytes of workspace moe_linear_q8 needs for `rows` rows (can be 0). */
 size_t moe_linear_q8_workspace_bytes(const moe_linear_t* L, int rows);
 
-/*   q  int8 [rows][ld_q] (device, 16-byte aligned, ld_q % 16 == 0), any codes
- *      -128..127; bytes past d_in are not used
+/*   q  int8 [rows][ld_q] (device, 16-byte aligned, ld_q % 16 == 0, <= 2^22),
+ *      any codes -128..127
  *   qs f32 [rows] (device)
- *   y  f32/bf16 [rows][ld_y] (device, out), ld_y >= n_out
+ *   y  f32/bf16 [rows][ld_y] (device, out), n_out <= ld_y <= 2^22
  *   ws workspace (device, 16-byte aligned; NULL where 0 bytes are needed)
  * rows >= 0 (0: a no-op), from one decoded token to prefill chunks. */
 int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_q, const float* qs,

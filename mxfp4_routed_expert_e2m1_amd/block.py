@@ -286,6 +286,18 @@ def moe_quant_row_q8(x, q=None, scales=None, stream=None):
     return q, scales
 
 
+def _codes(name, t):
+    """int8 rows that are readable up to the next multiple of 16 codes."""
+    ptr = _rows(name, t, (torch.int8,))
+    rows, cols = t.shape
+    if cols % 16 and rows:
+        end = t.storage_offset() + (rows - 1) * t.stride(0) + (cols + 15) // 16 * 16
+        if end > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the last row has to be readable up to a multiple of 16 "
+                             "codes (codes_buffer allocates such rows)")
+    return ptr
+
+
 class Linear:
     """moe_linear_t: int8 codes w [n_out][d_in] (16-byte-aligned rows, e.g.
     from moe_quant_row_q8 of the weights), w_scales f32 [n_out], bias f32
@@ -294,7 +306,7 @@ class Linear:
     def __init__(self, w, w_scales, bias=None):
         self.tensors = (w, w_scales, bias)  # keep alive
         self.n_out, self.d_in = w.shape
-        self.c = moe_linear_t(self.n_out, self.d_in, _rows("w", w, (torch.int8,)), _ld(w),
+        self.c = moe_linear_t(self.n_out, self.d_in, _codes("w", w), _ld(w),
                               _vec("w_scales", w_scales, self.n_out),
                               _vec("bias", bias, self.n_out))
         self.ref = C.byref(self.c)
@@ -309,7 +321,7 @@ def moe_linear_q8(linear, q, qs, y=None, dtype=torch.bfloat16, ws=None, stream=N
     """y[t][n] = qs[t] w_scales[n] sum_k q[t][k] w[n][k] (+ bias[n]) of int8
     codes q [rows][d_in] (16-byte-aligned rows) and their row scales.  y: the
     f32 or bf16 tensor to fill, or None (allocated with `dtype`)."""
-    qp = _rows("q", q, (torch.int8,))
+    qp = _codes("q", q)
     rows = q.shape[0]
     if q.shape[1] != linear.d_in:
         raise ValueError(f"q: {q.shape[1]} columns, the layer has d_in {linear.d_in}")

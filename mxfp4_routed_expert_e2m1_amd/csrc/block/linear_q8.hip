@@ -5,7 +5,13 @@
 // supplies channel row l % 32 of A and token row l % 32 of B, each with the
 // 16 codes of K slot l / 32, and receives token column l % 32 of D, element i
 // at channel row 8 (i / 4) + 4 (l / 32) + i % 4.  |sum| <= 2^14 d_in < 2^31.
+// The sums are exact, so tiles and splits of K change no bit.
+//
+// Two kernels: tiles through LDS (any rows), and a weight stream for up to 16
+// rows; plan() below says which, from the sizes alone.
 #include "block.h"
+
+#include <type_traits>
 
 namespace moe {
 
@@ -23,76 +29,534 @@ struct LinearArgs {
   int rows, n_out, d_in;
   void* y;
   int y_bf16;
+  int y_vec;  // rows of y are 16-byte aligned
   int64_t ld_y;
+  // split K: int32 sums of split i at parts + i * rows * parts_ld
+  int32_t* parts;
+  int64_t parts_ld;
 };
 
 __device__ inline i32x16 mfma_i8(i32x4 a, i32x4 b, i32x16 c) {
   return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
 }
 
-// 16 codes at row[k..k+15], those from d_in on 0; k % 16 == 0
-__device__ inline i32x4 load_codes(const int8_t* row, int k, int d_in) {
-  if (k + 16 <= d_in) return *(const i32x4*)(row + k);
-  i32x4 v = {0, 0, 0, 0};
-  for (int i = 0; k + i < d_in; ++i) v[i >> 2] |= (int)(uint8_t)row[k + i] << (8 * (i & 3));
+// the 16 codes of columns k.. with those from d_in on made 0
+__device__ inline i32x4 mask_codes(i32x4 v, int k, int d_in) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = d_in - (k + 4 * i);  // codes of this dword inside the row
+    v[i] &= n >= 4 ? -1 : n <= 0 ? 0 : (int)((1u << (8 * n)) - 1);
+  }
   return v;
 }
-
 // the epilogue's arithmetic, shared by every kernel (each operation rounded by
-// itself: no fused multiply-add with the bias)
-__device__ inline float linear_value(int sum, float qs, float ws, const float* bias, int n) {
+// itself: no fused multiply-add with the bias); without a bias, bias is -0,
+// which changes no value
+__device__ inline float linear_value(int sum, float qs, float ws, float bias) {
 #pragma clang fp contract(off)
-  float v = (float)sum * qs * ws;
-  if (bias) v = v + bias[n];
-  return v;
+  return (float)sum * qs * ws + bias;
 }
 __device__ inline void linear_store(const LinearArgs& a, int t, int n, float v) {
   if (a.y_bf16) ((__bf16*)a.y)[(int64_t)t * a.ld_y + n] = (__bf16)v;
   else ((float*)a.y)[(int64_t)t * a.ld_y + n] = v;
 }
 
-// One wave per 32 x 32 outputs, operands from memory as they are.
-__global__ __launch_bounds__(64) void linear_tile_kernel(LinearArgs a) {
-  const int lane = lane_id(), r = lane & 31, slot = lane >> 5;
-  const int n0 = blockIdx.x * 32, t0 = blockIdx.y * 32;
-  const bool n_in = n0 + r < a.n_out, t_in = t0 + r < a.rows;
-  const int8_t* w = a.w + (int64_t)min(n0 + r, a.n_out - 1) * a.ld_w;
-  const int8_t* q = a.q + (int64_t)min(t0 + r, a.rows - 1) * a.ld_q;
-  i32x16 c = {};
-  for (int k = 0; k < a.d_in; k += 32) {
-    i32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-    if (n_in) x = load_codes(w, k + 16 * slot, a.d_in);
-    if (t_in) y = load_codes(q, k + 16 * slot, a.d_in);
-    c = mfma_i8(x, y, c);
-  }
-  const int t = t0 + r;
-  if (t >= a.rows) return;
-  const float qs = a.qs[t];
+// ------------------------------------------------------ tiles through LDS
+// A workgroup of 4 waves, 2 x 2, computes 64 TT tokens x 64 TN channels, each
+// wave 32 TT x 32 TN of them.  K goes in steps of 64 codes, copied from memory
+// to LDS directly into a ring of four stages, three steps ahead, so that a
+// step has to wait neither for memory nor for the copy unit (which takes 64
+// bytes a cycle: the copies are spread evenly over the products).  A row's
+// four 16-byte pieces sit in LDS at piece ^ (row / 4 & 3), so the 16 rows that
+// a read takes at once lie in different banks; the copy takes the pieces from
+// memory in that order, since it can only write LDS in lane order.
+//
+// Within a step, the matrix core works on the operands of one K slice of 32
+// while the next slice's are read from LDS.
+constexpr int kStepK = 64, kStages = 4;
+
+// Workgroup id -> tile.  Consecutive ids go to the 8 XCDs in turn; each XCD
+// takes a contiguous run of an order that walks 8 token tiles, then the next
+// channel tile, so the tiles that share an L2 at one time share their rows.
+struct TilePlace {
+  int t, n;
+};
+__device__ inline TilePlace place_tile(int id, int total, int tiles_t) {
+  const int xcd = id & 7, per = total >> 3, extra = total & 7;
+  const int i = xcd * per + min(xcd, extra) + (id >> 3);
+  const int tiles_n = total / tiles_t;
+  const int band = i / (8 * tiles_n), left = i - band * 8 * tiles_n;
+  const int width = min(8, tiles_t - band * 8);
+  return {band * 8 + left % width, left / width};
+}
+
+// The 16-byte piece that holds a row's last code is read whole, what lies past
+// the code masked.
+__device__ inline int piece_end(int d_in) { return (d_in + 15) & ~15; }
+
+template <int ROWS>
+struct TileSource {
+  __amdgpu_buffer_rsrc_t rsrc;
+  uint32_t off[ROWS / 64];  // per lane: byte of this lane's piece in the tile's copy j
+
+  // rows r0.. of a matrix of n rows of d_in codes, ld apart; rows past the
+  // last repeat it (their products are not stored)
+  __device__ inline void set(const int8_t* p, int64_t ld, int r0, int n, int d_in) {
+    const int have = min(ROWS, n - r0);
+    rsrc = buf_rsrc(p + uniform((int64_t)r0 * ld), (uint32_t)((have - 1) * ld + piece_end(d_in)));
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int n = n0 + 8 * (i / 4) + 4 * slot + i % 4;
-    if (n < a.n_out) linear_store(a, t, n, linear_value(c[i], qs, a.ws[n], a.bias, n));
+    for (int j = 0; j < ROWS / 64; ++j) {
+      const int row = (j * 4 + wave) * 16 + (lane >> 2);
+      off[j] = (uint32_t)min(row, have - 1) * (uint32_t)ld + 16 * ((lane & 3) ^ ((row >> 2) & 3));
+    }
+  }
+  // copy j of the step at column k (k a whole step inside every row)
+  __device__ inline void copy(int j, int8_t* stage, int k) const { put(j, stage, off[j], k); }
+  // the same where the step may reach past the rows: what is past the last
+  // row's end reads as 0
+  __device__ inline void copy_tail(int j, int8_t* stage, int k) const {
+    put(j, stage, off[j] + k, 0);
+  }
+
+ private:
+  __device__ inline void put(int j, int8_t* stage, uint32_t lane_off, int off0) const {
+#ifdef __HIP_DEVICE_COMPILE__  // (the host pass does not know the 16-byte form)
+    const int wave = uniform((int)threadIdx.x >> 6);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(stage + (j * 4 + wave) * 1024), 16,
+                                             lane_off, off0, 0, 0);
+#endif
+  }
+};
+
+// Barrier after which every wave's copies but its newest N are in LDS and
+// every wave's LDS reads are done.
+template <int N>
+__device__ inline void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4 << 14));  // vmcnt N, lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A wave's 32 tokens x 32 TN channels of results, from the matrix core's lanes
+// through LDS to rows: 4 channels at a time in, 16 bytes (or, where the rows
+// of y do not divide so, one element) per lane out.  The stores go through a
+// buffer resource that ends with the last row, and a lane past the last
+// channel stores past that end, so there is no branch.
+struct RowsOut {
+  void* y;
+  int64_t ld;
+  int rows, cols, vec;  // vec: the rows are 16-byte aligned
+};
+template <int TN, typename T>
+__device__ inline void store_rows(const RowsOut& o, i32x16 (&c)[TN], int t0, int n0, float qs,
+                                  const float* ws, const float* bias, T* buf) {
+  constexpr int kCols = 32 * TN, kLd = kCols + 16 / (int)sizeof(T), kPer = 16 / (int)sizeof(T);
+  const int lane = lane_id(), half = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int n = 32 * i + 8 * g + 4 * half;
+      T v[4];
+      if constexpr (std::is_same_v<T, int32_t>) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = c[i][4 * g + e];
+      } else {
+        const f32x4 w = *(const f32x4*)(ws + n), b = *(const f32x4*)(bias + n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (T)linear_value(c[i][4 * g + e], qs, w[e], b[e]);
+      }
+      __builtin_memcpy(__builtin_assume_aligned(buf + (lane & 31) * kLd + n, 4 * sizeof(T)), v,
+                       sizeof(v));
+    }
+  __builtin_amdgcn_wave_barrier();
+  const int rows = min(32, o.rows - t0), cols = min(kCols, o.cols - n0);
+  const uint32_t ld = (uint32_t)o.ld * sizeof(T);
+  const auto y = buf_rsrc((T*)o.y + uniform((int64_t)t0 * o.ld + n0),
+                          (uint32_t)(rows - 1) * ld + (uint32_t)cols * sizeof(T));
+  constexpr uint32_t kOut = 0xFFFFFFF0u;
+  if (o.vec && cols % kPer == 0) {
+    constexpr int kLanes = kCols / kPer, kPasses = kLanes / 2;  // lanes per row
+    const int col = (lane % kLanes) * kPer, r0 = lane / kLanes;
+    u32x4 v[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      v[i] = *(const u32x4*)(buf + (r0 + i * (64 / kLanes)) * kLd + col);
+    const uint32_t at = col < cols ? r0 * ld + col * (uint32_t)sizeof(T) : kOut;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      __builtin_amdgcn_raw_buffer_store_b128(v[i], y, col < cols ? at + i * (64 / kLanes) * ld : kOut,
+                                             0, 0);
+  } else {
+    for (int r = 0; r < rows; ++r)
+#pragma unroll
+      for (int n = lane; n < kCols; n += 64) {
+        const uint32_t at = n < cols ? r * ld + n * (uint32_t)sizeof(T) : kOut;
+        if constexpr (sizeof(T) == 4)
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, buf[r * kLd + n]), y,
+                                                at, 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, buf[r * kLd + n]), y,
+                                                at, 0, 0);
+      }
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int TT, int TN>
+__global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tiles_t, int splits) {
+  constexpr int BT = 64 * TT, BN = 64 * TN, kStage = (BT + BN) * kStepK;
+  // (an array per stage: the compiler then knows that a read waits for the
+  // copies into its own stage alone)
+  __shared__ __align__(1024) int8_t lds0[kStage], lds1[kStage], lds2[kStage], lds3[kStage];
+  int8_t* const ring[kStages] = {lds0, lds1, lds2, lds3};
+  __shared__ float row_scale[BT];
+  __shared__ __align__(16) float channel_scale[BN], channel_bias[BN];
+  static_assert(BT <= 256 && BN <= 256, "a thread per row and per channel");
+  static_assert(kStage >= 32 * (32 * TN + 4) * 4, "a wave's results fit its share");
+  const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
+  const int wt = wave >> 1, wn = wave & 1;
+  const int split = blockIdx.x % splits;
+  const TilePlace at = place_tile(blockIdx.x / splits, gridDim.x / splits, tiles_t);
+  const int t0 = at.t * BT, n0 = at.n * BN;
+  TileSource<BT> xs;
+  TileSource<BN> ws;
+  xs.set(a.q, a.ld_q, t0, a.rows, a.d_in);
+  ws.set(a.w, a.ld_w, n0, a.n_out, a.d_in);
+  constexpr int kCopies = TT + TN, kReads = TT + TN, kProducts = TT * TN;
+  auto copy = [&](int j, int8_t* to, int k) {
+    if (j < TT) xs.copy(j, to, k);
+    else ws.copy(j - TT, to + BT * kStepK, k);
+  };
+  // the epilogue's factors, loaded ahead of the copies
+  const int lt = threadIdx.x % BT, ln = threadIdx.x % BN;
+  const float my_row = a.qs[min(t0 + lt, a.rows - 1)];
+  const float my_channel = a.ws[min(n0 + ln, a.n_out - 1)];
+  const float my_bias = a.bias ? a.bias[min(n0 + ln, a.n_out - 1)] : -0.f;
+  // past the last step it is copied again, unread, so that every step has as
+  // many copies in flight
+  const int steps_all = a.d_in / kStepK, first = (int64_t)steps_all * split / splits;
+  const int steps = (int64_t)steps_all * (split + 1) / splits - first;
+  const int base = first * kStepK, last = base + (steps - 1) * kStepK;
+  if (steps > 0) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) copy(j, ring[i], min(base + i * kStepK, last));
+  }
+  // this lane's byte in a tile of 32 rows, by K slice (2 pieces: lane / 32)
+  uint32_t rd[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    rd[s] = (lane & 31) * kStepK + 16 * ((2 * s + (lane >> 5)) ^ ((lane >> 2) & 3));
+  i32x16 c[TN][TT];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j) c[i][j] = i32x16{};
+  i32x4 fw[2][TN], fx[2][TT];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) fw[1][i] = i32x4{};
+#pragma unroll
+  for (int j = 0; j < TT; ++j) fx[1][j] = i32x4{};
+  auto read = [&](const int8_t* stage, int s, int set) {
+    const int8_t* x = stage + wt * 32 * TT * kStepK + rd[s];
+    const int8_t* w = stage + (BT + wn * 32 * TN) * kStepK + rd[s];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) fw[set][i] = *(const i32x4*)(w + i * 32 * kStepK);
+#pragma unroll
+    for (int j = 0; j < TT; ++j) fx[set][j] = *(const i32x4*)(x + j * 32 * kStepK);
+  };
+  auto multiply = [&](int set) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) c[i][j] = mfma_i8(fw[set][i], fx[set][j], c[i][j]);
+  };
+
+  auto step = [&](int k, const int8_t* stage, int8_t* to) {
+    stage_barrier<(kStages - 2) * kCopies>();
+    const int kn = min(base + (k + kStages - 1) * kStepK, last);
+    // the products of the slice before come first; a slice's reads and half
+    // the step's copies are spread over them
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int c0 = s * kCopies / 2, c1 = (s + 1) * kCopies / 2;
+      read(stage, s, s);
+#pragma unroll
+      for (int j = c0; j < c1; ++j) copy(j, to, kn);
+      multiply(s ^ 1);
+      const int gaps = kReads + (c1 - c0);
+#pragma unroll
+      for (int i = 0; i < gaps; ++i) {
+        if (i < kReads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+        else __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);             // copy
+        if (i < kProducts) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kProducts - gaps; ++i)
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+  };
+  int k = 0;
+  for (; k + kStages <= steps; k += kStages) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+      step(k + i, ring[i], ring[(i + kStages - 1) % kStages]);
+  }
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (k + i >= steps) break;
+    step(k + i, ring[i], ring[(i + kStages - 1) % kStages]);
+  }
+  if (a.d_in % kStepK && split == splits - 1) {
+    // the partial step, into stage 0; masking one operand is enough
+    stage_barrier<0>();
+    const int k0 = steps_all * kStepK;
+#pragma unroll
+    for (int j = 0; j < TT; ++j) xs.copy_tail(j, lds0, k0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) ws.copy_tail(j, lds0 + BT * kStepK, k0);
+    stage_barrier<0>();
+    multiply(1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      read(lds0, s, s);
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        fw[s][i] = mask_codes(fw[s][i], k0 + 32 * s + 16 * (lane >> 5), a.d_in);
+      if (s == 0) multiply(0);
+    }
+  }
+  multiply(1);
+
+  row_scale[lt] = my_row;  // (threads past BT or BN write what others write)
+  channel_scale[ln] = my_channel;
+  channel_bias[ln] = my_bias;
+  // every wave is done with the stages (and the copies that nobody reads are in)
+  stage_barrier<0>();
+  int8_t* mine = wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3;
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int t = t0 + (wt * TT + j) * 32, n = n0 + wn * 32 * TN;
+    if (t >= a.rows || n >= a.n_out) break;
+    i32x16 cj[TN];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) cj[i] = c[i][j];
+    const float qs = row_scale[t - t0 + (lane & 31)];
+    const float *cs = channel_scale + (n - n0), *cb = channel_bias + (n - n0);
+    const RowsOut o{a.y, a.ld_y, a.rows, a.n_out, a.y_vec};
+    if (a.parts) {
+      const RowsOut po{a.parts + split * (a.rows * a.parts_ld), a.parts_ld, a.rows,
+                       (int)a.parts_ld, 1};
+      store_rows<TN>(po, cj, t, n, qs, cs, cb, (int32_t*)mine);
+    } else if (a.y_bf16) {
+      store_rows<TN>(o, cj, t, n, qs, cs, cb, (__bf16*)mine);
+    } else {
+      store_rows<TN>(o, cj, t, n, qs, cs, cb, (float*)mine);
+    }
   }
 }
+
+// The splits' sums joined, 4 channels per thread.
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a, int splits) {
+  const int n = 4 * (blockIdx.x * 256 + threadIdx.x), t = blockIdx.y;
+  if (n >= a.n_out) return;
+  const int32_t* p = a.parts + t * a.parts_ld + n;
+  i32x4 v = *(const i32x4*)p;
+  for (int i = 1; i < splits; ++i) v += *(const i32x4*)(p + i * (a.rows * a.parts_ld));
+  const float qs = a.qs[t];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.n_out)
+      linear_store(a, t, n + i, linear_value(v[i], qs, a.ws[n + i], a.bias ? a.bias[n + i] : -0.f));
+}
+
+// ------------------------------------------------- few tokens: weight stream
+// Up to 16 tokens the weights are the traffic.  A workgroup of 4 waves takes
+// 16 channels and all tokens; its waves split K and work alone, each with a
+// ring of four stages of its own in LDS: 128 codes of every row, copied from
+// memory three stages ahead, so a wave keeps 6 KiB of weights on their way and
+// never waits for another (two workgroups share a CU; stages of 256 codes, one
+// workgroup per CU, took 17.8 us instead of 12.9 for a row of 14336 x 4096).
+// The products are 16x16x64: lane l supplies row l % 16 with the 16 codes of K
+// slot l / 16 and receives token column l % 16, element i at channel row
+// 4 (l / 16) + i.  Piece p of a row sits in LDS at p ^ (row / 2 & 7), so the 16
+// rows of a read lie in different banks.  The waves' sums, exact in int32, meet
+// in LDS at the end.  16 rows of 4096 x 14336 take 11.9 us, 4.9 TB/s.
+constexpr int kStreamWaves = 4, kStreamK = 128;
+
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
+  constexpr int kHalf = 16 * kStreamK, kStage = 2 * kHalf;  // a wave's: channels, tokens
+  constexpr int kCopyRows = 8, kCopies = 16 / kCopyRows;    // rows of a copy, copies of 16 rows
+  __shared__ __align__(1024) int8_t lds0[kStreamWaves * kStage], lds1[kStreamWaves * kStage],
+      lds2[kStreamWaves * kStage], lds3[kStreamWaves * kStage];
+  __shared__ i32x4 sums[kStreamWaves][64];
+  int8_t* const ring[kStages] = {lds0, lds1, lds2, lds3};
+  const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16, r = lane & 15, slot = lane >> 4;
+  const int have_n = min(16, a.n_out - n0);
+  const auto ws = buf_rsrc(a.w + uniform((int64_t)n0 * a.ld_w),
+                           (uint32_t)((have_n - 1) * a.ld_w + piece_end(a.d_in)));
+  const auto qs = buf_rsrc(a.q, (uint32_t)((a.rows - 1) * a.ld_q + piece_end(a.d_in)));
+  // this wave's steps [s0, s1)
+  const int steps = (a.d_in + kStreamK - 1) / kStreamK;
+  const int s0 = wave * steps / kStreamWaves, s1 = (wave + 1) * steps / kStreamWaves;
+  // per lane: byte of its piece in copy j; rows past the last repeat it (their
+  // sums are not stored)
+  uint32_t off_w[kCopies], off_q[kCopies];
+#pragma unroll
+  for (int j = 0; j < kCopies; ++j) {
+    const int row = kCopyRows * j + (lane >> 3), piece = 16 * ((lane & 7) ^ ((row >> 1) & 7));
+    off_w[j] = (uint32_t)min(row, have_n - 1) * (uint32_t)a.ld_w + piece;
+    off_q[j] = (uint32_t)min(row, a.rows - 1) * (uint32_t)a.ld_q + piece;
+  }
+  // a step's copies; what is past the last row's end reads as 0
+  auto copy = [&](int8_t* to, int s) {
+#ifdef __HIP_DEVICE_COMPILE__  // (the host pass does not know the 16-byte form)
+    const uint32_t k = (uint32_t)s * kStreamK;
+    int8_t* mine = to + wave * kStage;
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ws, (lds_ptr)(mine + j * 1024), 16, off_w[j] + k, 0,
+                                               0, 0);
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(qs, (lds_ptr)(mine + kHalf + j * 1024), 16,
+                                               off_q[j] + k, 0, 0, 0);
+#endif
+  };
+  i32x4 c = {0, 0, 0, 0};
+  auto multiply = [&](const int8_t* stage, int s, bool masked) {
+    const int8_t* mine = stage + wave * kStage + r * kStreamK;
+#pragma unroll
+    for (int h = 0; h < kStreamK / 64; ++h) {
+      const int at = 16 * ((4 * h + slot) ^ ((r >> 1) & 7));
+      i32x4 w = *(const i32x4*)(mine + at);
+      const i32x4 x = *(const i32x4*)(mine + kHalf + at);
+      if (masked) w = mask_codes(w, s * kStreamK + 64 * h + 16 * slot, a.d_in);
+      c = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, c, 0, 0, 0);
+    }
+  };
+  // copies step s + 3 into the stage that step s - 1 was read from, once those
+  // reads are done, then waits for step s (past the wave's last step it is
+  // copied again, unread)
+  auto advance = [&](int s, int8_t* to) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0
+    asm volatile("" ::: "memory");
+    copy(to, min(s + kStages - 1, s1 - 1));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((kStages - 1) * 2 * kCopies | 0xF70);  // vmcnt
+    asm volatile("" ::: "memory");
+  };
+  if (s0 < s1) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) copy(ring[i], min(s0 + i, s1 - 1));
+    const int full = min(s1, a.d_in / kStreamK);
+    int s = s0;
+    for (; s + kStages <= full; s += kStages) {
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) {
+        advance(s + i, ring[(i + kStages - 1) % kStages]);
+        multiply(ring[i], s + i, false);
+      }
+    }
+    // the remaining steps, the partial one among them
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {
+      if (s + i >= s1) break;
+      advance(s + i, ring[(i + kStages - 1) % kStages]);
+      multiply(ring[i], s + i, true);
+    }
+  }
+  sums[wave][lane] = c;
+  __syncthreads();
+  if (wave > 0 || r >= a.rows) return;
+  i32x4 v = sums[0][lane];
+#pragma unroll
+  for (int i = 1; i < kStreamWaves; ++i) v += sums[i][lane];
+  const int n = n0 + 4 * slot;
+  const float scale = a.qs[r];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.n_out)
+      linear_store(a, r, n + i,
+                   linear_value(v[i], scale, a.ws[n + i], a.bias ? a.bias[n + i] : -0.f));
+}
+
+// ------------------------------------------------------------- host side
+constexpr int64_t kMaxLd = 1 << 22;  // 256 rows of any operand within 32-bit offsets
 
 static int linear_check(const moe_linear_t* L) {
   if (!L || !L->w || !L->w_scales) return MOE_ERR_INVALID_ARG;
   if (L->n_out < 1 || L->d_in < 1 || L->d_in > 65536) return MOE_ERR_SHAPE;
-  if (L->ld_w < L->d_in) return MOE_ERR_STRIDE;
+  if (L->ld_w < L->d_in || L->ld_w > kMaxLd) return MOE_ERR_STRIDE;
   if (!aligned(L->w, 16) || L->ld_w % 16 != 0 || !aligned(L->w_scales, 4) ||
       !aligned(L->bias, 4))
     return MOE_ERR_ALIGNMENT;
   return MOE_OK;
 }
 
+// The tile sizes, tokens x channels in units of 64, with what a K step of 64
+// and a tile's start and end cost on a full chip (us, measured; the smaller
+// tiles share a CU, so their figures are per tile in turn).
+struct Tile8 {
+  int tt, tn;
+  float step_us, tile_us;
+};
+constexpr Tile8 kTiles[] = {
+    {4, 4, 0.95f, 6.f}, {4, 2, 0.56f, 3.f}, {2, 2, 0.31f, 2.f}, {1, 2, 0.20f, 1.f},
+    {1, 1, 0.13f, 1.f}};
+constexpr int kChipCus = 256;
+
+struct LinearPlan {
+  int tile;    // index into kTiles, or -1: the weight stream
+  int splits;  // of K
+};
+
+// Up to 16 rows the weight stream, unless there are channels enough for small
+// tiles to fill the chip (16 rows of 14336 x 4096: tiles 11.1 us, stream 13.2;
+// one row of 4096 x 4096: 10.0 and 5.8).  Otherwise the tile and the number of
+// K splits with the least estimated time: rounds of tiles over the chip, plus,
+// for splits, the launch that joins them and its traffic (48 rows of
+// 4096 x 14336: 31 us in one, 15.6 in four; 512 rows of 4096 x 4096: 17.3 in
+// one, 26.9 in two).
+static LinearPlan plan(int rows, int n_out, int d_in) {
+  if (rows <= 16 && (n_out + 63) / 64 < 3 * kChipCus / 4) return {-1, 1};
+  LinearPlan best{0, 1};
+  double best_us = 1e30;
+  const double steps = (d_in + kStepK - 1) / kStepK;
+  for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+    const Tile8& t = kTiles[i];
+    const int64_t tiles = (int64_t)((rows + 64 * t.tt - 1) / (64 * t.tt)) *
+                          ((n_out + 64 * t.tn - 1) / (64 * t.tn));
+    for (int s = 1; s <= 8; s *= 2) {
+      if (s > 1 && (steps / s < 8 || tiles * s > kChipCus)) break;
+      const double rounds = (double)((tiles * s + kChipCus - 1) / kChipCus);
+      double us = rounds * (steps / s * t.step_us + t.tile_us);
+      if (s > 1) us += 3. + (double)s * rows * n_out * 8 / 5e6;
+      if (us < best_us) {
+        best_us = us;
+        best = {i, s};
+      }
+    }
+  }
+  return best;
+}
+
+static int64_t parts_ld(int n_out) { return (n_out + 3) / 4 * 4; }
+
 }  // namespace moe
 
 using namespace moe;
 
 extern "C" size_t moe_linear_q8_workspace_bytes(const moe_linear_t* L, int rows) {
-  (void)L;
-  (void)rows;
-  return 0;
+  if (linear_check(L) != MOE_OK || rows < 1) return 0;
+  const LinearPlan p = plan(rows, L->n_out, L->d_in);
+  return p.splits > 1 ? (size_t)p.splits * rows * parts_ld(L->n_out) * sizeof(int32_t) : 0;
 }
 
 extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_q,
@@ -103,9 +567,11 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
   if (rows < 0 || !type_ok(y_type)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   if (!q || !qs || !y) return MOE_ERR_INVALID_ARG;
-  if (ld_q < L->d_in || ld_y < L->n_out) return MOE_ERR_STRIDE;
+  if (ld_q < L->d_in || ld_y < L->n_out || ld_q > kMaxLd || ld_y > kMaxLd) return MOE_ERR_STRIDE;
   if (!aligned(q, 16) || ld_q % 16 != 0 || !aligned(qs, 4) || !aligned(y, type_size(y_type)))
     return MOE_ERR_ALIGNMENT;
+  if ((int64_t)((rows + 63) / 64) * ((L->n_out + 63) / 64) > (1ll << 30)) return MOE_ERR_SHAPE;
+  const LinearPlan p = plan(rows, L->n_out, L->d_in);
   const size_t need = moe_linear_q8_workspace_bytes(L, rows);
   if (need > 0) {
     if (!ws) return MOE_ERR_INVALID_ARG;
@@ -114,9 +580,31 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
   }
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
   hipStream_t s = (hipStream_t)stream;
+  const int bf16 = y_type == MOE_TYPE_BF16;
   const LinearArgs a{L->w, L->ld_w, L->w_scales, L->bias, q, ld_q, qs, rows, L->n_out, L->d_in,
-                     y, y_type == MOE_TYPE_BF16, ld_y};
-  const dim3 grid((unsigned)((L->n_out + 31) / 32), (unsigned)((rows + 31) / 32));
-  hipLaunchKernelGGL(linear_tile_kernel, grid, dim3(64), 0, s, a);
+                     y, bf16, aligned(y, 16) && ld_y % (bf16 ? 8 : 4) == 0, ld_y,
+                     p.splits > 1 ? (int32_t*)ws : nullptr, parts_ld(L->n_out)};
+  if (p.tile < 0) {
+    hipLaunchKernelGGL(linear_stream_kernel, dim3((L->n_out + 15) / 16),
+                       dim3(64 * kStreamWaves), 0, s, a);
+    return launch_status();
+  }
+  const Tile8& t = kTiles[p.tile];
+  const int tiles_t = (rows + 64 * t.tt - 1) / (64 * t.tt);
+  const int tiles_n = (L->n_out + 64 * t.tn - 1) / (64 * t.tn);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_t * tiles_n * p.splits)), dim3(256), 0, s, a,
+                       tiles_t, p.splits);
+  };
+  switch (p.tile) {
+    case 0: go(linear_gemm_kernel<4, 4>); break;
+    case 1: go(linear_gemm_kernel<4, 2>); break;
+    case 2: go(linear_gemm_kernel<2, 2>); break;
+    case 3: go(linear_gemm_kernel<1, 2>); break;
+    default: go(linear_gemm_kernel<1, 1>); break;
+  }
+  if (p.splits > 1)
+    hipLaunchKernelGGL(linear_join_kernel, dim3((L->n_out + 1023) / 1024, rows), dim3(256), 0, s,
+                       a, p.splits);
   return launch_status();
 }

@@ -68,6 +68,24 @@ def test_large(rows, n, k):
     check(rows, n, k, BF16 if rows % 2 else F32)
 
 
+@pytest.mark.parametrize("rows,n,k", [(4096, 14336, 200), (4000, 14300, 321), (2048, 4096, 1000),
+                                      (2000, 4001, 130), (1000, 4096, 600), (1500, 3000, 2050)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_tiles_of_large_calls(rows, n, k, dtype):
+    """The larger tiles, whole and ragged; the sums by a 64-bit product on the GPU (exact: below
+    2^53), the later steps in fp32 one at a time."""
+    rng = np.random.default_rng([rows, n, k])
+    (q, _), (w, _) = codes(rng, rows, k, 16), codes(rng, n, k, 0)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(k)
+    qs, ws = (torch.rand(c, generator=g, device=DEV) + 0.5 for c in (rows, n))
+    b = torch.randn(n, generator=g, device=DEV)
+    y = m.moe_linear_q8(m.Linear(w, ws, b), q, qs, dtype=dtype)
+    want = (q.double() @ w.double().t().contiguous()).round().to(torch.int32).float()
+    want = ((want * qs[:, None]) * ws[None, :] + b[None, :]).to(dtype)
+    assert torch.equal(y, want)
+
+
 def test_largest_sums():
     """d_in 65536 of the most negative codes: the sum is 2^30."""
     k = 65536
