@@ -24,6 +24,7 @@ MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 _TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
+_F32, _INT8 = {torch.float32: MOE_TYPE_F32}, {torch.int8: 0}
 _QUANT = {None: MOE_QUANT_NONE, "block": MOE_QUANT_BLOCK, "row": MOE_QUANT_ROW}
 _SCORE = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 _GROUP = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
@@ -46,6 +47,7 @@ class moe_linear_t(C.Structure):
 
 def declare(L):
     """Argument types of this module's entry points on the loaded library."""
+    global _lib
     norm, rule, lin = C.POINTER(moe_norm_t), C.POINTER(moe_router_rule_t), C.POINTER(moe_linear_t)
     out = [P, I, I64, I, P, I64, P, I64]
     L.moe_norm_pre.argtypes = [norm, P, I, I64, I] + out + [P]
@@ -58,50 +60,61 @@ def declare(L):
     L.moe_linear_q8.argtypes = [lin, P, I64, P, I, P, I, I64, P, SZ, P]
     for f in EXPORTS:
         getattr(L, f).restype = SZ if f.endswith("_bytes") else I
+    _lib = L
 
 
-def _pkg():
+_lib = None  # set by declare()
+
+
+def _load():
     import mxfp4_routed_expert_e2m1_amd as m
-    return m
+    m.lib()
+    return _lib
 
 
-def _call(fn, *args):
-    m = _pkg()
-    rc = getattr(m._lib or m.lib(), fn)(*args)
+def _check(fn, rc):
     if rc != 0:
+        import mxfp4_routed_expert_e2m1_amd as m
         raise m.MoeError(fn, rc)
 
 
-def _stream(stream, device):
-    return (stream or torch.cuda.current_stream(device)).cuda_stream
+def _stream(stream, t):
+    """The stream's handle (by default torch's current one on t's device; its raw handle alone:
+    making the stream object costs 2 us, more than the rest of a call's arguments)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream
 
 
-def _rows(name, t, dtypes=_TYPES, shape=None):
-    """A 2-d tensor of contiguous rows on the GPU (row-strided views are fine)."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: {t.dtype} is not one of {[str(d) for d in dtypes]}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (shape and t.shape != shape):
-        raise ValueError(f"{name}: need contiguous rows {shape or '[rows][cols]'}, "
-                         f"got {tuple(t.shape)} with strides {t.stride()}")
+def _rows(name, t, shape=None, types=_TYPES):
+    """(pointer, type, leading dimension) of a 2-d tensor of contiguous rows on the GPU
+    (row-strided views are fine).  A single row needs no leading dimension: any aligned one."""
+    kind, sh, st = types.get(t.dtype), t.shape, t.stride()
+    if (kind is None or len(st) != 2 or (st[1] != 1 and sh[1] > 1) or not t.is_cuda
+            or (shape is not None and sh != shape)):
+        _refuse_rows(name, t, shape, types)
+    return t.data_ptr(), kind, st[0] if sh[0] > 1 else (sh[1] + 15) // 16 * 16
+
+
+def _refuse_rows(name, t, shape, types):
+    if t.dtype not in types:
+        raise TypeError(f"{name}: {t.dtype} is not one of {[str(d) for d in types]}")
     if not t.is_cuda:
         raise ValueError(f"{name}: not a GPU tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name}: need contiguous rows {list(shape) if shape else '[rows][cols]'}, "
+                     f"got {list(t.shape)} with strides {t.stride()}")
 
 
 def _vec(name, t, n, dtype=torch.float32, least=False):
-    """A contiguous 1-d tensor of n (or, with `least`, at least n) elements, or None."""
+    """Pointer of a contiguous tensor of n (or, with `least`, at least n) elements, or None."""
     if t is None:
         return None
     if t.dtype != dtype:
         raise TypeError(f"{name}: {t.dtype}, need {dtype}")
-    if not t.is_cuda or not t.is_contiguous() or (t.numel() < n if least else t.numel() != n):
+    have = t.numel()
+    if (have != n and not (least and have > n)) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: need {n} contiguous elements on the GPU")
     return t.data_ptr()
-
-
-def _ld(t):
-    """Leading dimension (of a single row, which needs none: any aligned one)."""
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
 
 
 # --------------------------------------------------------------------- norms
@@ -118,29 +131,31 @@ class Norm:
         self.ref = C.byref(self.c)
 
 
-def _norm_out(like, rows, cols, h, h_dtype, quant, q, qs):
+def _norm_out(like, h, h_dtype, quant, q, qs):
     """Output buffers of a norm and their C arguments."""
-    if quant not in _QUANT:
-        raise ValueError(f"quant: {quant!r} is not one of {list(_QUANT)}")
+    shape = like.shape
     if h is None:
-        h = torch.empty((rows, cols), dtype=h_dtype or like.dtype, device=like.device)
+        h = torch.empty(shape, dtype=h_dtype or like.dtype, device=like.device)
     if h is False:
         h, ha = None, (None, 0, 0)
     else:
-        ha = (_rows("h", h, shape=(rows, cols)), _TYPES[h.dtype], _ld(h))
+        ha = _rows("h", h, shape)
     if quant is None:
         return h, None, None, ha + (0, None, 0, None, 0)
+    if quant not in _QUANT:
+        raise ValueError(f"quant: {quant!r} is not one of {list(_QUANT)}")
+    rows, cols = shape
     if q is None:
         q = codes_buffer(rows, cols, like.device)
     n = cols // 32 if quant == "block" else 1
     if qs is None:
         qs = torch.empty((rows, n) if quant == "block" else rows, device=like.device)
+    qp, _, ld_q = _rows("q", q, shape, _INT8)
     if quant == "block":
-        qa = (_rows("qs", qs, (torch.float32,), (rows, n)), _ld(qs))
+        qsp, _, ld_qs = _rows("qs", qs, (rows, n), _F32)
     else:
-        qa = (_vec("qs", qs, rows), 1)
-    ha += (_QUANT[quant], _rows("q", q, (torch.int8,), (rows, cols)), _ld(q)) + qa
-    return h, q, qs, ha
+        qsp, ld_qs = _vec("qs", qs, rows), 1
+    return h, q, qs, ha + (_QUANT[quant], qp, ld_q, qsp, ld_qs)
 
 
 def moe_norm_pre(norm, x, h=None, h_dtype=None, quant=None, q=None, qs=None, stream=None):
@@ -149,30 +164,29 @@ def moe_norm_pre(norm, x, h=None, h_dtype=None, quant=None, q=None, qs=None, str
     only).  quant: None, "block" (codes as moe_quant_act_q8's, for the routed
     experts) or "row" (as moe_quant_row_q8's, for moe_linear_q8).  Returns h,
     or (h, q, qs) with quant."""
-    xp = _rows("x", x)
+    xa = _rows("x", x)
     rows, cols = x.shape
     if cols != norm.d_model:
         raise ValueError(f"x: {cols} columns, the norm has d_model {norm.d_model}")
-    h, q, qs, out = _norm_out(x, rows, cols, h, h_dtype, quant, q, qs)
-    _call("moe_norm_pre", norm.ref, xp, _TYPES[x.dtype], _ld(x), rows, *out,
-          _stream(stream, x.device))
+    h, q, qs, out = _norm_out(x, h, h_dtype, quant, q, qs)
+    _check("moe_norm_pre", (_lib or _load()).moe_norm_pre(norm.ref, *xa, rows, *out,
+                                                          _stream(stream, x)))
     return h if quant is None else (h, q, qs)
 
 
-def _gate_args(gate, rows, cols):
+def _gate_args(gate, shape):
     if gate is None:
         return None, 0, 0, 0
-    if gate.dtype not in _TYPES:
+    kind, sh, st = _TYPES.get(gate.dtype), gate.shape, gate.stride()
+    if kind is None:
         raise TypeError(f"gate: {gate.dtype} is not one of {[str(d) for d in _TYPES]}")
     if not gate.is_cuda:
         raise ValueError("gate: not a GPU tensor")
-    shape, st = gate.shape, gate.stride()
-    if len(shape) < 2:
-        shape, st = (1,) * (2 - len(shape)) + tuple(shape), (0,) * (2 - len(st)) + tuple(st)
-    if len(shape) != 2 or shape[0] not in (1, rows) or shape[1] not in (1, cols):
-        raise ValueError(f"gate: {tuple(gate.shape)} does not broadcast to ({rows}, {cols})")
-    row, col = (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
-    return gate.data_ptr(), _TYPES[gate.dtype], row, col
+    if len(sh) < 2:
+        sh, st = (1,) * (2 - len(sh)) + tuple(sh), (0,) * (2 - len(st)) + tuple(st)
+    if len(sh) != 2 or sh[0] not in (1, shape[0]) or sh[1] not in (1, shape[1]):
+        raise ValueError(f"gate: {tuple(gate.shape)} does not broadcast to {tuple(shape)}")
+    return gate.data_ptr(), kind, st[0] if sh[0] > 1 else 0, st[1] if sh[1] > 1 else 0
 
 
 def moe_norm_post(norm, y, residual, gate=None, out=None, next_norm=None, h=None, h_dtype=None,
@@ -184,23 +198,25 @@ def moe_norm_post(norm, y, residual, gate=None, out=None, next_norm=None, h=None
     next block's h = rms(out) * pre_w in the same pass; h, h_dtype (default:
     residual's type), quant, q, qs as for moe_norm_pre.  Returns out, (out, h)
     with next_norm, (out, h, q, qs) with quant too."""
-    yp, rp = _rows("y", y), _rows("residual", residual, shape=y.shape)
-    rows, cols = y.shape
-    if cols != norm.d_model:
-        raise ValueError(f"y: {cols} columns, the norm has d_model {norm.d_model}")
+    shape = y.shape
+    ya, ra = _rows("y", y), _rows("residual", residual, shape)
+    if shape[1] != norm.d_model:
+        raise ValueError(f"y: {shape[1]} columns, the norm has d_model {norm.d_model}")
     if out is None:
-        out = torch.empty((rows, cols), dtype=residual.dtype, device=y.device)
-    op = _rows("out", out, (residual.dtype,), y.shape)
+        out = torch.empty(shape, dtype=residual.dtype, device=y.device)
+    op, ot, ld_out = _rows("out", out, shape)
+    if ot != ra[1]:
+        raise TypeError(f"out: {out.dtype}, the residual is {residual.dtype}")
     if next_norm is None:
         if quant is not None or (h is not None and h is not False):
             raise ValueError("h and codes belong to next_norm, which is None")
         nx, nargs = None, (None, 0, 0, 0, None, 0, None, 0)
     else:
-        h, q, qs, nargs = _norm_out(residual, rows, cols, h, h_dtype, quant, q, qs)
+        h, q, qs, nargs = _norm_out(residual, h, h_dtype, quant, q, qs)
         nx = next_norm.ref
-    _call("moe_norm_post", norm.ref, yp, _TYPES[y.dtype], _ld(y), rp, _TYPES[residual.dtype],
-          _ld(residual), *_gate_args(gate, rows, cols), rows, op, _ld(out), nx, *nargs,
-          _stream(stream, y.device))
+    _check("moe_norm_post", (_lib or _load()).moe_norm_post(
+        norm.ref, *ya, *ra, *_gate_args(gate, shape), shape[0], op, ld_out, nx, *nargs,
+        _stream(stream, y)))
     if next_norm is None:
         return out
     return (out, h) if quant is None else (out, h, q, qs)
@@ -237,15 +253,14 @@ def route_outputs(rows, n_experts, top_k, device="cuda"):
 
 
 def moe_route_scored_workspace_bytes(rule, rows):
-    m = _pkg()
-    return int(m.lib().moe_route_scored_workspace_bytes(rule.ref, rows))
+    return int((_lib or _load()).moe_route_scored_workspace_bytes(rule.ref, rows))
 
 
 def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
     """Picks, weights and grouping of logits [rows][n_experts] (f32 or bf16)
     under a RouterRule.  Returns (ids, w, counts, offsets, sorted), as
     moe_route_group does; a slot without an expert holds id -1 and weight 0."""
-    lp = _rows("logits", logits)
+    la = _rows("logits", logits)
     rows, E, k = logits.shape[0], rule.n_experts, rule.top_k
     if logits.shape[1] != E:
         raise ValueError(f"logits: {logits.shape[1]} columns, the rule has {E} experts")
@@ -258,8 +273,8 @@ def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
     if ws is None:
         ws = torch.empty(moe_route_scored_workspace_bytes(rule, rows), dtype=torch.uint8,
                          device=logits.device)
-    _call("moe_route_scored", rule.ref, lp, _TYPES[logits.dtype], _ld(logits), rows, *ptrs,
-          ws.data_ptr(), ws.numel(), _stream(stream, logits.device))
+    _check("moe_route_scored", (_lib or _load()).moe_route_scored(
+        rule.ref, *la, rows, *ptrs, ws.data_ptr(), ws.numel(), _stream(stream, logits)))
     return out
 
 
@@ -274,28 +289,28 @@ def moe_quant_row_q8(x, q=None, scales=None, stream=None):
     """int8 codes and one scale per row of x [rows][cols] (f32 or bf16): of
     activations per token, or of weights [n_out][d_in] per channel.  Returns
     (q, scales); a q allocated here has 16-byte-aligned rows."""
-    xp = _rows("x", x)
-    rows, cols = x.shape
+    xa = _rows("x", x)
+    rows, cols = shape = x.shape
     if q is None:
         q = codes_buffer(rows, cols, x.device)
     if scales is None:
         scales = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _call("moe_quant_row_q8", xp, _TYPES[x.dtype], _ld(x), rows, cols,
-          _rows("q", q, (torch.int8,), (rows, cols)), _ld(q), _vec("scales", scales, rows),
-          _stream(stream, x.device))
+    qp, _, ld_q = _rows("q", q, shape, _INT8)
+    _check("moe_quant_row_q8", (_lib or _load()).moe_quant_row_q8(
+        *xa, rows, cols, qp, ld_q, _vec("scales", scales, rows), _stream(stream, x)))
     return q, scales
 
 
 def _codes(name, t):
     """int8 rows that are readable up to the next multiple of 16 codes."""
-    ptr = _rows(name, t, (torch.int8,))
+    ptr, _, ld = _rows(name, t, None, _INT8)
     rows, cols = t.shape
     if cols % 16 and rows:
         end = t.storage_offset() + (rows - 1) * t.stride(0) + (cols + 15) // 16 * 16
         if end > t.untyped_storage().nbytes():
             raise ValueError(f"{name}: the last row has to be readable up to a multiple of 16 "
                              "codes (codes_buffer allocates such rows)")
-    return ptr
+    return ptr, ld
 
 
 class Linear:
@@ -306,31 +321,30 @@ class Linear:
     def __init__(self, w, w_scales, bias=None):
         self.tensors = (w, w_scales, bias)  # keep alive
         self.n_out, self.d_in = w.shape
-        self.c = moe_linear_t(self.n_out, self.d_in, _codes("w", w), _ld(w),
+        self.c = moe_linear_t(self.n_out, self.d_in, *_codes("w", w),
                               _vec("w_scales", w_scales, self.n_out),
                               _vec("bias", bias, self.n_out))
         self.ref = C.byref(self.c)
 
 
 def moe_linear_q8_workspace_bytes(linear, rows):
-    m = _pkg()
-    return int(m.lib().moe_linear_q8_workspace_bytes(linear.ref, rows))
+    return int((_lib or _load()).moe_linear_q8_workspace_bytes(linear.ref, rows))
 
 
 def moe_linear_q8(linear, q, qs, y=None, dtype=torch.bfloat16, ws=None, stream=None):
     """y[t][n] = qs[t] w_scales[n] sum_k q[t][k] w[n][k] (+ bias[n]) of int8
     codes q [rows][d_in] (16-byte-aligned rows) and their row scales.  y: the
     f32 or bf16 tensor to fill, or None (allocated with `dtype`)."""
-    qp = _codes("q", q)
-    rows = q.shape[0]
-    if q.shape[1] != linear.d_in:
-        raise ValueError(f"q: {q.shape[1]} columns, the layer has d_in {linear.d_in}")
+    qp, ld_q = _codes("q", q)
+    rows, cols = q.shape
+    if cols != linear.d_in:
+        raise ValueError(f"q: {cols} columns, the layer has d_in {linear.d_in}")
     if y is None:
         y = torch.empty((rows, linear.n_out), dtype=dtype, device=q.device)
     if ws is None:
         ws = torch.empty(moe_linear_q8_workspace_bytes(linear, rows), dtype=torch.uint8,
                          device=q.device)
-    _call("moe_linear_q8", linear.ref, qp, _ld(q), _vec("qs", qs, rows), rows,
-          _rows("y", y, shape=(rows, linear.n_out)), _TYPES[y.dtype], _ld(y), ws.data_ptr(),
-          ws.numel(), _stream(stream, q.device))
+    _check("moe_linear_q8", (_lib or _load()).moe_linear_q8(
+        linear.ref, qp, ld_q, _vec("qs", qs, rows), rows, *_rows("y", y, (rows, linear.n_out)),
+        ws.data_ptr(), ws.numel(), _stream(stream, q)))
     return y
