@@ -22,20 +22,20 @@ inline size_t type_size(int t) { return t == MOE_TYPE_F32 ? 4 : 2; }
 
 // 8 consecutive elements of a row, in registers as loaded (a bf16 row uses
 // the first 16 bytes), so that several rows' loads are in flight before the
-// first is converted.
+// first is converted.  Rows need their elements' alignment alone: the memory
+// instructions take 16 bytes at any address.
 template <typename T>
 struct Raw8 {
   u32x4 a[sizeof(T) / 2];
 };
 
 template <typename T>
-__device__ inline Raw8<T> load8_vec(const T* p) {
+__device__ inline Raw8<T> load8(const T* p) {
   Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.a[i] = ((const u32x4*)p)[i];
+  __builtin_memcpy(&r, p, sizeof(r));
   return r;
 }
-// the first n of 8 elements (any alignment); the rest 0
+// the first n < 8 of 8 elements; the rest 0
 template <typename T>
 __device__ inline Raw8<T> load8_part(const T* p, int n) {
   Raw8<T> r;
@@ -59,11 +59,21 @@ __device__ inline void to_f32(const Raw8<T>& r, float (&v)[8]) {
   }
 }
 
-// Sum (or max) over the wave, in every lane's register as one value.
+// Sum over the wave in a fixed order, as a wave-uniform value (the DPP steps of
+// wave_max; lanes that a row broadcast does not reach add 0).
+template <int CTRL, int ROWS>
+__device__ inline float dpp_or_0(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
+                                                              ROWS, 0xF, false));
+}
 __device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+  v += dpp_mov<0xB1>(v);         // quad_perm [1,0,3,2]
+  v += dpp_mov<0x4E>(v);         // quad_perm [2,3,0,1]
+  v += dpp_mov<0x141>(v);        // row_half_mirror
+  v += dpp_mov<0x140>(v);        // row_mirror
+  v += dpp_or_0<0x142, 0xA>(v);  // row_bcast:15 into rows 1, 3
+  v += dpp_or_0<0x143, 0xC>(v);  // row_bcast:31 into rows 2, 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 int norm_args_check(const moe_norm_t* N);

@@ -63,17 +63,25 @@ __device__ inline void linear_store(const LinearArgs& a, int t, int n, float v) 
 
 // ------------------------------------------------------ tiles through LDS
 // A workgroup of 4 waves, 2 x 2, computes 64 TT tokens x 64 TN channels, each
-// wave 32 TT x 32 TN of them.  K goes in steps of 64 codes, copied from memory
-// to LDS directly into a ring of four stages, three steps ahead, so that a
-// step has to wait neither for memory nor for the copy unit (which takes 64
-// bytes a cycle: the copies are spread evenly over the products).  A row's
-// four 16-byte pieces sit in LDS at piece ^ (row / 4 & 3), so the 16 rows that
-// a read takes at once lie in different banks; the copy takes the pieces from
-// memory in that order, since it can only write LDS in lane order.
+// wave 32 TT x 32 TN of them.  K goes in steps of STEP codes, copied from
+// memory to LDS directly into a ring of four stages, three steps ahead, so that
+// a step has to wait neither for memory nor for the copy unit (which takes 64
+// bytes a cycle: the copies are spread evenly over the products).  The larger
+// tiles take steps of 64 codes (the largest one's ring fills the LDS), the two
+// smallest 128, for half the barriers (512 rows of 4096 x 4096: 16.5 -> 13.8
+// us).  A row's P = STEP / 16 pieces sit in LDS at
+// piece ^ (row / (16 / P) % P), so the 16 rows that a read takes at once lie in
+// different banks; the copy takes the pieces from memory in that order, since
+// it can only write LDS in lane order.
 //
 // Within a step, the matrix core works on the operands of one K slice of 32
 // while the next slice's are read from LDS.
-constexpr int kStepK = 64, kStages = 4;
+constexpr int kStages = 4;
+
+template <int STEP>
+__device__ inline int swizzle(int row) {
+  return row / (256 / STEP) % (STEP / 16);
+}
 
 // Workgroup id -> tile.  Consecutive ids go to the 8 XCDs in turn; each XCD
 // takes a contiguous run of an order that walks 8 token tiles, then the next
@@ -94,10 +102,12 @@ __device__ inline TilePlace place_tile(int id, int total, int tiles_t) {
 // the code masked.
 __device__ inline int piece_end(int d_in) { return (d_in + 15) & ~15; }
 
-template <int ROWS>
+template <int ROWS, int STEP>
 struct TileSource {
+  static constexpr int kPieces = STEP / 16, kCopyRows = 64 / kPieces;
+  static constexpr int kCopies = ROWS / (4 * kCopyRows);  // per wave
   __amdgpu_buffer_rsrc_t rsrc;
-  uint32_t off[ROWS / 64];  // per lane: byte of this lane's piece in the tile's copy j
+  uint32_t off[kCopies];  // per lane: byte of this lane's piece in the tile's copy j
 
   // rows r0.. of a matrix of n rows of d_in codes, ld apart; rows past the
   // last repeat it (their products are not stored)
@@ -106,9 +116,10 @@ struct TileSource {
     rsrc = buf_rsrc(p + uniform((int64_t)r0 * ld), (uint32_t)((have - 1) * ld + piece_end(d_in)));
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
 #pragma unroll
-    for (int j = 0; j < ROWS / 64; ++j) {
-      const int row = (j * 4 + wave) * 16 + (lane >> 2);
-      off[j] = (uint32_t)min(row, have - 1) * (uint32_t)ld + 16 * ((lane & 3) ^ ((row >> 2) & 3));
+    for (int j = 0; j < kCopies; ++j) {
+      const int row = (j * 4 + wave) * kCopyRows + lane / kPieces;
+      off[j] = (uint32_t)min(row, have - 1) * (uint32_t)ld +
+               16 * (lane % kPieces ^ swizzle<STEP>(row));
     }
   }
   // copy j of the step at column k (k a whole step inside every row)
@@ -205,9 +216,9 @@ __device__ inline void store_rows(const RowsOut& o, i32x16 (&c)[TN], int t0, int
   __builtin_amdgcn_wave_barrier();
 }
 
-template <int TT, int TN>
+template <int TT, int TN, int STEP>
 __global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tiles_t, int splits) {
-  constexpr int BT = 64 * TT, BN = 64 * TN, kStage = (BT + BN) * kStepK;
+  constexpr int BT = 64 * TT, BN = 64 * TN, kStage = (BT + BN) * STEP;
   // (an array per stage: the compiler then knows that a read waits for the
   // copies into its own stage alone)
   __shared__ __align__(1024) int8_t lds0[kStage], lds1[kStage], lds2[kStage], lds3[kStage];
@@ -221,14 +232,15 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tile
   const int split = blockIdx.x % splits;
   const TilePlace at = place_tile(blockIdx.x / splits, gridDim.x / splits, tiles_t);
   const int t0 = at.t * BT, n0 = at.n * BN;
-  TileSource<BT> xs;
-  TileSource<BN> ws;
+  TileSource<BT, STEP> xs;
+  TileSource<BN, STEP> ws;
   xs.set(a.q, a.ld_q, t0, a.rows, a.d_in);
   ws.set(a.w, a.ld_w, n0, a.n_out, a.d_in);
-  constexpr int kCopies = TT + TN, kReads = TT + TN, kProducts = TT * TN;
+  constexpr int kCopiesX = decltype(xs)::kCopies, kCopies = kCopiesX + decltype(ws)::kCopies;
+  constexpr int kSlices = STEP / 32, kReads = TT + TN, kProducts = TT * TN;
   auto copy = [&](int j, int8_t* to, int k) {
-    if (j < TT) xs.copy(j, to, k);
-    else ws.copy(j - TT, to + BT * kStepK, k);
+    if (j < kCopiesX) xs.copy(j, to, k);
+    else ws.copy(j - kCopiesX, to + BT * STEP, k);
   };
   // the epilogue's factors, loaded ahead of the copies
   const int lt = threadIdx.x % BT, ln = threadIdx.x % BN;
@@ -237,20 +249,20 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tile
   const float my_bias = a.bias ? a.bias[min(n0 + ln, a.n_out - 1)] : -0.f;
   // past the last step it is copied again, unread, so that every step has as
   // many copies in flight
-  const int steps_all = a.d_in / kStepK, first = (int64_t)steps_all * split / splits;
+  const int steps_all = a.d_in / STEP, first = (int64_t)steps_all * split / splits;
   const int steps = (int64_t)steps_all * (split + 1) / splits - first;
-  const int base = first * kStepK, last = base + (steps - 1) * kStepK;
+  const int base = first * STEP, last = base + (steps - 1) * STEP;
   if (steps > 0) {
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i)
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) copy(j, ring[i], min(base + i * kStepK, last));
+      for (int j = 0; j < kCopies; ++j) copy(j, ring[i], min(base + i * STEP, last));
   }
   // this lane's byte in a tile of 32 rows, by K slice (2 pieces: lane / 32)
-  uint32_t rd[2];
+  uint32_t rd[kSlices];
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
-    rd[s] = (lane & 31) * kStepK + 16 * ((2 * s + (lane >> 5)) ^ ((lane >> 2) & 3));
+  for (int s = 0; s < kSlices; ++s)
+    rd[s] = (lane & 31) * STEP + 16 * ((2 * s + (lane >> 5)) ^ swizzle<STEP>(lane & 31));
   i32x16 c[TN][TT];
 #pragma unroll
   for (int i = 0; i < TN; ++i)
@@ -262,12 +274,12 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tile
 #pragma unroll
   for (int j = 0; j < TT; ++j) fx[1][j] = i32x4{};
   auto read = [&](const int8_t* stage, int s, int set) {
-    const int8_t* x = stage + wt * 32 * TT * kStepK + rd[s];
-    const int8_t* w = stage + (BT + wn * 32 * TN) * kStepK + rd[s];
+    const int8_t* x = stage + wt * 32 * TT * STEP + rd[s];
+    const int8_t* w = stage + (BT + wn * 32 * TN) * STEP + rd[s];
 #pragma unroll
-    for (int i = 0; i < TN; ++i) fw[set][i] = *(const i32x4*)(w + i * 32 * kStepK);
+    for (int i = 0; i < TN; ++i) fw[set][i] = *(const i32x4*)(w + i * 32 * STEP);
 #pragma unroll
-    for (int j = 0; j < TT; ++j) fx[set][j] = *(const i32x4*)(x + j * 32 * kStepK);
+    for (int j = 0; j < TT; ++j) fx[set][j] = *(const i32x4*)(x + j * 32 * STEP);
   };
   auto multiply = [&](int set) {
 #pragma unroll
@@ -278,16 +290,16 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tile
 
   auto step = [&](int k, const int8_t* stage, int8_t* to) {
     stage_barrier<(kStages - 2) * kCopies>();
-    const int kn = min(base + (k + kStages - 1) * kStepK, last);
-    // the products of the slice before come first; a slice's reads and half
-    // the step's copies are spread over them
+    const int kn = min(base + (k + kStages - 1) * STEP, last);
+    // the products of the slice before come first; a slice's reads and its share
+    // of the step's copies are spread over them
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int c0 = s * kCopies / 2, c1 = (s + 1) * kCopies / 2;
-      read(stage, s, s);
+    for (int s = 0; s < kSlices; ++s) {
+      const int c0 = s * kCopies / kSlices, c1 = (s + 1) * kCopies / kSlices;
+      read(stage, s, s & 1);
 #pragma unroll
       for (int j = c0; j < c1; ++j) copy(j, to, kn);
-      multiply(s ^ 1);
+      multiply((s & 1) ^ 1);
       const int gaps = kReads + (c1 - c0);
 #pragma unroll
       for (int i = 0; i < gaps; ++i) {
@@ -311,23 +323,23 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tile
     if (k + i >= steps) break;
     step(k + i, ring[i], ring[(i + kStages - 1) % kStages]);
   }
-  if (a.d_in % kStepK && split == splits - 1) {
+  if (a.d_in % STEP && split == splits - 1) {
     // the partial step, into stage 0; masking one operand is enough
     stage_barrier<0>();
-    const int k0 = steps_all * kStepK;
+    const int k0 = steps_all * STEP;
 #pragma unroll
-    for (int j = 0; j < TT; ++j) xs.copy_tail(j, lds0, k0);
+    for (int j = 0; j < kCopiesX; ++j) xs.copy_tail(j, lds0, k0);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) ws.copy_tail(j, lds0 + BT * kStepK, k0);
+    for (int j = 0; j < kCopies - kCopiesX; ++j) ws.copy_tail(j, lds0 + BT * STEP, k0);
     stage_barrier<0>();
     multiply(1);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      read(lds0, s, s);
+    for (int s = 0; s < kSlices; ++s) {
+      read(lds0, s, s & 1);
 #pragma unroll
       for (int i = 0; i < TN; ++i)
-        fw[s][i] = mask_codes(fw[s][i], k0 + 32 * s + 16 * (lane >> 5), a.d_in);
-      if (s == 0) multiply(0);
+        fw[s & 1][i] = mask_codes(fw[s & 1][i], k0 + 32 * s + 16 * (lane >> 5), a.d_in);
+      if (s < kSlices - 1) multiply(s & 1);
     }
   }
   multiply(1);
@@ -508,8 +520,8 @@ struct Tile8 {
   float step_us, tile_us;
 };
 constexpr Tile8 kTiles[] = {
-    {4, 4, 0.95f, 6.f}, {4, 2, 0.56f, 3.f}, {2, 2, 0.31f, 2.f}, {1, 2, 0.20f, 1.f},
-    {1, 1, 0.13f, 1.f}};
+    {4, 4, 0.95f, 6.f}, {4, 2, 0.56f, 3.f}, {2, 2, 0.31f, 2.f}, {1, 2, 0.15f, 1.5f},
+    {1, 1, 0.085f, 1.2f}};
 constexpr int kChipCus = 256;
 
 struct LinearPlan {
@@ -519,16 +531,16 @@ struct LinearPlan {
 
 // Up to 16 rows the weight stream, unless there are channels enough for small
 // tiles to fill the chip (16 rows of 14336 x 4096: tiles 11.1 us, stream 13.2;
-// one row of 4096 x 4096: 10.0 and 5.8).  Otherwise the tile and the number of
+// one row of 4096 x 4096: 8.2 and 5.8).  Otherwise the tile and the number of
 // K splits with the least estimated time: rounds of tiles over the chip, plus,
 // for splits, the launch that joins them and its traffic (48 rows of
-// 4096 x 14336: 31 us in one, 15.6 in four; 512 rows of 4096 x 4096: 17.3 in
-// one, 26.9 in two).
+// 4096 x 14336: 21.5 us in one, 14.9 in four; 512 rows of 4096 x 4096: 13.8 in
+// one, 24.6 in two).
 static LinearPlan plan(int rows, int n_out, int d_in) {
   if (rows <= 16 && (n_out + 63) / 64 < 3 * kChipCus / 4) return {-1, 1};
   LinearPlan best{0, 1};
   double best_us = 1e30;
-  const double steps = (d_in + kStepK - 1) / kStepK;
+  const double steps = (d_in + 63) / 64;
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
     const Tile8& t = kTiles[i];
     const int64_t tiles = (int64_t)((rows + 64 * t.tt - 1) / (64 * t.tt)) *
@@ -597,11 +609,11 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
                        tiles_t, p.splits);
   };
   switch (p.tile) {
-    case 0: go(linear_gemm_kernel<4, 4>); break;
-    case 1: go(linear_gemm_kernel<4, 2>); break;
-    case 2: go(linear_gemm_kernel<2, 2>); break;
-    case 3: go(linear_gemm_kernel<1, 2>); break;
-    default: go(linear_gemm_kernel<1, 1>); break;
+    case 0: go(linear_gemm_kernel<4, 4, 64>); break;
+    case 1: go(linear_gemm_kernel<4, 2, 64>); break;
+    case 2: go(linear_gemm_kernel<2, 2, 64>); break;
+    case 3: go(linear_gemm_kernel<1, 2, 128>); break;
+    default: go(linear_gemm_kernel<1, 1, 128>); break;
   }
   if (p.splits > 1)
     hipLaunchKernelGGL(linear_join_kernel, dim3((L->n_out + 1023) / 1024, rows), dim3(256), 0, s,

@@ -49,53 +49,47 @@ struct NormArgs {
   NormOut o;
 };
 
-// Sum over the workgroup; `slots` is LDS of one float per wave, not shared
-// with another reduction of the same row.
-__device__ inline float wg_sum(float v, float* slots) {
-  v = wave_sum(v);
-  const int waves = blockDim.x >> 6;
+// Sum (or maximum of values >= 0) over the workgroup of up to 16 waves, in
+// every lane; `slots` is LDS of one float per wave, not shared with another
+// reduction of the same row.
+template <typename Op>
+__device__ inline float over_waves(float v, float* slots, Op op) {
+  const int waves = blockDim.x >> 6, lane = lane_id();
   if (waves == 1) return v;
-  if (lane_id() == 0) slots[threadIdx.x >> 6] = v;
+  if (lane == 0) slots[threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < waves; ++i) s += slots[i];
-  return s;
+  v = (lane & 15) < waves ? slots[lane & 15] : 0.f;
+  v = op(v, dpp_mov<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = op(v, dpp_mov<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = op(v, dpp_mov<0x141>(v));  // row_half_mirror
+  return op(v, dpp_mov<0x140>(v));  // row_mirror
+}
+__device__ inline float wg_sum(float v, float* slots) {
+  return over_waves(wave_sum(v), slots, [](float a, float b) { return a + b; });
 }
 __device__ inline float wg_max(float v, float* slots) {
-  v = wave_max(v);
-  const int waves = blockDim.x >> 6;
-  if (waves == 1) return v;
-  if (lane_id() == 0) slots[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = slots[0];
-  for (int i = 1; i < waves; ++i) s = fmaxf(s, slots[i]);
-  return s;
+  return over_waves(wave_max(v), slots, [](float a, float b) { return fmaxf(a, b); });
 }
 
-template <bool VEC, typename T>
+// WHOLE: the row is a whole number of units
+template <bool WHOLE, typename T>
 __device__ inline Raw8<T> load_unit(const T* row, int e, int cols) {
-  if constexpr (VEC) {
-    return e < cols ? load8_vec(row + e) : Raw8<T>{};
-  } else {
-    return load8_part(row + e, min(8, cols - e));
-  }
+  if (e + 8 <= cols) return load8(row + e);
+  if (!WHOLE && e < cols) return load8_part(row + e, cols - e);
+  return Raw8<T>{};
 }
 
-template <bool VEC, typename T>
+template <bool WHOLE, typename T>
 __device__ inline void store_unit(T* row, int e, int cols, const float (&v)[8]) {
-  if (e >= cols) return;
-  if constexpr (VEC) {
-    T t[8];
+  T t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = (T)v[i];
-    u32x4 r[sizeof(T) / 2];
-    __builtin_memcpy(r, t, sizeof(t));
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) ((u32x4*)(row + e))[i] = r[i];
-  } else {
+  for (int i = 0; i < 8; ++i) t[i] = (T)v[i];
+  if (e + 8 <= cols) {
+    __builtin_memcpy(row + e, t, sizeof(t));
+  } else if (!WHOLE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (e + i < cols) row[e + i] = (T)v[i];
+      if (e + i < cols) row[e + i] = t[i];
   }
 }
 
@@ -106,32 +100,27 @@ __device__ inline float stored(float v) {
 }
 
 // One row's h = v * r * w from its values in registers, with its codes.
-template <int U, bool VEC>
-__device__ inline void finish_row(float (&v)[U][8], int row, int cols, float r, const NormOut& o,
-                                  float* slots) {
+template <int U, bool WHOLE>
+__device__ inline void finish_row(float (&v)[U][8], const Raw8<float> (&rw)[U], int row, int cols,
+                                  float r, const NormOut& o, float* slots) {
   const int threads = blockDim.x;
   const bool h_bf16 = o.h != nullptr && o.h_type == MOE_TYPE_BF16;
   float amax = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int e = 8 * (u * threads + (int)threadIdx.x);
-    if (o.w) {
-      float w[8];
-      to_f32(load_unit<VEC>(o.w, e, cols), w);
+    float w[8];
+    to_f32(rw[u], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * r * w[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] *= r;
-    }
+    for (int i = 0; i < 8; ++i) v[u][i] = o.w ? v[u][i] * r * w[i] : v[u][i] * r;
     if (h_bf16) {
-      store_unit<VEC>((__bf16*)o.h + (int64_t)row * o.ld_h, e, cols, v[u]);
+      store_unit<WHOLE>((__bf16*)o.h + (int64_t)row * o.ld_h, e, cols, v[u]);
       if (o.quant) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[u][i] = stored<__bf16>(v[u][i]);
       }
     } else if (o.h) {
-      store_unit<VEC>((float*)o.h + (int64_t)row * o.ld_h, e, cols, v[u]);
+      store_unit<WHOLE>((float*)o.h + (int64_t)row * o.ld_h, e, cols, v[u]);
     }
     if (o.quant == MOE_QUANT_BLOCK) {
       // elements past the row are 0 (0 * r * 0); cols % 32 == 0 keeps the
@@ -172,15 +161,21 @@ __device__ inline void finish_row(float (&v)[U][8], int row, int cols, float r, 
   }
 }
 
-template <typename XT, int U, bool VEC>
-__global__ __launch_bounds__(512) void norm_pre_kernel(NormArgs a) {
+// Every load of a row goes out before the first reduction: a row's time is one
+// memory round trip and two reductions, not one round trip per operand.
+template <typename XT, int U, bool WHOLE>
+__global__ __launch_bounds__(1024) void norm_pre_kernel(NormArgs a) {
   __shared__ float slots[2][16];
   const int row = blockIdx.x, cols = a.cols;
   const XT* x = (const XT*)a.x + (int64_t)row * a.ld_x;
   Raw8<XT> raw[U];
+  Raw8<float> rw[U] = {};
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    raw[u] = load_unit<VEC>(x, 8 * (u * (int)blockDim.x + (int)threadIdx.x), cols);
+  for (int u = 0; u < U; ++u) {
+    const int e = 8 * (u * (int)blockDim.x + (int)threadIdx.x);
+    raw[u] = load_unit<WHOLE>(x, e, cols);
+    if (a.o.w) rw[u] = load_unit<WHOLE>(a.o.w, e, cols);
+  }
   float v[U][8], ss = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -189,23 +184,37 @@ __global__ __launch_bounds__(512) void norm_pre_kernel(NormArgs a) {
     for (int i = 0; i < 8; ++i) ss = fmaf(v[u][i], v[u][i], ss);
   }
   const float r = 1.0f / sqrtf(wg_sum(ss, slots[0]) / (float)cols + a.o.eps);
-  finish_row<U, VEC>(v, row, cols, r, a.o, slots[1]);
+  finish_row<U, WHOLE>(v, rw, row, cols, r, a.o, slots[1]);
 }
 
-template <typename XT, typename RT, int U, bool VEC>
-__global__ __launch_bounds__(512) void norm_post_kernel(NormArgs a) {
+template <typename XT, typename RT, int U, bool WHOLE>
+__global__ __launch_bounds__(1024) void norm_post_kernel(NormArgs a) {
   __shared__ float slots[3][16];
   const int row = blockIdx.x, cols = a.cols, threads = blockDim.x;
   const XT* x = (const XT*)a.x + (int64_t)row * a.ld_x;
   const RT* res = (const RT*)a.res + (int64_t)row * a.ld_res;
+  const bool wide = a.gate && a.gate_col;  // a gate for each element
+  const bool gate_f32 = a.gate_type == MOE_TYPE_F32;
+  const int64_t g0 = (int64_t)row * a.gate_row;
   Raw8<XT> raw[U];
   Raw8<RT> rres[U];
+  Raw8<float> rw[U] = {}, rg[U] = {}, rn[U] = {};
+  Raw8<__bf16> rh[U] = {};
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int e = 8 * (u * threads + (int)threadIdx.x);
-    raw[u] = load_unit<VEC>(x, e, cols);
-    rres[u] = load_unit<VEC>(res, e, cols);
+    raw[u] = load_unit<WHOLE>(x, e, cols);
+    rres[u] = load_unit<WHOLE>(res, e, cols);
+    if (a.post_norm && a.w) rw[u] = load_unit<WHOLE>(a.w, e, cols);
+    if (wide) {
+      if (gate_f32) rg[u] = load_unit<WHOLE>((const float*)a.gate + g0, e, cols);
+      else rh[u] = load_unit<WHOLE>((const __bf16*)a.gate + g0, e, cols);
+    }
+    if (a.has_next && a.o.w) rn[u] = load_unit<WHOLE>(a.o.w, e, cols);
   }
+  float g1 = 1.f;  // a gate that is one number for the row
+  if (a.gate && !wide)
+    g1 = gate_f32 ? ((const float*)a.gate)[g0] : (float)((const __bf16*)a.gate)[g0];
   float v[U][8], ss = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -215,38 +224,22 @@ __global__ __launch_bounds__(512) void norm_post_kernel(NormArgs a) {
   }
   float r = 1.f;
   if (a.post_norm) r = 1.0f / sqrtf(wg_sum(ss, slots[0]) / (float)cols + a.eps);
-  float g1 = 1.f;  // a gate that is one number for the row
-  if (a.gate && a.gate_col == 0)
-    g1 = a.gate_type == MOE_TYPE_F32 ? ((const float*)a.gate)[(int64_t)row * a.gate_row]
-                                     : (float)((const __bf16*)a.gate)[(int64_t)row * a.gate_row];
   ss = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int e = 8 * (u * threads + (int)threadIdx.x);
-    float s[8];
+    float s[8], w[8], g[8], gh[8];
     to_f32(rres[u], s);
-    if (a.post_norm) {
+    to_f32(rw[u], w);
+    to_f32(rg[u], g);
+    to_f32(rh[u], gh);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] *= r;
-      if (a.w) {
-        float w[8];
-        to_f32(load_unit<VEC>(a.w, e, cols), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] *= w[i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      if (a.post_norm) v[u][i] = a.w ? v[u][i] * r * w[i] : v[u][i] * r;
+      const float gi = !wide ? g1 : gate_f32 ? g[i] : gh[i];
+      v[u][i] = fmaf(a.res_scale, s[i], gi * v[u][i]);
     }
-    float g[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = g1;
-    if (a.gate && a.gate_col) {
-      if (a.gate_type == MOE_TYPE_F32)
-        to_f32(load_unit<VEC>((const float*)a.gate + (int64_t)row * a.gate_row, e, cols), g);
-      else
-        to_f32(load_unit<VEC>((const __bf16*)a.gate + (int64_t)row * a.gate_row, e, cols), g);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[u][i] = fmaf(a.res_scale, s[i], g[i] * v[u][i]);
-    store_unit<VEC>((RT*)a.out + (int64_t)row * a.ld_out, e, cols, v[u]);
+    store_unit<WHOLE>((RT*)a.out + (int64_t)row * a.ld_out, e, cols, v[u]);
     if (a.has_next) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -257,27 +250,39 @@ __global__ __launch_bounds__(512) void norm_post_kernel(NormArgs a) {
   }
   if (!a.has_next) return;
   r = 1.0f / sqrtf(wg_sum(ss, slots[1]) / (float)cols + a.o.eps);
-  finish_row<U, VEC>(v, row, cols, r, a.o, slots[2]);
+  finish_row<U, WHOLE>(v, rn, row, cols, r, a.o, slots[2]);
 }
 
-// Row quantiser: the row's largest magnitude, then its codes; the second
-// read comes from the caches.
-template <typename XT>
-__global__ __launch_bounds__(512) void quant_row_kernel(const XT* x0, int64_t ld_x, int cols, int8_t* q0, int64_t ld_q,
-                                 float* scales, int vec) {
+// Row quantiser: a row of up to 8 kThreads U elements is held in registers;
+// what is longer is read again, from the caches.
+constexpr int kQuantThreads = 512, kQuantUnits = 4;
+
+template <typename XT, bool WHOLE>
+__global__ __launch_bounds__(kQuantThreads) void quant_row_kernel(const XT* x0, int64_t ld_x,
+                                                                  int cols, int8_t* q0,
+                                                                  int64_t ld_q, float* scales) {
   __shared__ float slots[16];
-  const int row = blockIdx.x;
+  const int row = blockIdx.x, threads = blockDim.x, stride = 8 * threads;
   const XT* x = x0 + (int64_t)row * ld_x;
   int8_t* q = q0 + (int64_t)row * ld_q;
+  Raw8<XT> raw[kQuantUnits];
   float amax = 0.f, v[8];
-  for (int e = 8 * (int)threadIdx.x; e < cols; e += 8 * (int)blockDim.x) {
-    to_f32(vec ? load_unit<true>(x, e, cols) : load_unit<false>(x, e, cols), v);
+#pragma unroll
+  for (int u = 0; u < kQuantUnits; ++u)
+    raw[u] = load_unit<WHOLE>(x, 8 * (u * threads + (int)threadIdx.x), cols);
+#pragma unroll
+  for (int u = 0; u < kQuantUnits; ++u) {
+    to_f32(raw[u], v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  }
+  for (int e = kQuantUnits * stride + 8 * (int)threadIdx.x; e < cols; e += stride) {
+    to_f32(load_unit<WHOLE>(x, e, cols), v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
   }
   const float d = wg_max(amax, slots) / 127.0f;
-  for (int e = 8 * (int)threadIdx.x; e < cols; e += 8 * (int)blockDim.x) {
-    to_f32(vec ? load_unit<true>(x, e, cols) : load_unit<false>(x, e, cols), v);
+  auto write = [&](int e) {
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -289,6 +294,17 @@ __global__ __launch_bounds__(512) void quant_row_kernel(const XT* x0, int64_t ld
       for (int i = 0; i < 8; ++i)
         if (e + i < cols) q[e + i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
     }
+  };
+#pragma unroll
+  for (int u = 0; u < kQuantUnits; ++u) {
+    const int e = 8 * (u * threads + (int)threadIdx.x);
+    if (e >= cols) break;
+    to_f32(raw[u], v);
+    write(e);
+  }
+  for (int e = kQuantUnits * stride + 8 * (int)threadIdx.x; e < cols; e += stride) {
+    to_f32(load_unit<WHOLE>(x, e, cols), v);
+    write(e);
   }
   if (threadIdx.x == 0) scales[row] = d;
 }
@@ -323,56 +339,43 @@ static int norm_out_check(int cols, const NormOut& o) {
   return MOE_OK;
 }
 
-// rows in 16-byte pieces of 8 (bf16) or 4 (f32) elements
-static bool vec_rows(const void* p, int type, int64_t ld) {
-  return aligned(p, 16) && ld % (type == MOE_TYPE_F32 ? 4 : 8) == 0;
-}
-static bool vec_out(const NormOut& o) {
-  return (!o.h || vec_rows(o.h, o.h_type, o.ld_h)) && aligned(o.w, 16);
-}
-
 // Threads of a row and units of 8 elements per thread, by the row's length
 // alone (so a row's bits do not depend on the call).
 struct RowShape {
   int threads, units;
 };
 static RowShape row_shape(int cols) {
-  const int n = (cols + 7) / 8;
-  const int units = n <= 512 ? 1 : n <= 1024 ? 2 : 4;
+  const int n = (cols + 7) / 8, units = n <= 1024 ? 1 : 2;
   return {((n + units - 1) / units + 63) / 64 * 64, units};
 }
 
 template <typename XT>
-static void launch_pre(const NormArgs& a, int rows, bool vec, hipStream_t s) {
+static void launch_pre(const NormArgs& a, int rows, hipStream_t s) {
   const RowShape r = row_shape(a.cols);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(rows), dim3(r.threads), 0, s, a);
   };
-  if (vec) {
+  if (a.cols % 8 == 0) {
     if (r.units == 1) go(norm_pre_kernel<XT, 1, true>);
-    else if (r.units == 2) go(norm_pre_kernel<XT, 2, true>);
-    else go(norm_pre_kernel<XT, 4, true>);
+    else go(norm_pre_kernel<XT, 2, true>);
   } else {
     if (r.units == 1) go(norm_pre_kernel<XT, 1, false>);
-    else if (r.units == 2) go(norm_pre_kernel<XT, 2, false>);
-    else go(norm_pre_kernel<XT, 4, false>);
+    else go(norm_pre_kernel<XT, 2, false>);
   }
 }
 
 template <typename XT, typename RT>
-static void launch_post(const NormArgs& a, int rows, bool vec, hipStream_t s) {
+static void launch_post(const NormArgs& a, int rows, hipStream_t s) {
   const RowShape r = row_shape(a.cols);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(rows), dim3(r.threads), 0, s, a);
   };
-  if (vec) {
+  if (a.cols % 8 == 0) {
     if (r.units == 1) go(norm_post_kernel<XT, RT, 1, true>);
-    else if (r.units == 2) go(norm_post_kernel<XT, RT, 2, true>);
-    else go(norm_post_kernel<XT, RT, 4, true>);
+    else go(norm_post_kernel<XT, RT, 2, true>);
   } else {
     if (r.units == 1) go(norm_post_kernel<XT, RT, 1, false>);
-    else if (r.units == 2) go(norm_post_kernel<XT, RT, 2, false>);
-    else go(norm_post_kernel<XT, RT, 4, false>);
+    else go(norm_post_kernel<XT, RT, 2, false>);
   }
 }
 
@@ -400,10 +403,9 @@ extern "C" int moe_norm_pre(const moe_norm_t* N, const void* x, int x_type, int6
   a.ld_x = ld_x;
   a.cols = cols;
   a.o = o;
-  const bool vec = cols % 8 == 0 && vec_rows(x, x_type, ld_x) && vec_out(o);
   hipStream_t s = (hipStream_t)stream;
-  if (x_type == MOE_TYPE_F32) launch_pre<float>(a, rows, vec, s);
-  else launch_pre<__bf16>(a, rows, vec, s);
+  if (x_type == MOE_TYPE_F32) launch_pre<float>(a, rows, s);
+  else launch_pre<__bf16>(a, rows, s);
   return launch_status();
 }
 
@@ -439,16 +441,12 @@ extern "C" int moe_norm_post(const moe_norm_t* N, const void* y, int y_type, int
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
   NormArgs a{y, ld_y, cols, N->post_norm, N->eps, N->residual_scale, N->post_w, res, ld_res,
              gate, gate_type, gate_row, gate_col, out, ld_out, next != nullptr, o};
-  const bool vec = cols % 8 == 0 && vec_rows(y, y_type, ld_y) &&
-                   vec_rows(res, res_type, ld_res) && vec_rows(out, res_type, ld_out) &&
-                   (!gate || gate_col == 0 || vec_rows(gate, gate_type, gate_row)) &&
-                   aligned(N->post_w, 16) && (!next || vec_out(o));
   hipStream_t s = (hipStream_t)stream;
   const bool yf = y_type == MOE_TYPE_F32, rf = res_type == MOE_TYPE_F32;
-  if (yf && rf) launch_post<float, float>(a, rows, vec, s);
-  else if (yf) launch_post<float, __bf16>(a, rows, vec, s);
-  else if (rf) launch_post<__bf16, float>(a, rows, vec, s);
-  else launch_post<__bf16, __bf16>(a, rows, vec, s);
+  if (yf && rf) launch_post<float, float>(a, rows, s);
+  else if (yf) launch_post<float, __bf16>(a, rows, s);
+  else if (rf) launch_post<__bf16, float>(a, rows, s);
+  else launch_post<__bf16, __bf16>(a, rows, s);
   return launch_status();
 }
 
@@ -462,14 +460,18 @@ extern "C" int moe_quant_row_q8(const void* x, int x_type, int64_t ld_x, int row
   if (!aligned(x, type_size(x_type)) || !aligned(q, 8) || ld_q % 8 != 0 || !aligned(scales, 4))
     return MOE_ERR_ALIGNMENT;
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
-  const int threads = min(512, ((cols + 7) / 8 + 63) / 64 * 64);
-  const int vec = cols % 8 == 0 && vec_rows(x, x_type, ld_x);
+  const int n = (cols + 7) / 8;
+  const int threads = min(kQuantThreads, (n + 63) / 64 * 64);
   hipStream_t s = (hipStream_t)stream;
-  if (x_type == MOE_TYPE_F32)
-    hipLaunchKernelGGL(quant_row_kernel<float>, dim3(rows), dim3(threads), 0, s, (const float*)x,
-                       ld_x, cols, q, ld_q, scales, vec);
-  else
-    hipLaunchKernelGGL(quant_row_kernel<__bf16>, dim3(rows), dim3(threads), 0, s,
-                       (const __bf16*)x, ld_x, cols, q, ld_q, scales, vec);
+  auto go = [&](auto kernel, auto* p) {
+    hipLaunchKernelGGL(kernel, dim3(rows), dim3(threads), 0, s, p, ld_x, cols, q, ld_q, scales);
+  };
+  if (x_type == MOE_TYPE_F32) {
+    if (cols % 8 == 0) go(quant_row_kernel<float, true>, (const float*)x);
+    else go(quant_row_kernel<float, false>, (const float*)x);
+  } else {
+    if (cols % 8 == 0) go(quant_row_kernel<__bf16, true>, (const __bf16*)x);
+    else go(quant_row_kernel<__bf16, false>, (const __bf16*)x);
+  }
   return launch_status();
 }
