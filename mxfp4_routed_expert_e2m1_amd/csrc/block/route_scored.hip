@@ -42,6 +42,11 @@ struct RuleArgs {
   int32_t* sorted;
 };
 
+template <int CTRL>
+__device__ inline uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
+}
+
 // The picks of one row: lane s < top_k gets pick s (-1: none left) and its
 // weight.  `lds` holds 64 * PER_LANE words of this wave.
 template <int PER_LANE>
@@ -94,20 +99,32 @@ __device__ inline void choose_row(const RuleArgs& p, int row, uint32_t* lds, int
     for (int j = 0; j < PER_LANE; ++j) lds[lane + 64 * j] = k[j];
     __builtin_amdgcn_wave_barrier();
     // group g's lanes are g << lanes_log2 on; each reads every 2^lanes_log2-th
-    // member, then the lanes' two largest are merged
+    // member, four at a time, then the lanes' two largest are merged
     const int P = 1 << p.lanes_log2, g = lane >> p.lanes_log2;
     uint32_t k1 = 0, k2 = 0;
-    if (g < p.n_groups)
-      for (int i = lane & (P - 1); i < p.group_size; i += P) {
-        const uint32_t v = lds[g * p.group_size + i];
-        k2 = max(k2, min(k1, v));
-        k1 = max(k1, v);
+    for (int i0 = lane & (P - 1); i0 < p.group_size; i0 += 4 * P) {
+      uint32_t v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * P;
+        v[u] = g < p.n_groups && i < p.group_size ? lds[g * p.group_size + i] : 0u;
       }
-    for (int m = 1; m < P; m <<= 1) {
-      const uint32_t o1 = __shfl_xor(k1, m, 64), o2 = __shfl_xor(k2, m, 64);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        k2 = max(k2, min(k1, v[u]));
+        k1 = max(k1, v[u]);
+      }
+    }
+    auto merge = [&](uint32_t o1, uint32_t o2) {
       k2 = max(min(k1, o1), max(k2, o2));
       k1 = max(k1, o1);
-    }
+    };
+    // (lanes that have merged hold the same pair, so a mirror is a swap)
+    if (P >= 2) merge(dpp_u32<0xB1>(k1), dpp_u32<0xB1>(k2));    // quad_perm [1,0,3,2]
+    if (P >= 4) merge(dpp_u32<0x4E>(k1), dpp_u32<0x4E>(k2));    // quad_perm [2,3,0,1]
+    if (P >= 8) merge(dpp_u32<0x141>(k1), dpp_u32<0x141>(k2));  // row_half_mirror
+    if (P >= 16) merge(dpp_u32<0x140>(k1), dpp_u32<0x140>(k2));  // row_mirror
+    if (P >= 32) merge(__shfl_xor(k1, 16, 64), __shfl_xor(k2, 16, 64));
     uint32_t gk = k1;
     if (p.group_score == MOE_GROUP_TOP2 && k2 != 0)
       gk = logit_key(logit_of_key(k1) + logit_of_key(k2));
@@ -125,34 +142,34 @@ __device__ inline void choose_row(const RuleArgs& p, int row, uint32_t* lds, int
     }
   }
 
+  // the scores wait in LDS for the picks
+#pragma unroll
+  for (int j = 0; j < PER_LANE; ++j) lds[lane + 64 * j] = __builtin_bit_cast(uint32_t, s[j]);
   int id = -1;
-  float w = 0.f;
   for (int r = 0; r < p.top_k; ++r) {
     uint32_t lm = k[0];
 #pragma unroll
     for (int j = 1; j < PER_LANE; ++j) lm = max(lm, k[j]);
     const uint32_t bk = wave_max_u32(lm);
     if (bk == 0u) break;  // none left: the remaining slots keep -1
-    int be = 0;
-    float bs = 0.f;
+    int slot = 0;
+    uint64_t holders = 0;
 #pragma unroll
     for (int j = PER_LANE - 1; j >= 0; --j) {
       const uint64_t m = __ballot(k[j] == bk);
-      if (m != 0ull) {
-        be = 64 * j + (__ffsll((unsigned long long)m) - 1);
-        bs = s[j];
-      }
+      slot = m != 0ull ? j : slot;
+      holders = m != 0ull ? m : holders;
     }
-    bs = __builtin_bit_cast(float,
-                            __builtin_amdgcn_readlane(__builtin_bit_cast(int, bs), be & 63));
+    const int first = __ffsll((unsigned long long)holders) - 1;
+    const bool here = lane == first;
 #pragma unroll
     for (int j = 0; j < PER_LANE; ++j)
-      if (lane + 64 * j == be) k[j] = 0u;
-    if (lane == r) {
-      id = be;
-      w = bs;
-    }
+      if (here && slot == j) k[j] = 0u;
+    if (lane == r) id = 64 * slot + first;
   }
+  __builtin_amdgcn_wave_barrier();
+  float w = id >= 0 ? __builtin_bit_cast(float, lds[id]) : 0.f;
+  __builtin_amdgcn_wave_barrier();
   if (p.renorm) {
     float sum = 0.f;
     for (int r = 0; r < p.top_k; ++r)
@@ -222,17 +239,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_small_kernel(RuleArgs p) 
 
 // More rows, launch 1: run b (rows b*run_rows on) writes its rows' picks and
 // how many of them chose each expert, hist[b][e].
-template <int PER_LANE>
-__global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RuleArgs p, int run_rows,
-                                                                     uint16_t* hist,
-                                                                     int hist_ld) {
-  __shared__ uint32_t keys[kRouteWaves][64 * PER_LANE];
+template <int PER_LANE, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void route_choose_kernel(RuleArgs p, int run_rows,
+                                                                  uint16_t* hist, int hist_ld) {
+  __shared__ uint32_t keys[WAVES][64 * PER_LANE];
   __shared__ int count[kRuleMaxExperts];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e < hist_ld; e += kRouteThreads) count[e] = 0;
+  for (int e = tid; e < hist_ld; e += 64 * WAVES) count[e] = 0;
   __syncthreads();
   const int r1 = min(p.rows, ((int)blockIdx.x + 1) * run_rows);
-  for (int row = blockIdx.x * run_rows + wave; row < r1; row += kRouteWaves) {
+  for (int row = blockIdx.x * run_rows + wave; row < r1; row += WAVES) {
     int id;
     float w;
     choose_row<PER_LANE>(p, row, keys[wave], &id, &w);
@@ -243,7 +259,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RuleArgs p,
     }
   }
   __syncthreads();
-  for (int e = tid; e < hist_ld; e += kRouteThreads)
+  for (int e = tid; e < hist_ld; e += 64 * WAVES)
     hist[(int64_t)blockIdx.x * hist_ld + e] = (uint16_t)count[e];
 }
 
@@ -256,26 +272,43 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(
   __shared__ int slots[kRouteWaves];
   const int tid = threadIdx.x;
   const int run0 = blockIdx.x * group_runs;
-  for (int e = tid; e < kRuleMaxExperts; e += kRouteThreads) total_of[e] = next[e] = 0;
+  const int r0 = run0 * run_rows, r1 = min(p.rows, (run0 + group_runs) * run_rows);
+  // (the first 64 rows' ids: on their way while the counts are read)
+  const bool early = tid < 64 * p.top_k && r0 + tid / p.top_k < r1;
+  int e = early ? p.ids[(int64_t)r0 * p.top_k + tid] : -1;
+  for (int x = tid; x < kRuleMaxExperts; x += kRouteThreads) {
+    total_of[x] = next[x] = 0;
+    rows_of[x] = 0;
+  }
   __syncthreads();
-  // counts over all runs and over the runs before this workgroup's, two
-  // experts per thread
-  const int pairs = hist_ld / 2, strips = kRouteThreads / pairs;
-  const int col = tid % pairs, strip = tid / pairs;
+  // counts over all runs and over the runs before this workgroup's: eight
+  // experts per thread, every strips-th run, eight runs' loads at a time
+  const int cols = hist_ld / 8, strips = kRouteThreads / cols;
+  const int col = tid % cols, strip = tid / cols;
   if (strip < strips) {
-    int t0 = 0, t1 = 0, b0 = 0, b1 = 0;
-    for (int r = strip; r < n_runs; r += strips) {
-      const uint32_t v = ((const uint32_t*)hist)[(int64_t)r * pairs + col];
-      const int lo = v & 0xFFFF, hi = v >> 16;
-      t0 += lo;
-      t1 += hi;
-      b0 += r < run0 ? lo : 0;
-      b1 += r < run0 ? hi : 0;
+    int t[8] = {}, b[8] = {};
+    for (int r8 = strip; r8 < n_runs; r8 += 8 * strips) {
+      u32x4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = ((const u32x4*)hist)[(int64_t)min(r8 + u * strips, n_runs - 1) * cols + col];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int r = r8 + u * strips;
+        const uint32_t in = r < n_runs ? ~0u : 0u, earlier = r < run0 ? ~0u : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t x = (v[u][i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+          t[i] += (int)(x & in);
+          b[i] += (int)(x & earlier);
+        }
+      }
     }
-    atomicAdd(&total_of[2 * col], t0);
-    atomicAdd(&total_of[2 * col + 1], t1);
-    atomicAdd(&next[2 * col], b0);
-    atomicAdd(&next[2 * col + 1], b1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      atomicAdd(&total_of[8 * col + i], t[i]);
+      if (b[i] != 0) atomicAdd(&next[8 * col + i], b[i]);
+    }
   }
   __syncthreads();
   const int c = tid < p.n_experts ? total_of[tid] : 0;
@@ -283,7 +316,6 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(
   const int at = expert_scan(c, slots, &total);
   if (tid < p.n_experts) {
     next[tid] += at;
-    rows_of[tid] = 0;
     if (blockIdx.x == 0) {
       p.counts[tid] = c;
       p.offsets[tid] = at;
@@ -291,18 +323,18 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(
   }
   if (blockIdx.x == 0 && tid == 0) p.offsets[p.n_experts] = total;
   __syncthreads();
-  const int r0 = run0 * run_rows, r1 = min(p.rows, (run0 + group_runs) * run_rows);
   for (int rb = r0; rb < r1; rb += 64) {
     // one thread per assignment of 64 rows: at most 64 * MOE_MAX_TOP_K
     const int row = rb + tid / p.top_k;
     const bool mine = tid < 64 * p.top_k && row < r1;
     const int64_t a = (int64_t)rb * p.top_k + tid;
-    const int e = mine ? p.ids[a] : -1;
+    if (rb > r0) e = mine ? p.ids[a] : -1;
     if (e >= 0) atomicOr(&rows_of[e], 1ull << (row - rb));
     __syncthreads();
     if (e >= 0)
       p.sorted[next[e] + __popcll(rows_of[e] & ((1ull << (row - rb)) - 1))] = (int)a;
     if (mine && a >= total) p.sorted[a] = -1;
+    if (rb + 64 >= r1) break;
     __syncthreads();
     if (tid < p.n_experts) {
       next[tid] += __popcll(rows_of[tid]);
@@ -337,21 +369,24 @@ static int rule_check(const moe_router_rule_t* R) {
   return MOE_OK;
 }
 
-// Runs of launch 1: kRunRows rows each up to 8192 rows, longer beyond, so
-// that there are never more than 512 (a run's count of an expert, at most
-// 2^24 / 512 rows, fits 16 bits).  Launch 2 takes four runs per workgroup.
+// Runs of launch 1: 4 rows each, a wave per row and SIMD, up to 1024 rows (a
+// wave's work is long, so waves are better apart: 777 rows 7.7 -> 5.2 us), 16
+// rows beyond, and longer past 8192 rows, so that there are never more than
+// 512 (a run's count of an expert, at most 2^24 / 512 rows, fits 16 bits).
+// Launch 2 takes 64 rows or more, four or sixteen runs, per workgroup.
 struct RouteShape {
-  int run_rows, n_runs, hist_ld;
+  int waves, run_rows, n_runs, group_runs, hist_ld;
 };
 static RouteShape route_shape(int n_experts, int rows) {
-  const int m = (rows + 512 * kRunRows - 1) / (512 * kRunRows);
   RouteShape s;
-  s.run_rows = kRunRows * (m < 1 ? 1 : m);
+  s.waves = rows <= 1024 ? 4 : kRouteWaves;
+  const int m = (rows + 512 * s.waves - 1) / (512 * s.waves);
+  s.run_rows = s.waves * m;
   s.n_runs = (rows + s.run_rows - 1) / s.run_rows;
-  s.hist_ld = (n_experts + 1) / 2 * 2;
+  s.group_runs = 64 / s.waves;
+  s.hist_ld = (n_experts + 7) / 8 * 8;
   return s;
 }
-constexpr int kGroupRuns = 4;
 
 }  // namespace moe
 
@@ -425,14 +460,20 @@ extern "C" int moe_route_scored(const moe_router_rule_t* R, const void* logits, 
   }
   const RouteShape sh = route_shape(R->n_experts, rows);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(sh.n_runs), dim3(kRouteThreads), 0, s, p, sh.run_rows,
+    hipLaunchKernelGGL(kernel, dim3(sh.n_runs), dim3(64 * sh.waves), 0, s, p, sh.run_rows,
                        (uint16_t*)ws, sh.hist_ld);
   };
-  if (per_lane <= 2) go(route_choose_kernel<2>);
-  else if (per_lane <= 4) go(route_choose_kernel<4>);
-  else go(route_choose_kernel<8>);
-  hipLaunchKernelGGL(route_place_kernel, dim3((sh.n_runs + kGroupRuns - 1) / kGroupRuns),
-                     dim3(kRouteThreads), 0, s, p, sh.run_rows, sh.n_runs, kGroupRuns,
+  if (sh.waves == 4) {
+    if (per_lane <= 2) go(route_choose_kernel<2, 4>);
+    else if (per_lane <= 4) go(route_choose_kernel<4, 4>);
+    else go(route_choose_kernel<8, 4>);
+  } else {
+    if (per_lane <= 2) go(route_choose_kernel<2, kRouteWaves>);
+    else if (per_lane <= 4) go(route_choose_kernel<4, kRouteWaves>);
+    else go(route_choose_kernel<8, kRouteWaves>);
+  }
+  hipLaunchKernelGGL(route_place_kernel, dim3((sh.n_runs + sh.group_runs - 1) / sh.group_runs),
+                     dim3(kRouteThreads), 0, s, p, sh.run_rows, sh.n_runs, sh.group_runs,
                      (const uint16_t*)ws, sh.hist_ld);
   return launch_status();
 }
