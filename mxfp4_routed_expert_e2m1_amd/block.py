@@ -72,18 +72,14 @@ def _load():
     return _lib
 
 
-def _check(fn, rc):
-    if rc != 0:
-        import mxfp4_routed_expert_e2m1_amd as m
-        raise m.MoeError(fn, rc)
+def _fail(fn, rc):
+    import mxfp4_routed_expert_e2m1_amd as m
+    raise m.MoeError(fn, rc)
 
 
-def _stream(stream, t):
-    """The stream's handle (by default torch's current one on t's device; its raw handle alone:
-    making the stream object costs 2 us, more than the rest of a call's arguments)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return stream.cuda_stream
+# The raw handle of torch's current stream on a device: making the stream object costs 2 us,
+# about what the launch does.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _rows(name, t, shape=None, types=_TYPES):
@@ -109,10 +105,11 @@ def _vec(name, t, n, dtype=torch.float32, least=False):
     """Pointer of a contiguous tensor of n (or, with `least`, at least n) elements, or None."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: {t.dtype}, need {dtype}")
     have = t.numel()
-    if (have != n and not (least and have > n)) or not t.is_cuda or not t.is_contiguous():
+    if (t.dtype != dtype or (have != n and not (least and have > n)) or not t.is_cuda
+            or not t.is_contiguous()):
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: {t.dtype}, need {dtype}")
         raise ValueError(f"{name}: need {n} contiguous elements on the GPU")
     return t.data_ptr()
 
@@ -169,14 +166,18 @@ def moe_norm_pre(norm, x, h=None, h_dtype=None, quant=None, q=None, qs=None, str
     if cols != norm.d_model:
         raise ValueError(f"x: {cols} columns, the norm has d_model {norm.d_model}")
     h, q, qs, out = _norm_out(x, h, h_dtype, quant, q, qs)
-    _check("moe_norm_pre", (_lib or _load()).moe_norm_pre(norm.ref, *xa, rows, *out,
-                                                          _stream(stream, x)))
+    rc = (_lib or _load()).moe_norm_pre(
+        norm.ref, *xa, rows, *out,
+        stream.cuda_stream if stream else _raw_stream(x.get_device()))
+    if rc:
+        _fail("moe_norm_pre", rc)
     return h if quant is None else (h, q, qs)
 
 
+_NO_GATE = (None, 0, 0, 0)
+
+
 def _gate_args(gate, shape):
-    if gate is None:
-        return None, 0, 0, 0
     kind, sh, st = _TYPES.get(gate.dtype), gate.shape, gate.stride()
     if kind is None:
         raise TypeError(f"gate: {gate.dtype} is not one of {[str(d) for d in _TYPES]}")
@@ -214,9 +215,11 @@ def moe_norm_post(norm, y, residual, gate=None, out=None, next_norm=None, h=None
     else:
         h, q, qs, nargs = _norm_out(residual, h, h_dtype, quant, q, qs)
         nx = next_norm.ref
-    _check("moe_norm_post", (_lib or _load()).moe_norm_post(
-        norm.ref, *ya, *ra, *_gate_args(gate, shape), shape[0], op, ld_out, nx, *nargs,
-        _stream(stream, y)))
+    rc = (_lib or _load()).moe_norm_post(
+        norm.ref, *ya, *ra, *(_NO_GATE if gate is None else _gate_args(gate, shape)), shape[0],
+        op, ld_out, nx, *nargs, stream.cuda_stream if stream else _raw_stream(y.get_device()))
+    if rc:
+        _fail("moe_norm_post", rc)
     if next_norm is None:
         return out
     return (out, h) if quant is None else (out, h, q, qs)
@@ -273,15 +276,19 @@ def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
     if ws is None:
         ws = torch.empty(moe_route_scored_workspace_bytes(rule, rows), dtype=torch.uint8,
                          device=logits.device)
-    _check("moe_route_scored", (_lib or _load()).moe_route_scored(
-        rule.ref, *la, rows, *ptrs, ws.data_ptr(), ws.numel(), _stream(stream, logits)))
+    rc = (_lib or _load()).moe_route_scored(
+        rule.ref, *la, rows, *ptrs, ws.data_ptr(), ws.numel(),
+        stream.cuda_stream if stream else _raw_stream(logits.get_device()))
+    if rc:
+        _fail("moe_route_scored", rc)
     return out
 
 
 # ------------------------------------------------------------- linear layers
 def codes_buffer(rows, cols, device="cuda"):
-    """int8 [rows][cols] whose rows start 16-byte aligned, as the int8 calls need."""
-    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8,
+    """int8 [rows][cols] with rows a multiple of 128 bytes apart: the int8 calls need 16, and
+    rows that start a cache line are read fastest."""
+    return torch.empty((rows, (cols + 127) // 128 * 128), dtype=torch.int8,
                        device=device)[:, :cols]
 
 
@@ -296,8 +303,11 @@ def moe_quant_row_q8(x, q=None, scales=None, stream=None):
     if scales is None:
         scales = torch.empty(rows, dtype=torch.float32, device=x.device)
     qp, _, ld_q = _rows("q", q, shape, _INT8)
-    _check("moe_quant_row_q8", (_lib or _load()).moe_quant_row_q8(
-        *xa, rows, cols, qp, ld_q, _vec("scales", scales, rows), _stream(stream, x)))
+    rc = (_lib or _load()).moe_quant_row_q8(
+        *xa, rows, cols, qp, ld_q, _vec("scales", scales, rows),
+        stream.cuda_stream if stream else _raw_stream(x.get_device()))
+    if rc:
+        _fail("moe_quant_row_q8", rc)
     return q, scales
 
 
@@ -344,7 +354,9 @@ def moe_linear_q8(linear, q, qs, y=None, dtype=torch.bfloat16, ws=None, stream=N
     if ws is None:
         ws = torch.empty(moe_linear_q8_workspace_bytes(linear, rows), dtype=torch.uint8,
                          device=q.device)
-    _check("moe_linear_q8", (_lib or _load()).moe_linear_q8(
+    rc = (_lib or _load()).moe_linear_q8(
         linear.ref, qp, ld_q, _vec("qs", qs, rows), rows, *_rows("y", y, (rows, linear.n_out)),
-        ws.data_ptr(), ws.numel(), _stream(stream, q)))
+        ws.data_ptr(), ws.numel(), stream.cuda_stream if stream else _raw_stream(q.get_device()))
+    if rc:
+        _fail("moe_linear_q8", rc)
     return y

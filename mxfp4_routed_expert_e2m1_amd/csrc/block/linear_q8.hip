@@ -29,7 +29,6 @@ struct LinearArgs {
   int rows, n_out, d_in;
   void* y;
   int y_bf16;
-  int y_vec;  // rows of y are 16-byte aligned
   int64_t ld_y;
   // split K: int32 sums of split i at parts + i * rows * parts_ld
   int32_t* parts;
@@ -151,14 +150,13 @@ __device__ inline void stage_barrier() {
 }
 
 // A wave's 32 tokens x 32 TN channels of results, from the matrix core's lanes
-// through LDS to rows: 4 channels at a time in, 16 bytes (or, where the rows
-// of y do not divide so, one element) per lane out.  The stores go through a
-// buffer resource that ends with the last row, and a lane past the last
-// channel stores past that end, so there is no branch.
+// through LDS to rows: 4 channels at a time in, 16 bytes per lane out (at any
+// address: the rows of y need their elements' alignment alone), and what is
+// left of a row at the last channel one element at a time.
 struct RowsOut {
   void* y;
   int64_t ld;
-  int rows, cols, vec;  // vec: the rows are 16-byte aligned
+  int rows, cols;
 };
 template <int TN, typename T>
 __device__ inline void store_rows(const RowsOut& o, i32x16 (&c)[TN], int t0, int n0, float qs,
@@ -184,34 +182,23 @@ __device__ inline void store_rows(const RowsOut& o, i32x16 (&c)[TN], int t0, int
     }
   __builtin_amdgcn_wave_barrier();
   const int rows = min(32, o.rows - t0), cols = min(kCols, o.cols - n0);
-  const uint32_t ld = (uint32_t)o.ld * sizeof(T);
-  const auto y = buf_rsrc((T*)o.y + uniform((int64_t)t0 * o.ld + n0),
-                          (uint32_t)(rows - 1) * ld + (uint32_t)cols * sizeof(T));
-  constexpr uint32_t kOut = 0xFFFFFFF0u;
-  if (o.vec && cols % kPer == 0) {
-    constexpr int kLanes = kCols / kPer, kPasses = kLanes / 2;  // lanes per row
-    const int col = (lane % kLanes) * kPer, r0 = lane / kLanes;
-    u32x4 v[kPasses];
+  T* y = (T*)o.y + uniform((int64_t)t0 * o.ld + n0);
+  constexpr int kLanes = kCols / kPer, kPasses = kLanes / 2;  // lanes per row
+  const int col = (lane % kLanes) * kPer, r0 = lane / kLanes;
+  u32x4 v[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i)
+    v[i] = *(const u32x4*)(buf + (r0 + i * (64 / kLanes)) * kLd + col);
+  if (col + kPer <= cols) {
+    T* p = y + (int64_t)r0 * o.ld + col;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
-      v[i] = *(const u32x4*)(buf + (r0 + i * (64 / kLanes)) * kLd + col);
-    const uint32_t at = col < cols ? r0 * ld + col * (uint32_t)sizeof(T) : kOut;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      __builtin_amdgcn_raw_buffer_store_b128(v[i], y, col < cols ? at + i * (64 / kLanes) * ld : kOut,
-                                             0, 0);
-  } else {
-    for (int r = 0; r < rows; ++r)
-#pragma unroll
-      for (int n = lane; n < kCols; n += 64) {
-        const uint32_t at = n < cols ? r * ld + n * (uint32_t)sizeof(T) : kOut;
-        if constexpr (sizeof(T) == 4)
-          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, buf[r * kLd + n]), y,
-                                                at, 0, 0);
-        else
-          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, buf[r * kLd + n]), y,
-                                                at, 0, 0);
-      }
+      if (r0 + i * (64 / kLanes) < rows)
+        __builtin_memcpy(p + (int64_t)(i * (64 / kLanes)) * o.ld, &v[i], 16);
+  }
+  if (cols % kPer && lane < rows) {
+    for (int n = cols / kPer * kPer; n < cols; ++n)
+      y[(int64_t)lane * o.ld + n] = buf[lane * kLd + n];
   }
   __builtin_amdgcn_wave_barrier();
 }
@@ -359,10 +346,10 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tile
     for (int i = 0; i < TN; ++i) cj[i] = c[i][j];
     const float qs = row_scale[t - t0 + (lane & 31)];
     const float *cs = channel_scale + (n - n0), *cb = channel_bias + (n - n0);
-    const RowsOut o{a.y, a.ld_y, a.rows, a.n_out, a.y_vec};
+    const RowsOut o{a.y, a.ld_y, a.rows, a.n_out};
     if (a.parts) {
       const RowsOut po{a.parts + split * (a.rows * a.parts_ld), a.parts_ld, a.rows,
-                       (int)a.parts_ld, 1};
+                       (int)a.parts_ld};
       store_rows<TN>(po, cj, t, n, qs, cs, cb, (int32_t*)mine);
     } else if (a.y_bf16) {
       store_rows<TN>(o, cj, t, n, qs, cs, cb, (__bf16*)mine);
@@ -594,7 +581,7 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
   hipStream_t s = (hipStream_t)stream;
   const int bf16 = y_type == MOE_TYPE_BF16;
   const LinearArgs a{L->w, L->ld_w, L->w_scales, L->bias, q, ld_q, qs, rows, L->n_out, L->d_in,
-                     y, bf16, aligned(y, 16) && ld_y % (bf16 ? 8 : 4) == 0, ld_y,
+                     y, bf16, ld_y,
                      p.splits > 1 ? (int32_t*)ws : nullptr, parts_ld(L->n_out)};
   if (p.tile < 0) {
     hipLaunchKernelGGL(linear_stream_kernel, dim3((L->n_out + 15) / 16),
