@@ -65,9 +65,9 @@ __device__ inline void linear_store(const LinearArgs& a, int t, int n, float v) 
 // wave 32 TT x 32 TN of them.  K goes in steps of STEP codes, copied from
 // memory to LDS directly into a ring of four stages, three steps ahead, so that
 // a step has to wait neither for memory nor for the copy unit (which takes 64
-// bytes a cycle: the copies are spread evenly over the products).  The larger
-// tiles take steps of 64 codes (the largest one's ring fills the LDS), the two
-// smallest 128, for half the barriers (512 rows of 4096 x 4096: 16.5 -> 13.8
+// bytes a cycle: the copies are spread evenly over the products).  The two
+// larger tiles take steps of 64 codes (the ring of the largest fills the LDS),
+// the others 128, for half the barriers (512 rows of 4096 x 4096: 16.5 -> 13.8
 // us).  A row's P = STEP / 16 pieces sit in LDS at
 // piece ^ (row / (16 / P) % P), so the 16 rows that a read takes at once lie in
 // different banks; the copy takes the pieces from memory in that order, since
@@ -500,47 +500,86 @@ static int linear_check(const moe_linear_t* L) {
 }
 
 // The tile sizes, tokens x channels in units of 64, with what a K step of 64
-// and a tile's start and end cost on a full chip (us, measured; the smaller
-// tiles share a CU, so their figures are per tile in turn).
+// costs a tile alone and on a full chip, and a tile's start and end (us,
+// measured; the smaller tiles share a CU, so theirs are per tile in turn).
 struct Tile8 {
   int tt, tn;
-  float step_us, tile_us;
+  float alone_us, full_us, ends_us;
 };
-constexpr Tile8 kTiles[] = {
-    {4, 4, 0.95f, 6.f}, {4, 2, 0.56f, 3.f}, {2, 2, 0.31f, 2.f}, {1, 2, 0.15f, 1.5f},
-    {1, 1, 0.085f, 1.2f}};
+constexpr Tile8 kTiles[] = {{4, 4, 0.53f, 0.88f, 4.f},
+                            {4, 2, 0.36f, 0.52f, 3.f},
+                            {2, 2, 0.18f, 0.30f, 2.f},
+                            {1, 2, 0.12f, 0.15f, 1.5f},
+                            {1, 1, 0.08f, 0.085f, 1.2f}};
 constexpr int kChipCus = 256;
 
-struct LinearPlan {
-  int tile;    // index into kTiles, or -1: the weight stream
-  int splits;  // of K
+// One launch: a tile size (-1: the weight stream), K splits, and the channels
+// it takes from the first that is left.
+struct LinearPart {
+  int tile, splits, channels;
 };
+struct LinearPlan {
+  LinearPart part[2];
+  int n_parts;
+};
+
+static int ceil_div(int64_t a, int b) { return (int)((a + b - 1) / b); }
+
+// Estimated time of `tiles` tiles of `steps` K steps each: full rounds over the
+// chip, then the tiles that are left.
+static double rounds_us(const Tile8& t, int64_t tiles, double steps) {
+  const double left = (double)(tiles % kChipCus) / kChipCus;
+  const double full = (double)(tiles / kChipCus) * (steps * t.full_us + t.ends_us);
+  return left == 0 ? full
+                   : full + steps * (t.alone_us + left * (t.full_us - t.alone_us)) + t.ends_us;
+}
+
+// The tile and the number of K splits with the least estimated time for
+// `channels` channels: rounds of tiles over the chip, plus, for splits, the
+// launch that joins them and its traffic (48 rows of 4096 x 14336: 21.5 us in
+// one, 14.9 in four; 512 rows of 4096 x 4096: 13.8 in one, 24.6 in two).
+static LinearPart best_part(int rows, int channels, int d_in, int most_splits, double* us) {
+  LinearPart best{0, 1, channels};
+  *us = 1e30;
+  const double steps = ceil_div(d_in, 64);
+  for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+    const Tile8& t = kTiles[i];
+    const int64_t tiles = (int64_t)ceil_div(rows, 64 * t.tt) * ceil_div(channels, 64 * t.tn);
+    for (int s = 1; s <= most_splits; s *= 2) {
+      if (s > 1 && (steps / s < 8 || tiles * s > kChipCus)) break;
+      double x = rounds_us(t, tiles * s, steps / s);
+      if (s > 1) x += 4. + (double)s * rows * channels * 8 / 5e6;
+      if (x < *us) {
+        *us = x;
+        best = {i, s, channels};
+      }
+    }
+  }
+  return best;
+}
 
 // Up to 16 rows the weight stream, unless there are channels enough for small
 // tiles to fill the chip (16 rows of 14336 x 4096: tiles 11.1 us, stream 13.2;
-// one row of 4096 x 4096: 8.2 and 5.8).  Otherwise the tile and the number of
-// K splits with the least estimated time: rounds of tiles over the chip, plus,
-// for splits, the launch that joins them and its traffic (48 rows of
-// 4096 x 14336: 21.5 us in one, 14.9 in four; 512 rows of 4096 x 4096: 13.8 in
-// one, 24.6 in two).
+// one row of 4096 x 4096: 8.2 and 5.8).  Otherwise the best tile; or, where its
+// last round would leave much of the chip idle, whole rounds of it and a second
+// launch with the best tile for the channels left.
 static LinearPlan plan(int rows, int n_out, int d_in) {
-  if (rows <= 16 && (n_out + 63) / 64 < 3 * kChipCus / 4) return {-1, 1};
-  LinearPlan best{0, 1};
-  double best_us = 1e30;
-  const double steps = (d_in + 63) / 64;
-  for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+  if (rows <= 16 && ceil_div(n_out, 64) < 3 * kChipCus / 4) return {{{-1, 1, n_out}, {}}, 1};
+  double us;
+  LinearPlan best{{best_part(rows, n_out, d_in, 8, &us), {}}, 1};
+  for (int i = 0; i < 2; ++i) {  // (smaller tiles have short last rounds)
     const Tile8& t = kTiles[i];
-    const int64_t tiles = (int64_t)((rows + 64 * t.tt - 1) / (64 * t.tt)) *
-                          ((n_out + 64 * t.tn - 1) / (64 * t.tn));
-    for (int s = 1; s <= 8; s *= 2) {
-      if (s > 1 && (steps / s < 8 || tiles * s > kChipCus)) break;
-      const double rounds = (double)((tiles * s + kChipCus - 1) / kChipCus);
-      double us = rounds * (steps / s * t.step_us + t.tile_us);
-      if (s > 1) us += 3. + (double)s * rows * n_out * 8 / 5e6;
-      if (us < best_us) {
-        best_us = us;
-        best = {i, s};
-      }
+    const int tiles_t = ceil_div(rows, 64 * t.tt);
+    const int64_t tiles = (int64_t)tiles_t * ceil_div(n_out, 64 * t.tn);
+    const int rounds = (int)(tiles / kChipCus);
+    const int64_t main = (int64_t)rounds * kChipCus / tiles_t * 64 * t.tn;
+    if (rounds == 0 || main == 0 || main >= n_out) continue;
+    double rest_us;
+    const LinearPart rest = best_part(rows, (int)(n_out - main), d_in, 1, &rest_us);
+    const double x = 2. + rest_us + rounds_us(t, (int64_t)rounds * kChipCus, ceil_div(d_in, 64));
+    if (x < us) {
+      us = x;
+      best = {{{i, 1, (int)main}, rest}, 2};
     }
   }
   return best;
@@ -554,7 +593,7 @@ using namespace moe;
 
 extern "C" size_t moe_linear_q8_workspace_bytes(const moe_linear_t* L, int rows) {
   if (linear_check(L) != MOE_OK || rows < 1) return 0;
-  const LinearPlan p = plan(rows, L->n_out, L->d_in);
+  const LinearPart p = plan(rows, L->n_out, L->d_in).part[0];
   return p.splits > 1 ? (size_t)p.splits * rows * parts_ld(L->n_out) * sizeof(int32_t) : 0;
 }
 
@@ -580,30 +619,36 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
   hipStream_t s = (hipStream_t)stream;
   const int bf16 = y_type == MOE_TYPE_BF16;
-  const LinearArgs a{L->w, L->ld_w, L->w_scales, L->bias, q, ld_q, qs, rows, L->n_out, L->d_in,
-                     y, bf16, ld_y,
-                     p.splits > 1 ? (int32_t*)ws : nullptr, parts_ld(L->n_out)};
-  if (p.tile < 0) {
-    hipLaunchKernelGGL(linear_stream_kernel, dim3((L->n_out + 15) / 16),
-                       dim3(64 * kStreamWaves), 0, s, a);
-    return launch_status();
+  int first = 0;  // channel
+  for (int i = 0; i < p.n_parts; ++i) {
+    const LinearPart& part = p.part[i];
+    const LinearArgs a{L->w + first * L->ld_w, L->ld_w, L->w_scales + first,
+                       L->bias ? L->bias + first : nullptr, q, ld_q, qs, rows, part.channels,
+                       L->d_in, (char*)y + first * type_size(y_type), bf16, ld_y,
+                       part.splits > 1 ? (int32_t*)ws : nullptr, parts_ld(part.channels)};
+    first += part.channels;
+    if (part.tile < 0) {
+      hipLaunchKernelGGL(linear_stream_kernel, dim3(ceil_div(part.channels, 16)),
+                         dim3(64 * kStreamWaves), 0, s, a);
+      continue;
+    }
+    const Tile8& t = kTiles[part.tile];
+    const int tiles_t = ceil_div(rows, 64 * t.tt);
+    const int tiles = tiles_t * ceil_div(part.channels, 64 * t.tn);
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * part.splits)), dim3(256), 0, s, a,
+                         tiles_t, part.splits);
+    };
+    switch (part.tile) {
+      case 0: go(linear_gemm_kernel<4, 4, 64>); break;
+      case 1: go(linear_gemm_kernel<4, 2, 64>); break;
+      case 2: go(linear_gemm_kernel<2, 2, 128>); break;
+      case 3: go(linear_gemm_kernel<1, 2, 128>); break;
+      default: go(linear_gemm_kernel<1, 1, 128>); break;
+    }
+    if (part.splits > 1)
+      hipLaunchKernelGGL(linear_join_kernel, dim3(ceil_div(part.channels, 1024), rows), dim3(256),
+                         0, s, a, part.splits);
   }
-  const Tile8& t = kTiles[p.tile];
-  const int tiles_t = (rows + 64 * t.tt - 1) / (64 * t.tt);
-  const int tiles_n = (L->n_out + 64 * t.tn - 1) / (64 * t.tn);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_t * tiles_n * p.splits)), dim3(256), 0, s, a,
-                       tiles_t, p.splits);
-  };
-  switch (p.tile) {
-    case 0: go(linear_gemm_kernel<4, 4, 64>); break;
-    case 1: go(linear_gemm_kernel<4, 2, 64>); break;
-    case 2: go(linear_gemm_kernel<2, 2, 64>); break;
-    case 3: go(linear_gemm_kernel<1, 2, 128>); break;
-    default: go(linear_gemm_kernel<1, 1, 128>); break;
-  }
-  if (p.splits > 1)
-    hipLaunchKernelGGL(linear_join_kernel, dim3((L->n_out + 1023) / 1024, rows), dim3(256), 0, s,
-                       a, p.splits);
   return launch_status();
 }
