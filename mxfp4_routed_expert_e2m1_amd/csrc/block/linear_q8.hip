@@ -158,7 +158,12 @@ struct RowsOut {
   int64_t ld;
   int rows, cols;
 };
-template <int TN, typename T>
+typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+
+// STREAM: results of large calls, far more than the L2s hold, are written past
+// them, which leaves the operands there (4096 rows of 14336 x 4096: 239 -> 227
+// us).
+template <int TN, bool STREAM, typename T>
 __device__ inline void store_rows(const RowsOut& o, i32x16 (&c)[TN], int t0, int n0, float qs,
                                   const float* ws, const float* bias, T* buf) {
   constexpr int kCols = 32 * TN, kLd = kCols + 16 / (int)sizeof(T), kPer = 16 / (int)sizeof(T);
@@ -184,6 +189,10 @@ __device__ inline void store_rows(const RowsOut& o, i32x16 (&c)[TN], int t0, int
   const int rows = min(32, o.rows - t0), cols = min(kCols, o.cols - n0);
   T* y = (T*)o.y + uniform((int64_t)t0 * o.ld + n0);
   constexpr int kLanes = kCols / kPer, kPasses = kLanes / 2;  // lanes per row
+  auto store16 = [](T* p, u32x4 x) {
+    if constexpr (STREAM) __builtin_nontemporal_store(x, (any_u32x4*)p);
+    else *(any_u32x4*)p = x;
+  };
   const int col = (lane % kLanes) * kPer, r0 = lane / kLanes;
   u32x4 v[kPasses];
 #pragma unroll
@@ -194,7 +203,7 @@ __device__ inline void store_rows(const RowsOut& o, i32x16 (&c)[TN], int t0, int
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
       if (r0 + i * (64 / kLanes) < rows)
-        __builtin_memcpy(p + (int64_t)(i * (64 / kLanes)) * o.ld, &v[i], 16);
+        store16(p + (int64_t)(i * (64 / kLanes)) * o.ld, v[i]);
   }
   if (cols % kPer && lane < rows) {
     for (int n = cols / kPer * kPer; n < cols; ++n)
@@ -350,11 +359,11 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(LinearArgs a, int tile
     if (a.parts) {
       const RowsOut po{a.parts + split * (a.rows * a.parts_ld), a.parts_ld, a.rows,
                        (int)a.parts_ld};
-      store_rows<TN>(po, cj, t, n, qs, cs, cb, (int32_t*)mine);
+      store_rows<TN, false>(po, cj, t, n, qs, cs, cb, (int32_t*)mine);
     } else if (a.y_bf16) {
-      store_rows<TN>(o, cj, t, n, qs, cs, cb, (__bf16*)mine);
+      store_rows<TN, TT * TN >= 8>(o, cj, t, n, qs, cs, cb, (__bf16*)mine);
     } else {
-      store_rows<TN>(o, cj, t, n, qs, cs, cb, (float*)mine);
+      store_rows<TN, TT * TN >= 8>(o, cj, t, n, qs, cs, cb, (float*)mine);
     }
   }
 }
@@ -587,14 +596,19 @@ static LinearPlan plan(int rows, int n_out, int d_in) {
 
 static int64_t parts_ld(int n_out) { return (n_out + 3) / 4 * 4; }
 
+// Workspace of a plan (a second launch has no splits).
+static size_t plan_bytes(const LinearPlan& p, int rows) {
+  const LinearPart& f = p.part[0];
+  return f.splits > 1 ? (size_t)f.splits * rows * parts_ld(f.channels) * sizeof(int32_t) : 0;
+}
+
 }  // namespace moe
 
 using namespace moe;
 
 extern "C" size_t moe_linear_q8_workspace_bytes(const moe_linear_t* L, int rows) {
   if (linear_check(L) != MOE_OK || rows < 1) return 0;
-  const LinearPart p = plan(rows, L->n_out, L->d_in).part[0];
-  return p.splits > 1 ? (size_t)p.splits * rows * parts_ld(L->n_out) * sizeof(int32_t) : 0;
+  return plan_bytes(plan(rows, L->n_out, L->d_in), rows);
 }
 
 extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_q,
@@ -610,7 +624,7 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
     return MOE_ERR_ALIGNMENT;
   if ((int64_t)((rows + 63) / 64) * ((L->n_out + 63) / 64) > (1ll << 30)) return MOE_ERR_SHAPE;
   const LinearPlan p = plan(rows, L->n_out, L->d_in);
-  const size_t need = moe_linear_q8_workspace_bytes(L, rows);
+  const size_t need = plan_bytes(p, rows);
   if (need > 0) {
     if (!ws) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
