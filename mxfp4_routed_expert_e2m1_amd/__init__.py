@@ -15,7 +15,7 @@ import torch
 
 from . import block
 from .block import (  # noqa: F401
-    Linear, Norm, RouterRule, codes_buffer, moe_linear_q8, moe_linear_q8_workspace_bytes,
+    Linear, Norm, RouteOutputs, RouterRule, codes_buffer, moe_linear_q8, moe_linear_q8_workspace_bytes,
     moe_norm_post, moe_norm_pre, moe_quant_row_q8, moe_route_scored,
     moe_route_scored_workspace_bytes, route_outputs)
 

@@ -245,14 +245,29 @@ class RouterRule:
         self.ref = C.byref(self.c)
 
 
+class RouteOutputs(tuple):
+    """Buffers (ids, w, counts, offsets, sorted) of a routing call, checked once, for callers that
+    keep them: five tensors' checks are a fifth of a decode call's host time."""
+
+    def __new__(cls, ids, w, counts, offsets, srt):
+        self = super().__new__(cls, (ids, w, counts, offsets, srt))
+        rows, k = ids.shape
+        E, i32 = counts.numel(), torch.int32
+        self.key = (rows, E, k)
+        self.ptrs = (_vec("ids", ids, rows * k, i32), _vec("w", w, rows * k),
+                     _vec("counts", counts, E, i32), _vec("offsets", offsets, E + 1, i32),
+                     _vec("sorted", srt, rows * k, i32, least=True))
+        return self
+
+
 def route_outputs(rows, n_experts, top_k, device="cuda"):
-    """Buffers (ids, w, counts, offsets, sorted) of a routing call."""
+    """New buffers for a routing call."""
     i32 = torch.int32
-    return (torch.empty((rows, top_k), dtype=i32, device=device),
-            torch.empty((rows, top_k), dtype=torch.float32, device=device),
-            torch.empty(n_experts, dtype=i32, device=device),
-            torch.empty(n_experts + 1, dtype=i32, device=device),
-            torch.empty(rows * top_k, dtype=i32, device=device))
+    return RouteOutputs(torch.empty((rows, top_k), dtype=i32, device=device),
+                        torch.empty((rows, top_k), dtype=torch.float32, device=device),
+                        torch.empty(n_experts, dtype=i32, device=device),
+                        torch.empty(n_experts + 1, dtype=i32, device=device),
+                        torch.empty(rows * top_k, dtype=i32, device=device))
 
 
 def moe_route_scored_workspace_bytes(rule, rows):
@@ -269,15 +284,15 @@ def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
         raise ValueError(f"logits: {logits.shape[1]} columns, the rule has {E} experts")
     if out is None:
         out = route_outputs(rows, E, k, logits.device)
-    ids, w, counts, offsets, srt = out
-    i32, n = torch.int32, rows * k
-    ptrs = (_vec("ids", ids, n, i32), _vec("w", w, n), _vec("counts", counts, E, i32),
-            _vec("offsets", offsets, E + 1, i32), _vec("sorted", srt, n, i32, least=True))
+    elif type(out) is not RouteOutputs:
+        out = RouteOutputs(*out)
+    if out.key != (rows, E, k):
+        raise ValueError(f"out: buffers of {out.key} rows, experts and picks, need {(rows, E, k)}")
     if ws is None:
         ws = torch.empty(moe_route_scored_workspace_bytes(rule, rows), dtype=torch.uint8,
                          device=logits.device)
     rc = (_lib or _load()).moe_route_scored(
-        rule.ref, *la, rows, *ptrs, ws.data_ptr(), ws.numel(),
+        rule.ref, *la, rows, *out.ptrs, ws.data_ptr(), ws.numel(),
         stream.cuda_stream if stream else _raw_stream(logits.get_device()))
     if rc:
         _fail("moe_route_scored", rc)

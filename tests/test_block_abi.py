@@ -186,3 +186,5 @@ def test_python_argument_checks():
         m.moe_route_scored(m.RouterRule(8, 2), x.double())
     with pytest.raises(TypeError):
         m.moe_quant_row_q8(x.double())
+    with pytest.raises(ValueError):
+        m.route_outputs(4, 8, 2, device="cpu")
