@@ -34,6 +34,7 @@ struct NormArgs {
   const void* x;  // the rows to normalise: x before a block, y after one
   int64_t ld_x;
   int cols;
+  double inv_cols;
   // after a block
   int post_norm;
   float eps, res_scale;
@@ -49,26 +50,43 @@ struct NormArgs {
   NormOut o;
 };
 
-// Sum (or maximum of values >= 0) over the workgroup of up to 16 waves, in
-// every lane; `slots` is LDS of one float per wave, not shared with another
-// reduction of the same row.
-template <typename Op>
-__device__ inline float over_waves(float v, float* slots, Op op) {
+// Sum over the workgroup of up to 16 waves, in every lane; `slots` is LDS of one
+// value per wave, not shared with another reduction of the same row.  A
+// thread's and a 16-lane row's part are added in fp32, whose errors average
+// out over the row's many parts; the last additions, whose errors would stay,
+// in fp64.
+__device__ inline double wg_sum(float v, double* slots) {
+  v += dpp_mov<0xB1>(v);   // quad_perm [1,0,3,2]
+  v += dpp_mov<0x4E>(v);   // quad_perm [2,3,0,1]
+  v += dpp_mov<0x141>(v);  // row_half_mirror
+  v += dpp_mov<0x140>(v);  // row_mirror
+  auto lane_value = [&](int l) {
+    return (double)__builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+  };
+  double s = (lane_value(0) + lane_value(16)) + (lane_value(32) + lane_value(48));
+  const int waves = blockDim.x >> 6, lane = lane_id();
+  if (waves == 1) return s;
+  if (lane == 0) slots[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = (lane & 15) < waves ? slots[lane & 15] : 0.;
+  s += dpp_f64<0xB1>(s);
+  s += dpp_f64<0x4E>(s);
+  s += dpp_f64<0x141>(s);
+  return s + dpp_f64<0x140>(s);
+}
+// Maximum of values >= 0, likewise.
+__device__ inline float wg_max(float v, float* slots) {
+  v = wave_max(v);
   const int waves = blockDim.x >> 6, lane = lane_id();
   if (waves == 1) return v;
   if (lane == 0) slots[threadIdx.x >> 6] = v;
   __syncthreads();
   v = (lane & 15) < waves ? slots[lane & 15] : 0.f;
-  v = op(v, dpp_mov<0xB1>(v));   // quad_perm [1,0,3,2]
-  v = op(v, dpp_mov<0x4E>(v));   // quad_perm [2,3,0,1]
-  v = op(v, dpp_mov<0x141>(v));  // row_half_mirror
-  return op(v, dpp_mov<0x140>(v));  // row_mirror
-}
-__device__ inline float wg_sum(float v, float* slots) {
-  return over_waves(wave_sum(v), slots, [](float a, float b) { return a + b; });
-}
-__device__ inline float wg_max(float v, float* slots) {
-  return over_waves(wave_max(v), slots, [](float a, float b) { return fmaxf(a, b); });
+  v = fmaxf(v, dpp_mov<0xB1>(v));
+  v = fmaxf(v, dpp_mov<0x4E>(v));
+  v = fmaxf(v, dpp_mov<0x141>(v));
+  return fmaxf(v, dpp_mov<0x140>(v));
 }
 
 // WHOLE: the row is a whole number of units
@@ -91,6 +109,18 @@ __device__ inline void store_unit(T* row, int e, int cols, const float (&v)[8]) 
     for (int i = 0; i < 8; ++i)
       if (e + i < cols) row[e + i] = t[i];
   }
+}
+
+// a x + b y, each operation rounded by itself
+__device__ inline float scaled_sum(float a, float x, float b, float y) {
+#pragma clang fp contract(off)
+  return a * x + b * y;
+}
+
+// 1 / rms of a row from the sum of its squares (the hardware's root, one step
+// of the last place)
+__device__ inline float inverse_rms(double ss, double inv_cols, float eps) {
+  return rsqrtf((float)(ss * inv_cols) + eps);
 }
 
 // the value an element keeps once it is stored in T
@@ -165,7 +195,8 @@ __device__ inline void finish_row(float (&v)[U][8], const Raw8<float> (&rw)[U], 
 // memory round trip and two reductions, not one round trip per operand.
 template <typename XT, int U, bool WHOLE>
 __global__ __launch_bounds__(1024) void norm_pre_kernel(NormArgs a) {
-  __shared__ float slots[2][16];
+  __shared__ double sums[16];
+  __shared__ float slots[16];
   const int row = blockIdx.x, cols = a.cols;
   const XT* x = (const XT*)a.x + (int64_t)row * a.ld_x;
   Raw8<XT> raw[U];
@@ -183,13 +214,14 @@ __global__ __launch_bounds__(1024) void norm_pre_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(v[u][i], v[u][i], ss);
   }
-  const float r = 1.0f / sqrtf(wg_sum(ss, slots[0]) / (float)cols + a.o.eps);
-  finish_row<U, WHOLE>(v, rw, row, cols, r, a.o, slots[1]);
+  const float r = inverse_rms(wg_sum(ss, sums), a.inv_cols, a.o.eps);
+  finish_row<U, WHOLE>(v, rw, row, cols, r, a.o, slots);
 }
 
 template <typename XT, typename RT, int U, bool WHOLE>
 __global__ __launch_bounds__(1024) void norm_post_kernel(NormArgs a) {
-  __shared__ float slots[3][16];
+  __shared__ double sums[2][16];
+  __shared__ float slots[16];
   const int row = blockIdx.x, cols = a.cols, threads = blockDim.x;
   const XT* x = (const XT*)a.x + (int64_t)row * a.ld_x;
   const RT* res = (const RT*)a.res + (int64_t)row * a.ld_res;
@@ -223,7 +255,7 @@ __global__ __launch_bounds__(1024) void norm_post_kernel(NormArgs a) {
     for (int i = 0; i < 8; ++i) ss = fmaf(v[u][i], v[u][i], ss);
   }
   float r = 1.f;
-  if (a.post_norm) r = 1.0f / sqrtf(wg_sum(ss, slots[0]) / (float)cols + a.eps);
+  if (a.post_norm) r = inverse_rms(wg_sum(ss, sums[0]), a.inv_cols, a.eps);
   ss = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -237,7 +269,7 @@ __global__ __launch_bounds__(1024) void norm_post_kernel(NormArgs a) {
     for (int i = 0; i < 8; ++i) {
       if (a.post_norm) v[u][i] = a.w ? v[u][i] * r * w[i] : v[u][i] * r;
       const float gi = !wide ? g1 : gate_f32 ? g[i] : gh[i];
-      v[u][i] = fmaf(a.res_scale, s[i], gi * v[u][i]);
+      v[u][i] = scaled_sum(a.res_scale, s[i], gi, v[u][i]);
     }
     store_unit<WHOLE>((RT*)a.out + (int64_t)row * a.ld_out, e, cols, v[u]);
     if (a.has_next) {
@@ -249,8 +281,8 @@ __global__ __launch_bounds__(1024) void norm_post_kernel(NormArgs a) {
     }
   }
   if (!a.has_next) return;
-  r = 1.0f / sqrtf(wg_sum(ss, slots[1]) / (float)cols + a.o.eps);
-  finish_row<U, WHOLE>(v, rn, row, cols, r, a.o, slots[2]);
+  r = inverse_rms(wg_sum(ss, sums[1]), a.inv_cols, a.o.eps);
+  finish_row<U, WHOLE>(v, rn, row, cols, r, a.o, slots);
 }
 
 // Row quantiser: a row of up to 8 kThreads U elements is held in registers;
@@ -402,6 +434,7 @@ extern "C" int moe_norm_pre(const moe_norm_t* N, const void* x, int x_type, int6
   a.x = x;
   a.ld_x = ld_x;
   a.cols = cols;
+  a.inv_cols = 1.0 / cols;
   a.o = o;
   hipStream_t s = (hipStream_t)stream;
   if (x_type == MOE_TYPE_F32) launch_pre<float>(a, rows, s);
@@ -439,7 +472,7 @@ extern "C" int moe_norm_post(const moe_norm_t* N, const void* y, int y_type, int
     if (rc != MOE_OK) return rc;
   }
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
-  NormArgs a{y, ld_y, cols, N->post_norm, N->eps, N->residual_scale, N->post_w, res, ld_res,
+  NormArgs a{y, ld_y, cols, 1.0 / cols, N->post_norm, N->eps, N->residual_scale, N->post_w, res, ld_res,
              gate, gate_type, gate_row, gate_col, out, ld_out, next != nullptr, o};
   hipStream_t s = (hipStream_t)stream;
   const bool yf = y_type == MOE_TYPE_F32, rf = res_type == MOE_TYPE_F32;

@@ -2,8 +2,8 @@
 
 Tolerance.  A row's sum of squares is at most 32 fused steps in a thread, 6
 over a wave and 16 over the waves, so its relative error is below 54 2^-24 and
-its inverse root's below 27 2^-24; mean, root, reciprocal and the three
-products add at most 8 more: |h - ref| <= 40 2^-24 |ref|.  A block's result
+its inverse root's below 27 2^-24; mean, root and the three products add at
+most 8 more: |h - ref| <= 40 2^-24 |ref|.  A block's result
 b carries that too, and out = rs res + g b at most two roundings of its own:
 |out - ref| <= 48 2^-24 (|rs res| + |g b|).  A bf16 result adds half a step,
 at most 2^-8 of its value (2^-134 among the subnormals).
