@@ -129,6 +129,33 @@ __device__ inline float stored(float v) {
   return (float)(T)v;
 }
 
+// The codes of 8 values for a row's scale d, little-endian: rint(v / d) within
+// +-127, 0 for d = 0.  The quotient by way of the reciprocal is off by less
+// than 127 * 3 * 2^-24 < 2^-15, so it rounds to the same code unless it lies
+// within 2^-12 of a midpoint; a wave that holds such a value (or a scale whose
+// reciprocal is not safe) divides.  4096 rows of 4096 bf16: 14.8 -> 12.9 us.
+__device__ inline u32x2 row_codes(const float (&v)[8], float d) {
+  const float inv = 1.0f / d;
+  const bool safe = d > 0x1p-100f && d < 0x1p100f;
+  float q[8];
+  bool near = !safe;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = v[i] * inv;
+    q[i] = rintf(t);
+    near |= fabsf(t - q[i]) > 0.5f - 0x1p-12f;
+  }
+  if (__any(near)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = q8_code(v[i], d);
+  }
+  u32x2 w = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i >> 2] |= ((uint32_t)(int32_t)q[i] & 0xFFu) << (8 * (i & 3));
+  return w;
+}
+
 // One row's h = v * r * w from its values in registers, with its codes.
 template <int U, bool WHOLE>
 __device__ inline void finish_row(float (&v)[U][8], const Raw8<float> (&rw)[U], int row, int cols,
@@ -175,12 +202,9 @@ __device__ inline void finish_row(float (&v)[U][8], const Raw8<float> (&rw)[U], 
       const int e = 8 * (u * threads + (int)threadIdx.x);
       if (e >= cols) continue;
       int8_t* q = o.q + (int64_t)row * o.ld_q + e;
-      uint32_t w[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i >> 2] |= ((uint32_t)(int32_t)q8_code(v[u][i], d) & 0xFFu) << (8 * (i & 3));
+      const u32x2 w = row_codes(v[u], d);
       if (e + 8 <= cols) {
-        *(u32x2*)q = u32x2{w[0], w[1]};
+        *(u32x2*)q = w;
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -315,12 +339,9 @@ __global__ __launch_bounds__(kQuantThreads) void quant_row_kernel(const XT* x0, 
   }
   const float d = wg_max(amax, slots) / 127.0f;
   auto write = [&](int e) {
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= ((uint32_t)(int32_t)q8_code(v[i], d) & 0xFFu) << (8 * (i & 3));
+    const u32x2 w = row_codes(v, d);
     if (e + 8 <= cols) {
-      *(u32x2*)(q + e) = u32x2{w[0], w[1]};
+      *(u32x2*)(q + e) = w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -494,7 +515,9 @@ extern "C" int moe_quant_row_q8(const void* x, int x_type, int64_t ld_x, int row
     return MOE_ERR_ALIGNMENT;
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
   const int n = (cols + 7) / 8;
-  const int threads = min(kQuantThreads, (n + 63) / 64 * 64);
+  // (two units per thread keep more loads on their way: 4096 rows of 4096 bf16
+  // 15.7 -> 12.9 us)
+  const int threads = min(kQuantThreads, ((n + 1) / 2 + 63) / 64 * 64);
   hipStream_t s = (hipStream_t)stream;
   auto go = [&](auto kernel, auto* p) {
     hipLaunchKernelGGL(kernel, dim3(rows), dim3(threads), 0, s, p, ld_x, cols, q, ld_q, scales);

@@ -232,3 +232,20 @@ def test_quant_rows_bit_exact(rows, cols, pad, dtype):
     qr, sr = ref.quant_rows(x.float().cpu().numpy())
     assert np.array_equal(q.cpu().numpy(), qr) and np.array_equal(s.cpu().numpy(), sr)
     assert (buf[:, cols:] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_quant_rows_at_midpoints_and_extreme_scales(dtype):
+    """Values on and one step beside every midpoint between codes, and rows whose
+    scale is subnormal, tiny, huge or infinite in its reciprocal."""
+    half = torch.arange(-126, 127, dtype=torch.float64) + 0.5
+    row = torch.cat([half, torch.tensor([127.0])]).float()
+    up, down = (torch.nextafter(row, torch.tensor(s)) for s in (np.inf, -np.inf))
+    up[-1] = down[-1] = 127.0
+    x = torch.stack([row, up, down]).to(DEV)
+    rows = [x * 2.0**p for p in (0, -3, 40, -60, -99, -101, -130, -142, -148, 90, 99, 101, 120)]
+    rows += [x * f for f in (1.1, 0.3, 7.7, 3e-20)]
+    x = torch.cat(rows).to(dtype)
+    q, s = m.moe_quant_row_q8(x)
+    qr, sr = ref.quant_rows(x.float().cpu().numpy())
+    assert np.array_equal(s.cpu().numpy(), sr) and np.array_equal(q.cpu().numpy(), qr)
