@@ -2,10 +2,11 @@
 // balance bias for the choice alone, expert groups, top-k, weights, and the
 // stable grouping by expert.
 //
-// One wave per row.  Expert e sits in lane e % 64, slot e / 64, as an
-// order-preserving integer key (0: out of reach or already picked), so the
-// choice is a wave maximum per round and the lowest lane of the lowest slot
-// holding it, which is the lowest expert among equals.
+// One wave per row.  A lane holds PER_LANE consecutive experts as
+// order-preserving integer keys (0: out of reach or already picked), so a round
+// is each lane's first largest key, the wave's maximum, and the first lane that
+// holds it: the lowest expert among equals.  A row's time is this chain of
+// dependent steps, 0.2 us a round.
 //
 // Grouping.  An expert takes a row at most once, so the rows that chose it are
 // a bit set: an assignment's place among its expert's is the number of
@@ -42,9 +43,59 @@ struct RuleArgs {
   int32_t* sorted;
 };
 
+// exp_rows (the same operations on the same values, so the same bits) without
+// a branch: a lane's several scores are computed side by side.
+__device__ inline float exp_flat(float x) {
+  const float c = fminf(fmaxf(x, -104.0f), 89.0f);
+  const float k = rintf(c * 0x1.715476p+0f);
+  float r = fmaf(-k, 0x1.62e4p-1f, c);
+  r = fmaf(-k, 0x1.7f7d1cp-20f, r);
+  float p = 0x1.a01a02p-13f;
+  p = fmaf(p, r, 0x1.6c16c2p-10f);
+  p = fmaf(p, r, 0x1.111112p-7f);
+  p = fmaf(p, r, 0x1.555556p-5f);
+  p = fmaf(p, r, 0x1.555556p-3f);
+  p = fmaf(p, r, 0x1p-1f);
+  p = fmaf(p, r, 1.0f);
+  p = fmaf(p, r, 1.0f);
+  const float e = ldexpf(p, (int)k);
+  return x > 89.0f ? __builtin_inff() : x >= -104.0f ? e : 0.0f;
+}
+
 template <int CTRL>
 __device__ inline uint32_t dpp_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
+}
+
+// Maximum over the wave, wave-uniform.  (Lanes that a step does not reach take
+// part with 0, the least key, so that each step is one instruction.)
+template <int CTRL, int ROWS>
+__device__ inline uint32_t max_step(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, true));
+}
+__device__ inline uint32_t wave_max_key(uint32_t v) {
+  v = max_step<0xB1, 0xF>(v);   // quad_perm [1,0,3,2]
+  v = max_step<0x4E, 0xF>(v);   // quad_perm [2,3,0,1]
+  v = max_step<0x141, 0xF>(v);  // row_half_mirror
+  v = max_step<0x140, 0xF>(v);  // row_mirror
+  v = max_step<0x142, 0xA>(v);  // row_bcast:15 into rows 1, 3
+  v = max_step<0x143, 0xC>(v);  // row_bcast:31 into rows 2, 3
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// A lane's experts e0.. of a row of E, as floats, in one load where all are in
+// the row; 0 past it.
+template <int N, typename T>
+__device__ inline void load_lane(const T* row, int e0, int E, float (&v)[N]) {
+  T t[N];
+  if (e0 + N <= E) {
+    __builtin_memcpy(t, row + e0, sizeof(t));
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = e0 + j < E ? row[e0 + j] : (T)0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = (float)t[j];
 }
 
 // The picks of one row: lane s < top_k gets pick s (-1: none left) and its
@@ -52,24 +103,19 @@ __device__ inline uint32_t dpp_u32(uint32_t v) {
 template <int PER_LANE>
 __device__ inline void choose_row(const RuleArgs& p, int row, uint32_t* lds, int* my_id,
                                   float* my_w) {
-  const int lane = lane_id(), E = p.n_experts;
+  const int lane = lane_id(), E = p.n_experts, e0 = PER_LANE * lane;
   float l[PER_LANE], s[PER_LANE], b[PER_LANE];
-  if (p.l_type == MOE_TYPE_F32) {
-    const float* r = (const float*)p.logits + (int64_t)row * p.ld_l;
+  if (p.l_type == MOE_TYPE_F32)
+    load_lane<PER_LANE>((const float*)p.logits + (int64_t)row * p.ld_l, e0, E, l);
+  else
+    load_lane<PER_LANE>((const __bf16*)p.logits + (int64_t)row * p.ld_l, e0, E, l);
 #pragma unroll
-    for (int j = 0; j < PER_LANE; ++j) l[j] = r[min(lane + 64 * j, E - 1)];
-  } else {
-    const __bf16* r = (const __bf16*)p.logits + (int64_t)row * p.ld_l;
-#pragma unroll
-    for (int j = 0; j < PER_LANE; ++j) l[j] = (float)r[min(lane + 64 * j, E - 1)];
-  }
-#pragma unroll
-  for (int j = 0; j < PER_LANE; ++j)
-    b[j] = p.bias ? p.bias[min(lane + 64 * j, E - 1)] : 0.f;
+  for (int j = 0; j < PER_LANE; ++j) b[j] = 0.f;
+  if (p.bias) load_lane<PER_LANE>(p.bias, e0, E, b);
   bool in[PER_LANE];
 #pragma unroll
   for (int j = 0; j < PER_LANE; ++j)
-    in[j] = lane + 64 * j < E && l[j] > -__builtin_inff();  // not NaN either
+    in[j] = e0 + j < E && l[j] > -__builtin_inff();  // not NaN either
   if (p.score == MOE_SCORE_SOFTMAX) {
     float m = -__builtin_inff();
 #pragma unroll
@@ -80,15 +126,22 @@ __device__ inline void choose_row(const RuleArgs& p, int row, uint32_t* lds, int
 #pragma unroll
     for (int j = 0; j < PER_LANE; ++j) {
       // (an infinite maximum: its holders share, the others get 0)
-      s[j] = !in[j] ? 0.f : l[j] == m ? 1.f : exp_rows(l[j] - m);
+      const float e = exp_flat(l[j] - m);
+      s[j] = !in[j] ? 0.f : l[j] == m ? 1.f : e;
       sum += s[j];
     }
-    sum = wave_sum(sum);
+    sum = wave_sum(sum);  // (0 where no expert is in reach: the quotients are not used)
 #pragma unroll
-    for (int j = 0; j < PER_LANE; ++j) s[j] = in[j] ? s[j] / sum : 0.f;
+    for (int j = 0; j < PER_LANE; ++j) {
+      const float q = s[j] / sum;
+      s[j] = in[j] ? q : 0.f;
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < PER_LANE; ++j) s[j] = in[j] ? 1.0f / (1.0f + exp_rows(-l[j])) : 0.f;
+    for (int j = 0; j < PER_LANE; ++j) {
+      const float q = 1.0f / (1.0f + exp_flat(-l[j]));
+      s[j] = in[j] ? q : 0.f;
+    }
   }
   uint32_t k[PER_LANE];
 #pragma unroll
@@ -96,7 +149,7 @@ __device__ inline void choose_row(const RuleArgs& p, int row, uint32_t* lds, int
 
   if (p.n_groups > 1 && p.top_groups < p.n_groups) {
 #pragma unroll
-    for (int j = 0; j < PER_LANE; ++j) lds[lane + 64 * j] = k[j];
+    for (int j = 0; j < PER_LANE; ++j) lds[e0 + j] = k[j];
     __builtin_amdgcn_wave_barrier();
     // group g's lanes are g << lanes_log2 on; each reads every 2^lanes_log2-th
     // member, four at a time, then the lanes' two largest are merged
@@ -137,35 +190,31 @@ __device__ inline void choose_row(const RuleArgs& p, int row, uint32_t* lds, int
     const uint64_t stays = __ballot(g < p.n_groups && gk != 0 && before < p.top_groups);
 #pragma unroll
     for (int j = 0; j < PER_LANE; ++j) {
-      const uint32_t mine = ((uint32_t)(lane + 64 * j) * p.group_inv) >> 20;
+      const uint32_t mine = ((uint32_t)(e0 + j) * p.group_inv) >> 20;
       if (mine >= (uint32_t)p.n_groups || !((stays >> (mine << p.lanes_log2)) & 1)) k[j] = 0u;
     }
   }
 
   // the scores wait in LDS for the picks
 #pragma unroll
-  for (int j = 0; j < PER_LANE; ++j) lds[lane + 64 * j] = __builtin_bit_cast(uint32_t, s[j]);
+  for (int j = 0; j < PER_LANE; ++j) lds[e0 + j] = __builtin_bit_cast(uint32_t, s[j]);
   int id = -1;
   for (int r = 0; r < p.top_k; ++r) {
-    uint32_t lm = k[0];
+    uint32_t most = k[0];
+    int at = 0;
 #pragma unroll
-    for (int j = 1; j < PER_LANE; ++j) lm = max(lm, k[j]);
-    const uint32_t bk = wave_max_u32(lm);
-    if (bk == 0u) break;  // none left: the remaining slots keep -1
-    int slot = 0;
-    uint64_t holders = 0;
-#pragma unroll
-    for (int j = PER_LANE - 1; j >= 0; --j) {
-      const uint64_t m = __ballot(k[j] == bk);
-      slot = m != 0ull ? j : slot;
-      holders = m != 0ull ? m : holders;
+    for (int j = 1; j < PER_LANE; ++j) {
+      at = k[j] > most ? j : at;
+      most = max(most, k[j]);
     }
-    const int first = __ffsll((unsigned long long)holders) - 1;
-    const bool here = lane == first;
+    const uint32_t best = wave_max_key(most);
+    if (best == 0u) break;  // none left: the remaining slots keep -1
+    const int first = __ffsll((unsigned long long)__ballot(most == best)) - 1;
+    const int pick = PER_LANE * first + __builtin_amdgcn_readlane(at, first);
+    const int gone = lane == first ? at : -1;
 #pragma unroll
-    for (int j = 0; j < PER_LANE; ++j)
-      if (here && slot == j) k[j] = 0u;
-    if (lane == r) id = 64 * slot + first;
+    for (int j = 0; j < PER_LANE; ++j) k[j] = gone == j ? 0u : k[j];
+    id = lane == r ? pick : id;
   }
   __builtin_amdgcn_wave_barrier();
   float w = id >= 0 ? __builtin_bit_cast(float, lds[id]) : 0.f;
