@@ -425,8 +425,10 @@ typedef struct moe_norm {
  * order set by d_model alone, so a row's bits do not depend on the rows that
  * share a call, on strides or on alignment; |x| up to 2^56 does not
  * overflow.  A row with an infinity or a NaN gives what the formula gives,
- * for that row alone.  Rows need no alignment beyond their elements' (16
- * bytes and d_model % 8 == 0 are the fast form).  rows == 0 is a no-op. */
+ * for that row alone, and its MOE_QUANT_ROW scale is NaN (MOE_QUANT_BLOCK:
+ * outside the contract, as in moe_quant_act_q8).  Rows need no alignment
+ * beyond their elements' (16 bytes and d_model % 8 == 0 are the fast form).
+ * rows == 0 is a no-op. */
 int moe_norm_pre(const moe_norm_t* N, const void* x, int x_type, int64_t ld_x, int rows,
                  void* h, int h_type, int64_t ld_h, int quant, int8_t* q, int64_t ld_q,
                  float* qs, int64_t ld_qs, void* stream);
@@ -506,7 +508,9 @@ int moe_route_scored(const moe_router_rule_t* R, const void* logits, int l_type,
  *   x      f32/bf16 [rows][ld_x] (device)
  *   q      int8 [rows][ld_q] (device, 8-byte aligned, ld_q % 8 == 0)
  *   scales f32 [rows] (device)
- * cols >= 1; rows == 0 is a no-op.  NaN/Inf inputs are outside the contract. */
+ * cols >= 1; rows == 0 is a no-op.  A row with a NaN has a NaN scale, one
+ * with an infinity an infinite or NaN scale, and codes of no meaning; other
+ * rows are not affected. */
 int moe_quant_row_q8(const void* x, int x_type, int64_t ld_x, int rows, int cols, int8_t* q,
                      int64_t ld_q, float* scales, void* stream);
 

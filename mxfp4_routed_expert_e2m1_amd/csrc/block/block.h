@@ -84,6 +84,4 @@ __device__ inline double dpp_f64(double v) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-int norm_args_check(const moe_norm_t* N);
-
 }  // namespace moe

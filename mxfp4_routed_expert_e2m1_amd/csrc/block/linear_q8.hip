@@ -594,6 +594,11 @@ static LinearPlan plan(int rows, int n_out, int d_in) {
   return best;
 }
 
+static int64_t part_tiles(const LinearPart& p, int rows) {
+  const Tile8& t = kTiles[p.tile];
+  return (int64_t)ceil_div(rows, 64 * t.tt) * ceil_div(p.channels, 64 * t.tn);
+}
+
 static int64_t parts_ld(int n_out) { return (n_out + 3) / 4 * 4; }
 
 // Workspace of a plan (a second launch has no splits).
@@ -622,8 +627,9 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
   if (ld_q < L->d_in || ld_y < L->n_out || ld_q > kMaxLd || ld_y > kMaxLd) return MOE_ERR_STRIDE;
   if (!aligned(q, 16) || ld_q % 16 != 0 || !aligned(qs, 4) || !aligned(y, type_size(y_type)))
     return MOE_ERR_ALIGNMENT;
-  if ((int64_t)((rows + 63) / 64) * ((L->n_out + 63) / 64) > (1ll << 30)) return MOE_ERR_SHAPE;
   const LinearPlan p = plan(rows, L->n_out, L->d_in);
+  for (int i = 0; i < p.n_parts; ++i)  // (a launch takes fewer than 2^32 threads)
+    if (p.part[i].tile >= 0 && part_tiles(p.part[i], rows) >= 1 << 24) return MOE_ERR_SHAPE;
   const size_t need = plan_bytes(p, rows);
   if (need > 0) {
     if (!ws) return MOE_ERR_INVALID_ARG;
@@ -646,9 +652,8 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
                          dim3(64 * kStreamWaves), 0, s, a);
       continue;
     }
-    const Tile8& t = kTiles[part.tile];
-    const int tiles_t = ceil_div(rows, 64 * t.tt);
-    const int tiles = tiles_t * ceil_div(part.channels, 64 * t.tn);
+    const int tiles_t = ceil_div(rows, 64 * kTiles[part.tile].tt);
+    const int tiles = (int)part_tiles(part, rows);
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * part.splits)), dim3(256), 0, s, a,
                          tiles_t, part.splits);

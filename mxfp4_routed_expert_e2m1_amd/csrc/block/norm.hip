@@ -31,6 +31,7 @@ struct NormOut {
 };
 
 struct NormArgs {
+  int row0;       // of the launch
   const void* x;  // the rows to normalise: x before a block, y after one
   int64_t ld_x;
   int cols;
@@ -75,18 +76,24 @@ __device__ inline double wg_sum(float v, double* slots) {
   s += dpp_f64<0x141>(s);
   return s + dpp_f64<0x140>(s);
 }
-// Maximum of values >= 0, likewise.
-__device__ inline float wg_max(float v, float* slots) {
-  v = wave_max(v);
+// Largest magnitude of the workgroup, likewise, from the bits of |v|: their
+// order is that of the numbers, with a NaN above them all, so a row that holds
+// one has a NaN scale (a floating-point maximum would drop it).
+__device__ inline uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+template <int CTRL>
+__device__ inline uint32_t max_moved(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false));
+}
+__device__ inline float wg_max(uint32_t v, uint32_t* slots) {
+  v = wave_max_u32(v);
   const int waves = blockDim.x >> 6, lane = lane_id();
-  if (waves == 1) return v;
-  if (lane == 0) slots[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = (lane & 15) < waves ? slots[lane & 15] : 0.f;
-  v = fmaxf(v, dpp_mov<0xB1>(v));
-  v = fmaxf(v, dpp_mov<0x4E>(v));
-  v = fmaxf(v, dpp_mov<0x141>(v));
-  return fmaxf(v, dpp_mov<0x140>(v));
+  if (waves > 1) {
+    if (lane == 0) slots[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = (lane & 15) < waves ? slots[lane & 15] : 0u;
+    v = max_moved<0x140>(max_moved<0x141>(max_moved<0x4E>(max_moved<0xB1>(v))));
+  }
+  return __uint_as_float(v);
 }
 
 // WHOLE: the row is a whole number of units
@@ -159,10 +166,10 @@ __device__ inline u32x2 row_codes(const float (&v)[8], float d) {
 // One row's h = v * r * w from its values in registers, with its codes.
 template <int U, bool WHOLE>
 __device__ inline void finish_row(float (&v)[U][8], const Raw8<float> (&rw)[U], int row, int cols,
-                                  float r, const NormOut& o, float* slots) {
+                                  float r, const NormOut& o, uint32_t* slots) {
   const int threads = blockDim.x;
   const bool h_bf16 = o.h != nullptr && o.h_type == MOE_TYPE_BF16;
-  float amax = 0.f;
+  uint32_t amax = 0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int e = 8 * (u * threads + (int)threadIdx.x);
@@ -191,12 +198,11 @@ __device__ inline void finish_row(float (&v)[U][8], const Raw8<float> (&rw)[U], 
     } else if (o.quant == MOE_QUANT_ROW) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (e + i < cols) amax = fmaxf(amax, fabsf(v[u][i]));
+        if (e + i < cols) amax = max(amax, magnitude(v[u][i]));
     }
   }
   if (o.quant == MOE_QUANT_ROW) {
-    amax = wg_max(amax, slots);
-    const float d = amax / 127.0f;
+    const float d = wg_max(amax, slots) / 127.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int e = 8 * (u * threads + (int)threadIdx.x);
@@ -220,8 +226,8 @@ __device__ inline void finish_row(float (&v)[U][8], const Raw8<float> (&rw)[U], 
 template <typename XT, int U, bool WHOLE>
 __global__ __launch_bounds__(1024) void norm_pre_kernel(NormArgs a) {
   __shared__ double sums[16];
-  __shared__ float slots[16];
-  const int row = blockIdx.x, cols = a.cols;
+  __shared__ uint32_t slots[16];
+  const int row = a.row0 + (int)blockIdx.x, cols = a.cols;
   const XT* x = (const XT*)a.x + (int64_t)row * a.ld_x;
   Raw8<XT> raw[U];
   Raw8<float> rw[U] = {};
@@ -245,8 +251,8 @@ __global__ __launch_bounds__(1024) void norm_pre_kernel(NormArgs a) {
 template <typename XT, typename RT, int U, bool WHOLE>
 __global__ __launch_bounds__(1024) void norm_post_kernel(NormArgs a) {
   __shared__ double sums[2][16];
-  __shared__ float slots[16];
-  const int row = blockIdx.x, cols = a.cols, threads = blockDim.x;
+  __shared__ uint32_t slots[16];
+  const int row = a.row0 + (int)blockIdx.x, cols = a.cols, threads = blockDim.x;
   const XT* x = (const XT*)a.x + (int64_t)row * a.ld_x;
   const RT* res = (const RT*)a.res + (int64_t)row * a.ld_res;
   const bool wide = a.gate && a.gate_col;  // a gate for each element
@@ -317,12 +323,13 @@ template <typename XT, bool WHOLE>
 __global__ __launch_bounds__(kQuantThreads) void quant_row_kernel(const XT* x0, int64_t ld_x,
                                                                   int cols, int8_t* q0,
                                                                   int64_t ld_q, float* scales) {
-  __shared__ float slots[16];
+  __shared__ uint32_t slots[16];
   const int row = blockIdx.x, threads = blockDim.x, stride = 8 * threads;
   const XT* x = x0 + (int64_t)row * ld_x;
   int8_t* q = q0 + (int64_t)row * ld_q;
   Raw8<XT> raw[kQuantUnits];
-  float amax = 0.f, v[8];
+  uint32_t amax = 0;
+  float v[8];
 #pragma unroll
   for (int u = 0; u < kQuantUnits; ++u)
     raw[u] = load_unit<WHOLE>(x, 8 * (u * threads + (int)threadIdx.x), cols);
@@ -330,12 +337,12 @@ __global__ __launch_bounds__(kQuantThreads) void quant_row_kernel(const XT* x0, 
   for (int u = 0; u < kQuantUnits; ++u) {
     to_f32(raw[u], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(v[i]));
   }
   for (int e = kQuantUnits * stride + 8 * (int)threadIdx.x; e < cols; e += stride) {
     to_f32(load_unit<WHOLE>(x, e, cols), v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(v[i]));
   }
   const float d = wg_max(amax, slots) / 127.0f;
   auto write = [&](int e) {
@@ -363,7 +370,7 @@ __global__ __launch_bounds__(kQuantThreads) void quant_row_kernel(const XT* x0, 
 }
 
 // ------------------------------------------------------------- host side
-int norm_args_check(const moe_norm_t* N) {
+static int norm_args_check(const moe_norm_t* N) {
   if (!N) return MOE_ERR_INVALID_ARG;
   if (N->d_model < 1 || N->d_model > kMaxNormCols) return MOE_ERR_SHAPE;
   if (!(N->eps > 0.f) || !isfinite(N->eps) || !isfinite(N->residual_scale) ||
@@ -392,6 +399,9 @@ static int norm_out_check(int cols, const NormOut& o) {
   return MOE_OK;
 }
 
+// A launch takes fewer than 2^32 threads: more rows go in several.
+constexpr int kLaunchRows = 1 << 21;
+
 // Threads of a row and units of 8 elements per thread, by the row's length
 // alone (so a row's bits do not depend on the call).
 struct RowShape {
@@ -403,10 +413,13 @@ static RowShape row_shape(int cols) {
 }
 
 template <typename XT>
-static void launch_pre(const NormArgs& a, int rows, hipStream_t s) {
+static void launch_pre(NormArgs a, int rows, hipStream_t s) {
   const RowShape r = row_shape(a.cols);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(rows), dim3(r.threads), 0, s, a);
+    for (int64_t r0 = 0; r0 < rows; r0 += kLaunchRows) {
+      a.row0 = (int)r0;
+      hipLaunchKernelGGL(kernel, dim3(min(kLaunchRows, rows - a.row0)), dim3(r.threads), 0, s, a);
+    }
   };
   if (a.cols % 8 == 0) {
     if (r.units == 1) go(norm_pre_kernel<XT, 1, true>);
@@ -418,10 +431,13 @@ static void launch_pre(const NormArgs& a, int rows, hipStream_t s) {
 }
 
 template <typename XT, typename RT>
-static void launch_post(const NormArgs& a, int rows, hipStream_t s) {
+static void launch_post(NormArgs a, int rows, hipStream_t s) {
   const RowShape r = row_shape(a.cols);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(rows), dim3(r.threads), 0, s, a);
+    for (int64_t r0 = 0; r0 < rows; r0 += kLaunchRows) {
+      a.row0 = (int)r0;
+      hipLaunchKernelGGL(kernel, dim3(min(kLaunchRows, rows - a.row0)), dim3(r.threads), 0, s, a);
+    }
   };
   if (a.cols % 8 == 0) {
     if (r.units == 1) go(norm_post_kernel<XT, RT, 1, true>);
@@ -493,8 +509,8 @@ extern "C" int moe_norm_post(const moe_norm_t* N, const void* y, int y_type, int
     if (rc != MOE_OK) return rc;
   }
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
-  NormArgs a{y, ld_y, cols, 1.0 / cols, N->post_norm, N->eps, N->residual_scale, N->post_w, res, ld_res,
-             gate, gate_type, gate_row, gate_col, out, ld_out, next != nullptr, o};
+  NormArgs a{0, y, ld_y, cols, 1.0 / cols, N->post_norm, N->eps, N->residual_scale, N->post_w,
+             res, ld_res, gate, gate_type, gate_row, gate_col, out, ld_out, next != nullptr, o};
   hipStream_t s = (hipStream_t)stream;
   const bool yf = y_type == MOE_TYPE_F32, rf = res_type == MOE_TYPE_F32;
   if (yf && rf) launch_post<float, float>(a, rows, s);
@@ -520,7 +536,10 @@ extern "C" int moe_quant_row_q8(const void* x, int x_type, int64_t ld_x, int row
   const int threads = min(kQuantThreads, ((n + 1) / 2 + 63) / 64 * 64);
   hipStream_t s = (hipStream_t)stream;
   auto go = [&](auto kernel, auto* p) {
-    hipLaunchKernelGGL(kernel, dim3(rows), dim3(threads), 0, s, p, ld_x, cols, q, ld_q, scales);
+    for (int64_t r0 = 0; r0 < rows; r0 += kLaunchRows)
+      hipLaunchKernelGGL(kernel, dim3((unsigned)min((int64_t)kLaunchRows, rows - r0)),
+                         dim3(threads), 0, s, p + r0 * ld_x, ld_x, cols, q + r0 * ld_q, ld_q,
+                         scales + r0);
   };
   if (x_type == MOE_TYPE_F32) {
     if (cols % 8 == 0) go(quant_row_kernel<float, true>, (const float*)x);

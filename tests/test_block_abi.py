@@ -188,3 +188,9 @@ def test_python_argument_checks():
         m.moe_quant_row_q8(x.double())
     with pytest.raises(ValueError):
         m.route_outputs(4, 8, 2, device="cpu")
+
+
+def test_linear_refuses_more_tiles_than_a_launch():
+    L = m.lib()
+    lay = lin(N=1 << 22, K=64)
+    assert L.moe_linear_q8(lay, A, 64, A, 2**31 - 1, A, 0, 1 << 22, A, 1 << 30, None) == SHAPE
