@@ -9,6 +9,10 @@
 // One workgroup holds one row in registers, 8 consecutive elements per thread
 // and unit, so every input is read once and every output written once; a row
 // statistic is a sum per thread, per wave, then over the waves through LDS.
+// Few rows are bound by a launch and one memory round trip (one row of 4096:
+// 2.0 us of GPU time; 16 rows after a block, with the next norm and its codes:
+// 3.9 us), many by memory (4096 such rows of 4096: 34.0 us, 4.9 TB/s, a large
+// copy's rate; 26.6 us where the rows are in the last-level cache).
 #include "block.h"
 
 #include <math.h>
