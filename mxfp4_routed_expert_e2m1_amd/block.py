@@ -4,8 +4,8 @@ residual, scored routing, int8 linear layers.
 Like the rest of the binding, every function has the name of the C entry point
 it calls and only marshals arguments; a non-zero status raises MoeError.
 Element types and devices, which the C side cannot see, are checked here and
-raise TypeError or ValueError.  A call with `stream` runs, and allocates what it
-was not given, as it would under torch.cuda.stream(stream).
+raise TypeError or ValueError.  A call with `stream` runs on it, and what it was
+not given (outputs, workspaces) it allocates as under torch.cuda.stream(stream).
 """
 from __future__ import annotations
 
@@ -156,13 +156,17 @@ def _norm_out(like, h, h_dtype, quant, q, qs):
     return h, q, qs, ha + (_QUANT[quant], qp, ld_q, qsp, ld_qs)
 
 
+def _codes_missing(quant, q, qs):
+    return quant is not None and (q is None or qs is None)
+
+
 def moe_norm_pre(norm, x, h=None, h_dtype=None, quant=None, q=None, qs=None, stream=None):
     """h = rms(x) * pre_w of x [rows][d_model] (f32 or bf16).  h: the tensor to
     fill, None (allocated; h_dtype, by default x's type) or False (codes
     only).  quant: None, "block" (codes as moe_quant_act_q8's, for the routed
     experts) or "row" (as moe_quant_row_q8's, for moe_linear_q8).  Returns h,
     or (h, q, qs) with quant."""
-    if stream is not None:  # (also for what is allocated here)
+    if stream is not None and (h is None or _codes_missing(quant, q, qs)):
         with torch.cuda.stream(stream):
             return moe_norm_pre(norm, x, h, h_dtype, quant, q, qs)
     xa = _rows("x", x)
@@ -172,7 +176,7 @@ def moe_norm_pre(norm, x, h=None, h_dtype=None, quant=None, q=None, qs=None, str
     h, q, qs, out = _norm_out(x, h, h_dtype, quant, q, qs)
     rc = (_lib or _load()).moe_norm_pre(
         norm.ref, *xa, rows, *out,
-        _raw_stream(x.get_device()))
+        stream.cuda_stream if stream else _raw_stream(x.get_device()))
     if rc:
         _fail("moe_norm_pre", rc)
     return h if quant is None else (h, q, qs)
@@ -203,7 +207,8 @@ def moe_norm_post(norm, y, residual, gate=None, out=None, next_norm=None, h=None
     next block's h = rms(out) * pre_w in the same pass; h, h_dtype (default:
     residual's type), quant, q, qs as for moe_norm_pre.  Returns out, (out, h)
     with next_norm, (out, h, q, qs) with quant too."""
-    if stream is not None:  # (also for what is allocated here)
+    if stream is not None and (out is None or next_norm is not None and (
+            h is None or _codes_missing(quant, q, qs))):
         with torch.cuda.stream(stream):
             return moe_norm_post(norm, y, residual, gate, out, next_norm, h, h_dtype, quant, q,
                                  qs)
@@ -225,7 +230,7 @@ def moe_norm_post(norm, y, residual, gate=None, out=None, next_norm=None, h=None
         nx = next_norm.ref
     rc = (_lib or _load()).moe_norm_post(
         norm.ref, *ya, *ra, *(_NO_GATE if gate is None else _gate_args(gate, shape)), shape[0],
-        op, ld_out, nx, *nargs, _raw_stream(y.get_device()))
+        op, ld_out, nx, *nargs, stream.cuda_stream if stream else _raw_stream(y.get_device()))
     if rc:
         _fail("moe_norm_post", rc)
     if next_norm is None:
@@ -286,7 +291,7 @@ def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
     """Picks, weights and grouping of logits [rows][n_experts] (f32 or bf16)
     under a RouterRule.  Returns (ids, w, counts, offsets, sorted), as
     moe_route_group does; a slot without an expert holds id -1 and weight 0."""
-    if stream is not None:  # (also for what is allocated here)
+    if stream is not None and (out is None or ws is None):
         with torch.cuda.stream(stream):
             return moe_route_scored(rule, logits, out, ws)
     la = _rows("logits", logits)
@@ -304,7 +309,7 @@ def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
                          device=logits.device)
     rc = (_lib or _load()).moe_route_scored(
         rule.ref, *la, rows, *out.ptrs, ws.data_ptr(), ws.numel(),
-        _raw_stream(logits.get_device()))
+        stream.cuda_stream if stream else _raw_stream(logits.get_device()))
     if rc:
         _fail("moe_route_scored", rc)
     return out
@@ -322,7 +327,7 @@ def moe_quant_row_q8(x, q=None, scales=None, stream=None):
     """int8 codes and one scale per row of x [rows][cols] (f32 or bf16): of
     activations per token, or of weights [n_out][d_in] per channel.  Returns
     (q, scales); a q allocated here has 16-byte-aligned rows."""
-    if stream is not None:  # (also for what is allocated here)
+    if stream is not None and (q is None or scales is None):
         with torch.cuda.stream(stream):
             return moe_quant_row_q8(x, q, scales)
     xa = _rows("x", x)
@@ -334,7 +339,7 @@ def moe_quant_row_q8(x, q=None, scales=None, stream=None):
     qp, _, ld_q = _rows("q", q, shape, _INT8)
     rc = (_lib or _load()).moe_quant_row_q8(
         *xa, rows, cols, qp, ld_q, _vec("scales", scales, rows),
-        _raw_stream(x.get_device()))
+        stream.cuda_stream if stream else _raw_stream(x.get_device()))
     if rc:
         _fail("moe_quant_row_q8", rc)
     return q, scales
@@ -374,7 +379,7 @@ def moe_linear_q8(linear, q, qs, y=None, dtype=torch.bfloat16, ws=None, stream=N
     """y[t][n] = qs[t] w_scales[n] sum_k q[t][k] w[n][k] (+ bias[n]) of int8
     codes q [rows][d_in] (16-byte-aligned rows) and their row scales.  y: the
     f32 or bf16 tensor to fill, or None (allocated with `dtype`)."""
-    if stream is not None:  # (also for what is allocated here)
+    if stream is not None and (y is None or ws is None):
         with torch.cuda.stream(stream):
             return moe_linear_q8(linear, q, qs, y, dtype, ws)
     qp, ld_q = _codes("q", q)
@@ -388,7 +393,7 @@ def moe_linear_q8(linear, q, qs, y=None, dtype=torch.bfloat16, ws=None, stream=N
                          device=q.device)
     rc = (_lib or _load()).moe_linear_q8(
         linear.ref, qp, ld_q, _vec("qs", qs, rows), rows, *_rows("y", y, (rows, linear.n_out)),
-        ws.data_ptr(), ws.numel(), _raw_stream(q.get_device()))
+        ws.data_ptr(), ws.numel(), stream.cuda_stream if stream else _raw_stream(q.get_device()))
     if rc:
         _fail("moe_linear_q8", rc)
     return y

@@ -87,3 +87,30 @@ def test_another_stream_keeps_its_buffers():
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert all((t == 255).all() for t in taken)
+
+
+def test_given_buffers_on_a_given_stream():
+    side = torch.cuda.Stream()
+    g = gen(4)
+    z = torch.randn((777, 160), generator=g, device=DEV)
+    x = torch.randn((48, 4096), generator=g, device=DEV)
+    w = torch.randn((512, 4096), generator=g, device=DEV)
+    lay, rule, N = m.Linear(*m.moe_quant_row_q8(w)), m.RouterRule(160, 6), m.Norm(4096)
+    q, s = m.moe_quant_row_q8(x)
+    want = [*m.moe_route_scored(rule, z), m.moe_linear_q8(lay, q, s), q, s,
+            *m.moe_norm_post(N, x, x, next_norm=N, quant="row")]
+    route, y = m.route_outputs(777, 160, 6), torch.empty_like(want[5])
+    wr = torch.empty(m.moe_route_scored_workspace_bytes(rule, 777), dtype=torch.uint8, device=DEV)
+    wl = torch.empty(max(m.moe_linear_q8_workspace_bytes(lay, 48), 16), dtype=torch.uint8,
+                     device=DEV)
+    q2, s2, out, h = m.codes_buffer(48, 4096), torch.empty_like(s), *torch.empty((2, 48, 4096),
+                                                                                 device=DEV)
+    q3, s3 = m.codes_buffer(48, 4096), torch.empty_like(s)
+    torch.cuda.synchronize()
+    m.moe_route_scored(rule, z, out=route, ws=wr, stream=side)
+    m.moe_quant_row_q8(x, q=q2, scales=s2, stream=side)
+    m.moe_linear_q8(lay, q2, s2, y=y, ws=wl, stream=side)
+    m.moe_norm_post(N, x, x, out=out, next_norm=N, h=h, quant="row", q=q3, qs=s3, stream=side)
+    side.synchronize()
+    for a, b in zip([*route, y, q2, s2, out, h, q3, s3], want, strict=True):
+        assert torch.equal(a, b)
