@@ -115,6 +115,14 @@ def _vec(name, t, n, dtype=torch.float32, least=False):
     return t.data_ptr()
 
 
+def _workspace(ws):
+    """Pointer and bytes of a workspace, which the kernels fill from its first byte to its last."""
+    n = ws.nbytes
+    if n and not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws: need a contiguous tensor on the GPU")
+    return ws.data_ptr(), n
+
+
 # --------------------------------------------------------------------- norms
 class Norm:
     """moe_norm_t with its weights (f32 [d_model] or None): pre_w of the norm
@@ -308,7 +316,7 @@ def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
         ws = torch.empty(moe_route_scored_workspace_bytes(rule, rows), dtype=torch.uint8,
                          device=logits.device)
     rc = (_lib or _load()).moe_route_scored(
-        rule.ref, *la, rows, *out.ptrs, ws.data_ptr(), ws.numel(),
+        rule.ref, *la, rows, *out.ptrs, *_workspace(ws),
         stream.cuda_stream if stream else _raw_stream(logits.get_device()))
     if rc:
         _fail("moe_route_scored", rc)
@@ -393,7 +401,7 @@ def moe_linear_q8(linear, q, qs, y=None, dtype=torch.bfloat16, ws=None, stream=N
                          device=q.device)
     rc = (_lib or _load()).moe_linear_q8(
         linear.ref, qp, ld_q, _vec("qs", qs, rows), rows, *_rows("y", y, (rows, linear.n_out)),
-        ws.data_ptr(), ws.numel(), stream.cuda_stream if stream else _raw_stream(q.get_device()))
+        *_workspace(ws), stream.cuda_stream if stream else _raw_stream(q.get_device()))
     if rc:
         _fail("moe_linear_q8", rc)
     return y

@@ -1,0 +1,88 @@
+"""What the binding of the block operators refuses or hands on, with CPU tensors
+that say they are on a GPU and a library that only records its calls."""
+import pytest
+import torch
+
+import mxfp4_routed_expert_e2m1_amd as m
+from mxfp4_routed_expert_e2m1_amd import block as b
+
+F32, I8, U8 = torch.float32, torch.int8, torch.uint8
+
+
+class OnGpu(torch.Tensor):
+    """A tensor in host memory that gives itself out as one of GPU `gpu`."""
+    gpu = 0
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.gpu
+
+
+def on(gpu, *shape, dtype=F32):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+    t.gpu = gpu
+    return t
+
+
+class Recorder:
+    """Stands for the loaded library: every entry point succeeds and is noted down."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, fn):
+        def call(*args):
+            if fn.endswith("_bytes"):
+                return 64
+            self.calls.append((fn, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(b, "_lib", r)
+    monkeypatch.setattr(b, "_raw_stream", lambda gpu: 1000 + gpu)
+    return r
+
+
+def a_route(gpu=0, **kw):
+    i32 = torch.int32
+    out = (on(gpu, 20, 4, dtype=i32), on(gpu, 20, 4), on(gpu, 64, dtype=i32),
+           on(gpu, 65, dtype=i32), on(gpu, 80, dtype=i32))
+    return m.moe_route_scored(m.RouterRule(64, 4), on(gpu, 20, 64),
+                              **{"out": out, "ws": on(gpu, 64, dtype=U8), **kw})
+
+
+def a_linear(gpu=0, **kw):
+    lay = m.Linear(on(gpu, 8, 32, dtype=I8), on(gpu, 8))
+    return m.moe_linear_q8(lay, on(gpu, 20, 32, dtype=I8), on(gpu, 20),
+                           **{"y": on(gpu, 20, 8), "ws": on(gpu, 64, dtype=U8), **kw})
+
+
+# ---------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("call", [a_route, a_linear])
+def test_a_workspace_in_host_memory_is_refused(lib, call):
+    with pytest.raises(ValueError):
+        call(ws=torch.zeros(64, dtype=U8))
+    assert not lib.calls
+    call(ws=torch.empty(0, dtype=U8))  # (nothing in it that could be read)
+    assert len(lib.calls) == 1
+
+
+@pytest.mark.parametrize("call", [a_route, a_linear])
+def test_a_workspace_with_gaps_is_refused(lib, call):
+    with pytest.raises(ValueError):
+        call(ws=on(0, 128, dtype=U8)[::2])
+    one = on(0, 1, dtype=U8).expand(64)
+    one.gpu = 0
+    with pytest.raises(ValueError):
+        call(ws=one)
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("call,at", [(a_route, -2), (a_linear, -2)])
+def test_a_workspace_counts_in_bytes(lib, call, at):
+    call(ws=on(0, 16))
+    assert lib.calls[0][1][at] == 64
