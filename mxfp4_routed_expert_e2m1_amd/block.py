@@ -267,18 +267,31 @@ class RouterRule:
 
 
 class RouteOutputs(tuple):
-    """Buffers (ids, w, counts, offsets, sorted) of a routing call, checked once, for callers that
-    keep them: five tensors' checks are a fifth of a decode call's host time."""
+    """Buffers (ids, w, counts, offsets, sorted) of a routing call, checked when they are made, for
+    callers that keep them: all the checks of five tensors are a fifth of a decode call's host
+    time.  A call looks whether they are still where they were and of the size they were, and
+    otherwise checks them again."""
 
     def __new__(cls, ids, w, counts, offsets, srt):
         self = super().__new__(cls, (ids, w, counts, offsets, srt))
-        rows, k = ids.shape
+        rows, k = self.shape = ids.shape
         E, i32 = counts.numel(), torch.int32
         self.key = (rows, E, k)
         self.ptrs = (_vec("ids", ids, rows * k, i32), _vec("w", w, rows * k),
                      _vec("counts", counts, E, i32), _vec("offsets", offsets, E + 1, i32),
                      _vec("sorted", srt, rows * k, i32, least=True))
+        self.sizes = (w.numel(), E, E + 1, srt.numel())
         return self
+
+    def __reduce__(self):  # (a copy of the buffers has addresses of its own)
+        return RouteOutputs, tuple(self)
+
+    def unchanged(self):
+        ids, w, counts, offsets, srt = self
+        return (ids.shape == self.shape
+                and (w.numel(), counts.numel(), offsets.numel(), srt.numel()) == self.sizes
+                and (ids.data_ptr(), w.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
+                     srt.data_ptr()) == self.ptrs)
 
 
 def route_outputs(rows, n_experts, top_k, device="cuda"):
@@ -308,7 +321,7 @@ def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
         raise ValueError(f"logits: {logits.shape[1]} columns, the rule has {E} experts")
     if out is None:
         out = route_outputs(rows, E, k, logits.device)
-    elif type(out) is not RouteOutputs:
+    elif type(out) is not RouteOutputs or not out.unchanged():
         out = RouteOutputs(*out)
     if out.key != (rows, E, k):
         raise ValueError(f"out: buffers of {out.key} rows, experts and picks, need {(rows, E, k)}")

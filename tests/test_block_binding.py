@@ -1,5 +1,7 @@
 """What the binding of the block operators refuses or hands on, with CPU tensors
 that say they are on a GPU and a library that only records its calls."""
+import copy
+
 import pytest
 import torch
 
@@ -16,6 +18,11 @@ class OnGpu(torch.Tensor):
 
     def get_device(self):
         return self.gpu
+
+    def __deepcopy__(self, memo):
+        t = self.clone()
+        t.gpu = self.gpu
+        return t
 
 
 def on(gpu, *shape, dtype=F32):
@@ -86,3 +93,48 @@ def test_a_workspace_with_gaps_is_refused(lib, call):
 def test_a_workspace_counts_in_bytes(lib, call, at):
     call(ws=on(0, 16))
     assert lib.calls[0][1][at] == 64
+
+
+# ------------------------------------------------- buffers that a caller keeps
+def addresses(out):
+    return tuple(t.data_ptr() for t in out)
+
+
+def kept(lib):
+    return m.RouteOutputs(*a_route())
+
+
+def test_kept_outputs_that_moved_are_written_where_they_are(lib):
+    out = kept(lib)
+    out[0].set_(torch.zeros(20, 4, dtype=torch.int32))
+    out[1].data = torch.zeros(20, 4)
+    a_route(out=out)
+    assert lib.calls[-1][1][5:10] == addresses(out)
+
+
+@pytest.mark.parametrize("i", range(5))
+def test_kept_outputs_of_another_size_are_refused(lib, i):
+    out = kept(lib)
+    n = len(lib.calls)
+    out[i].resize_(3, 1)        # in place: the address stays
+    with pytest.raises(ValueError):
+        a_route(out=out)
+    assert len(lib.calls) == n
+
+
+def test_kept_outputs_that_grow_serve_the_larger_call(lib):
+    out = kept(lib)
+    for i, shape in ((0, (21, 4)), (1, (21, 4)), (4, (84,))):
+        out[i].resize_(shape)
+    m.moe_route_scored(m.RouterRule(64, 4), on(0, 21, 64), out=out, ws=on(0, 64, dtype=U8))
+    assert lib.calls[-1][1][5:10] == addresses(out)
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy])
+def test_kept_outputs_can_be_copied(lib, how):
+    out = kept(lib)
+    other = how(out)
+    assert type(other) is m.RouteOutputs
+    assert (addresses(other) == addresses(out)) == (how is copy.copy)
+    a_route(out=other)
+    assert lib.calls[-1][1][5:10] == addresses(other)
