@@ -1,6 +1,8 @@
 """What the binding of the block operators refuses or hands on, with CPU tensors
 that say they are on a GPU and a library that only records its calls."""
+import contextlib
 import copy
+import types
 
 import pytest
 import torch
@@ -32,16 +34,18 @@ def on(gpu, *shape, dtype=F32):
 
 
 class Recorder:
-    """Stands for the loaded library: every entry point succeeds and is noted down."""
+    """Stands for the loaded library: every entry point succeeds and is noted down, with the
+    GPU that was current then."""
 
     def __init__(self):
-        self.calls = []
+        self.calls, self.gpu, self.gpus = [], 0, []
 
     def __getattr__(self, fn):
         def call(*args):
             if fn.endswith("_bytes"):
                 return 64
             self.calls.append((fn, args))
+            self.gpus.append(self.gpu)
             return 0
         return call
 
@@ -51,6 +55,14 @@ def lib(monkeypatch):
     r = Recorder()
     monkeypatch.setattr(b, "_lib", r)
     monkeypatch.setattr(b, "_raw_stream", lambda gpu: 1000 + gpu)
+    monkeypatch.setattr(b, "_current_gpu", lambda: r.gpu, raising=False)
+
+    @contextlib.contextmanager
+    def device(gpu):
+        r.gpu, was = gpu, r.gpu
+        yield
+        r.gpu = was
+    monkeypatch.setattr(torch.cuda, "device", device)
     return r
 
 
@@ -138,3 +150,83 @@ def test_kept_outputs_can_be_copied(lib, how):
     assert (addresses(other) == addresses(out)) == (how is copy.copy)
     a_route(out=other)
     assert lib.calls[-1][1][5:10] == addresses(other)
+
+
+# ------------------------------------------------------------------- devices
+def a_norm_pre(gpu=0, w=None, **kw):
+    return m.moe_norm_pre(m.Norm(64, pre_w=w), on(gpu, 5, 64),
+                          **{"h": on(gpu, 5, 64), "quant": "row", "q": on(gpu, 5, 64, dtype=I8),
+                             "qs": on(gpu, 5), **kw})
+
+
+def a_norm_post(gpu=0, w=None, w2=None, **kw):
+    kw = {"residual": on(gpu, 5, 64), "out": on(gpu, 5, 64), "h": on(gpu, 5, 64),
+          "quant": "block", "q": on(gpu, 5, 64, dtype=I8), "qs": on(gpu, 5, 2), **kw}
+    return m.moe_norm_post(m.Norm(64, post_w=w), on(gpu, 5, 64),
+                           next_norm=m.Norm(64, pre_w=w2), **kw)
+
+
+def a_quant(gpu=0, **kw):
+    return m.moe_quant_row_q8(on(gpu, 5, 64), **{"q": on(gpu, 5, 64, dtype=I8),
+                                                "scales": on(gpu, 5), **kw})
+
+
+NEW = {a_norm_pre: "h", a_norm_post: "out", a_quant: "q", a_route: "ws", a_linear: "ws"}
+CALLS = [a_norm_pre, a_norm_post, a_quant, a_route, a_linear]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_the_tensors_gpu_is_current_during_the_call(lib, call):
+    call(1)
+    call(0)
+    assert lib.gpus == [1, 0] and lib.gpu == 0
+    assert [args[-1] for _, args in lib.calls] == [1001, 1000]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_stream_of_another_gpu_is_refused(lib, call):
+    stream = lambda gpu: types.SimpleNamespace(device_index=gpu, cuda_stream=77)  # noqa: E731
+    with pytest.raises(ValueError):
+        call(0, stream=stream(1))
+    with pytest.raises(ValueError):  # (with a buffer that would be allocated under it)
+        call(0, stream=stream(1), **{NEW[call]: None})
+    assert not lib.calls
+    call(1, stream=stream(1))
+    assert lib.gpus == [1] and lib.calls[0][1][-1] == 77
+
+
+F, R = (on(1, 5, 64), on(1, 5))
+Q = on(1, 5, 64, dtype=I8)
+
+
+@pytest.mark.parametrize("call,kw", [
+    (a_norm_pre, {"w": on(1, 64)}), (a_norm_pre, {"h": F}), (a_norm_pre, {"q": Q}),
+    (a_norm_pre, {"qs": R}),
+    (a_norm_post, {"w": on(1, 64)}), (a_norm_post, {"w2": on(1, 64)}),
+    (a_norm_post, {"residual": F}), (a_norm_post, {"gate": on(1, 64)}), (a_norm_post, {"out": F}),
+    (a_norm_post, {"h": F}), (a_norm_post, {"q": Q}), (a_norm_post, {"qs": on(1, 5, 2)}),
+    (a_quant, {"q": Q}), (a_quant, {"scales": R}),
+    (a_route, {"ws": on(1, 64, dtype=U8)}), (a_linear, {"ws": on(1, 64, dtype=U8)}),
+    (a_linear, {"y": on(1, 20, 8)})])
+def test_tensors_of_two_gpus_are_refused(lib, call, kw):
+    with pytest.raises(ValueError):
+        call(**kw)
+    assert not lib.calls
+
+
+def test_descriptors_and_kept_outputs_of_another_gpu_are_refused(lib):
+    out, ws = m.RouteOutputs(*a_route(1)), on(0, 64, dtype=U8)
+    lib.calls.clear()
+    z, q, s = on(0, 20, 64), on(0, 20, 32, dtype=I8), on(0, 20)
+    lay = m.Linear(on(1, 8, 32, dtype=I8), on(1, 8))
+    for f in (lambda: m.moe_route_scored(m.RouterRule(64, 4), z, out=out, ws=ws),
+              lambda: m.moe_route_scored(m.RouterRule(64, 4, bias=on(1, 64)), z, ws=ws,
+                                         out=a_route()),
+              lambda: m.moe_linear_q8(lay, q, s, y=on(0, 20, 8), ws=ws),
+              lambda: m.Linear(on(0, 8, 32, dtype=I8), on(1, 8)),
+              lambda: m.Linear(on(0, 8, 32, dtype=I8), on(0, 8), on(1, 8)),
+              lambda: m.Norm(64, pre_w=on(0, 64), post_w=on(1, 64)),
+              lambda: m.RouteOutputs(*[t for t in out[:4]], on(0, 80, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            f()
+    assert [fn for fn, args in lib.calls] == ["moe_route_scored"]  # a_route()'s own
