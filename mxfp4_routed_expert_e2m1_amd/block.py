@@ -80,9 +80,11 @@ def _fail(fn, rc):
     raise m.MoeError(fn, rc)
 
 
-# The raw handle of torch's current stream on a device: making the stream object costs 2 us,
-# about what the launch does.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The raw handle of torch's current stream on a GPU, and the current GPU.  Making the stream
+# object costs 2 us, about what the launch does, so torch's own shortcuts are taken where it has
+# them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda gpu: torch.cuda.current_stream(gpu).cuda_stream)
 _current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 

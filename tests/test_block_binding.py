@@ -2,12 +2,15 @@
 that say they are on a GPU and a library that only records its calls."""
 import contextlib
 import copy
+import subprocess
+import sys
 import types
 
 import pytest
 import torch
 
 import mxfp4_routed_expert_e2m1_amd as m
+from conftest import ROOT
 from mxfp4_routed_expert_e2m1_amd import block as b
 
 F32, I8, U8 = torch.float32, torch.int8, torch.uint8
@@ -230,3 +233,21 @@ def test_descriptors_and_kept_outputs_of_another_gpu_are_refused(lib):
         with pytest.raises(ValueError):
             f()
     assert [fn for fn, args in lib.calls] == ["moe_route_scored"]  # a_route()'s own
+
+
+def test_the_package_needs_no_private_names_of_torch():
+    """Without torch's quick ways to the current stream and GPU the package still imports, and
+    asks the public ones."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from mxfp4_routed_expert_e2m1_amd import block
+class Stream:
+    cuda_stream = 77
+torch.cuda.current_stream = lambda gpu: Stream
+assert block._raw_stream(1) == 77 and block._current_gpu is torch.cuda.current_device
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
