@@ -33,6 +33,9 @@ _SCORE = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 _GROUP = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
 
 
+_MOST = 2**31 - 1  # of a C int, which ctypes would cut larger numbers to without an error
+
+
 class moe_norm_t(C.Structure):
     _fields_ = [("d_model", I), ("post_norm", I), ("eps", F), ("residual_scale", F),
                 ("pre_w", P), ("post_w", P)]
@@ -120,7 +123,8 @@ def _rows(name, t, gpu, shape=None, types=_TYPES):
     (row-strided views are fine).  A single row needs no leading dimension: any aligned one."""
     kind, sh, st = types.get(t.dtype), t.shape, t.stride()
     if (kind is None or len(st) != 2 or (st[1] != 1 and sh[1] > 1) or t.get_device() != gpu
-            or gpu < 0 or (shape is not None and sh != shape)):
+            or gpu < 0 or sh[0] > _MOST or sh[1] > _MOST
+            or (shape is not None and sh != shape)):
         _refuse_rows(name, t, gpu, shape, types)
     return t.data_ptr(), kind, st[0] if sh[0] > 1 else (sh[1] + 15) // 16 * 16
 
@@ -130,6 +134,8 @@ def _refuse_rows(name, t, gpu, shape, types):
         raise TypeError(f"{name}: {t.dtype} is not one of {[str(d) for d in types]}")
     if t.get_device() != gpu or gpu < 0:
         _refuse_gpu(name, t, gpu)
+    if max(t.shape, default=0) > _MOST:
+        raise ValueError(f"{name}: {list(t.shape)} is more than {_MOST} rows or columns")
     raise ValueError(f"{name}: need contiguous rows {list(shape) if shape else '[rows][cols]'}, "
                      f"got {list(t.shape)} with strides {t.stride()}")
 
@@ -147,6 +153,12 @@ def _vec(name, t, n, gpu, dtype=torch.float32, least=False):
             _refuse_gpu(name, t, gpu)
         raise ValueError(f"{name}: need {n} contiguous elements on the GPU")
     return t.data_ptr()
+
+
+def _int(name, v):
+    if not -_MOST <= v <= _MOST:
+        raise ValueError(f"{name}: {v} is more than {_MOST}")
+    return v
 
 
 def _workspace(ws, gpu):
@@ -167,7 +179,7 @@ class Norm:
         self.tensors = (pre_w, post_w)  # keep alive
         self.d_model = d_model
         self.gpu = gpu = _gpu(pre_w, post_w)
-        self.c = moe_norm_t(d_model, int(post_norm), eps, residual_scale,
+        self.c = moe_norm_t(_int("d_model", d_model), int(post_norm), eps, residual_scale,
                             _vec("pre_w", pre_w, d_model, gpu),
                             _vec("post_w", post_w, d_model, gpu))
         self.ref = C.byref(self.c)
@@ -308,9 +320,10 @@ class RouterRule:
                              f"{list(_SCORE)} / {list(_GROUP)}")
         self.tensors = (bias,)  # keep alive
         self.n_experts, self.top_k, self.gpu = n_experts, top_k, _gpu(bias)
-        self.c = moe_router_rule_t(n_experts, top_k, n_groups,
-                                   n_groups if top_groups is None else top_groups, _SCORE[score],
-                                   _GROUP[group_score], int(renorm), scale,
+        top_groups = n_groups if top_groups is None else top_groups
+        self.c = moe_router_rule_t(_int("n_experts", n_experts), _int("top_k", top_k),
+                                   _int("n_groups", n_groups), _int("top_groups", top_groups),
+                                   _SCORE[score], _GROUP[group_score], int(renorm), scale,
                                    _vec("bias", bias, n_experts, self.gpu))
         self.ref = C.byref(self.c)
 
@@ -355,7 +368,7 @@ def route_outputs(rows, n_experts, top_k, device="cuda"):
 
 
 def moe_route_scored_workspace_bytes(rule, rows):
-    return int((_lib or _load()).moe_route_scored_workspace_bytes(rule.ref, rows))
+    return int((_lib or _load()).moe_route_scored_workspace_bytes(rule.ref, _int("rows", rows)))
 
 
 def moe_route_scored(rule, logits, out=None, ws=None, stream=None):
@@ -456,7 +469,7 @@ class Linear:
 
 
 def moe_linear_q8_workspace_bytes(linear, rows):
-    return int((_lib or _load()).moe_linear_q8_workspace_bytes(linear.ref, rows))
+    return int((_lib or _load()).moe_linear_q8_workspace_bytes(linear.ref, _int("rows", rows)))
 
 
 def moe_linear_q8(linear, q, qs, y=None, dtype=torch.bfloat16, ws=None, stream=None):

@@ -251,3 +251,54 @@ assert block._raw_stream(1) == 77 and block._current_gpu is torch.cuda.current_d
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+# ------------------------------------------------------ sizes past 32 bits
+BIG = 2**32 + 20  # (its low 32 bits are an ordinary size)
+
+
+class Says(OnGpu):
+    """One that gives itself another shape, its rows without gaps."""
+    shape = property(lambda self: torch.Size(self.says))
+
+    def stride(self):
+        return (self.says[1], 1)
+
+    def numel(self):
+        return self.says[0] * self.says[-1]
+
+
+def says(*shape, dtype=F32):
+    t = torch.zeros(1, dtype=dtype).as_subclass(Says)
+    t.says = shape
+    return t
+
+
+def test_sizes_that_c_would_cut_are_refused(lib):
+    tall, wide, codes = says(BIG, 64), says(20, BIG), says(BIG, 64, dtype=I8)
+    many = on(0, 1).expand(BIG)
+    norm = m.Norm(64)
+    norm.d_model = BIG
+    for f in (lambda: m.moe_norm_pre(m.Norm(64), tall, h=tall),
+              lambda: m.moe_norm_pre(norm, wide, h=wide),
+              lambda: m.moe_norm_post(m.Norm(64), tall, tall, out=tall),
+              lambda: m.moe_quant_row_q8(tall, q=codes, scales=many),
+              lambda: m.moe_quant_row_q8(wide, q=says(20, BIG, dtype=I8), scales=on(0, 20)),
+              lambda: m.moe_route_scored(m.RouterRule(64, 4), tall),
+              lambda: m.moe_linear_q8(m.Linear(on(0, 8, 64, dtype=I8), on(0, 8)), codes, many),
+              lambda: m.Linear(codes, many),
+              lambda: m.moe_route_scored_workspace_bytes(m.RouterRule(64, 4), BIG),
+              lambda: m.moe_linear_q8_workspace_bytes(
+                  m.Linear(on(0, 8, 64, dtype=I8), on(0, 8)), BIG)):
+        with pytest.raises(ValueError, match="2147483647"):
+            f()
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("kw", [{"n_experts": BIG}, {"top_k": BIG}, {"n_groups": BIG},
+                                {"top_groups": BIG}, {"n_experts": -BIG}])
+def test_rules_that_c_would_cut_are_refused(kw):
+    with pytest.raises(ValueError):
+        m.RouterRule(**{"n_experts": 64, "top_k": 4, **kw})
+    with pytest.raises(ValueError):
+        m.Norm(BIG)
