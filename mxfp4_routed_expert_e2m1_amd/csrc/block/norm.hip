@@ -100,10 +100,11 @@ __device__ inline float wg_max(uint32_t v, uint32_t* slots) {
   return __uint_as_float(v);
 }
 
-// WHOLE: the row is a whole number of units
+// WHOLE: the row is a whole number of units.  (e and cols are up to 2^31 - 1 in
+// the row quantiser, so e + 8 is not formed.)
 template <bool WHOLE, typename T>
 __device__ inline Raw8<T> load_unit(const T* row, int e, int cols) {
-  if (e + 8 <= cols) return load8(row + e);
+  if (cols - e >= 8) return load8(row + e);
   if (!WHOLE && e < cols) return load8_part(row + e, cols - e);
   return Raw8<T>{};
 }
@@ -343,20 +344,21 @@ __global__ __launch_bounds__(kQuantThreads) void quant_row_kernel(const XT* x0, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(v[i]));
   }
-  for (int e = kQuantUnits * stride + 8 * (int)threadIdx.x; e < cols; e += stride) {
-    to_f32(load_unit<WHOLE>(x, e, cols), v);
+  // (unsigned: the step past the end of the longest row is past 2^31 - 1)
+  for (uint32_t e = kQuantUnits * stride + 8 * threadIdx.x; e < (uint32_t)cols; e += stride) {
+    to_f32(load_unit<WHOLE>(x, (int)e, cols), v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(v[i]));
   }
   const float d = wg_max(amax, slots) / 127.0f;
   auto write = [&](int e) {
     const u32x2 w = row_codes(v, d);
-    if (e + 8 <= cols) {
+    if (cols - e >= 8) {
       *(u32x2*)(q + e) = w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (e + i < cols) q[e + i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+        if (i < cols - e) q[e + i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
     }
   };
 #pragma unroll
@@ -366,9 +368,9 @@ __global__ __launch_bounds__(kQuantThreads) void quant_row_kernel(const XT* x0, 
     to_f32(raw[u], v);
     write(e);
   }
-  for (int e = kQuantUnits * stride + 8 * (int)threadIdx.x; e < cols; e += stride) {
-    to_f32(load_unit<WHOLE>(x, e, cols), v);
-    write(e);
+  for (uint32_t e = kQuantUnits * stride + 8 * threadIdx.x; e < (uint32_t)cols; e += stride) {
+    to_f32(load_unit<WHOLE>(x, (int)e, cols), v);
+    write((int)e);
   }
   if (threadIdx.x == 0) scales[row] = d;
 }
@@ -534,7 +536,7 @@ extern "C" int moe_quant_row_q8(const void* x, int x_type, int64_t ld_x, int row
   if (!aligned(x, type_size(x_type)) || !aligned(q, 8) || ld_q % 8 != 0 || !aligned(scales, 4))
     return MOE_ERR_ALIGNMENT;
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
-  const int n = (cols + 7) / 8;
+  const int n = (int)(((int64_t)cols + 7) / 8);
   // (two units per thread keep more loads on their way: 4096 rows of 4096 bf16
   // 15.7 -> 12.9 us)
   const int threads = min(kQuantThreads, ((n + 1) / 2 + 63) / 64 * 64);
