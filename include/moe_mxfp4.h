@@ -487,8 +487,9 @@ typedef struct moe_router_rule {
   const float* bias; /* f32 [n_experts] (device), finite, or NULL */
 } moe_router_rule_t;
 
-/* Bytes of workspace moe_route_scored needs for `rows` rows (0 for decode
- * rows; 0 as well for a rule that it rejects). */
+/* Bytes of workspace that serve moe_route_scored for any number of rows up to
+ * `rows`: never less for more rows, so one workspace for the largest chunk
+ * serves all (0 for decode rows; 0 as well for a rule that it rejects). */
 size_t moe_route_scored_workspace_bytes(const moe_router_rule_t* R, int rows);
 
 /*   logits f32/bf16 [rows][ld_l] (device), ld_l >= n_experts

@@ -441,15 +441,25 @@ static RouteShape route_shape(int n_experts, int rows) {
   return s;
 }
 
+// Workspace of a call: its runs' counts (all that is not decode has one, also
+// where one workgroup does without).
+static size_t route_bytes(int n_experts, int64_t runs) {
+  return (size_t)runs * ((n_experts + 7) / 8 * 8) * sizeof(uint16_t);
+}
+static size_t route_need(int n_experts, int rows) {
+  return rows <= MOE_MAX_DECODE_ROWS ? 0 : route_bytes(n_experts, route_shape(n_experts, rows).n_runs);
+}
+
 }  // namespace moe
 
 using namespace moe;
 
 extern "C" size_t moe_route_scored_workspace_bytes(const moe_router_rule_t* R, int rows) {
-  // (all that is not decode asks for it, also where one workgroup does without)
   if (rule_check(R) != MOE_OK || rows <= MOE_MAX_DECODE_ROWS) return 0;
-  const RouteShape s = route_shape(R->n_experts, rows);
-  return (size_t)s.n_runs * s.hist_ld * sizeof(uint16_t);
+  // the most runs that as many rows or fewer come in: 4 rows each up to 1024
+  // rows, then 16 each up to 8192 (512 runs), then fewer
+  const int64_t runs = rows <= 1024 ? (rows + 3) / 4 : max(256, min(512, (rows - 1) / 16 + 1));
+  return route_bytes(R->n_experts, runs);
 }
 
 extern "C" int moe_route_scored(const moe_router_rule_t* R, const void* logits, int l_type,
@@ -466,7 +476,7 @@ extern "C" int moe_route_scored(const moe_router_rule_t* R, const void* logits, 
       (rows > 0 && (!aligned(logits, type_size(l_type)) || !aligned(ids, 4) || !aligned(w, 4) ||
                     !aligned(sorted, 4))))
     return MOE_ERR_ALIGNMENT;
-  const size_t need = moe_route_scored_workspace_bytes(R, rows);
+  const size_t need = route_need(R->n_experts, rows);
   if (need > 0) {
     if (!ws) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
