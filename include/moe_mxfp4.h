@@ -531,7 +531,9 @@ typedef struct moe_linear {
   const float* bias;     /* f32 [n_out] (device) or NULL */
 } moe_linear_t;
 
-/* Bytes of workspace moe_linear_q8 needs for `rows` rows (can be 0). */
+/* Bytes of workspace that serve moe_linear_q8 for any number of rows up to
+ * `rows` (can be 0): never less for more rows, so one workspace for the largest
+ * chunk serves all. */
 size_t moe_linear_q8_workspace_bytes(const moe_linear_t* L, int rows);
 
 /*   q  int8 [rows][ld_q] (device, 16-byte aligned, ld_q % 16 == 0, <= 2^22),

@@ -572,8 +572,12 @@ static LinearPart best_part(int rows, int channels, int d_in, int most_splits, d
 // one row of 4096 x 4096: 8.2 and 5.8).  Otherwise the best tile; or, where its
 // last round would leave much of the chip idle, whole rounds of it and a second
 // launch with the best tile for the channels left.
+constexpr int kStreamRows = 16;
+static bool streams(int rows, int n_out) {
+  return rows <= kStreamRows && ceil_div(n_out, 64) < 3 * kChipCus / 4;
+}
 static LinearPlan plan(int rows, int n_out, int d_in) {
-  if (rows <= 16 && ceil_div(n_out, 64) < 3 * kChipCus / 4) return {{{-1, 1, n_out}, {}}, 1};
+  if (streams(rows, n_out)) return {{{-1, 1, n_out}, {}}, 1};
   double us;
   LinearPlan best{{best_part(rows, n_out, d_in, 8, &us), {}}, 1};
   for (int i = 0; i < 2; ++i) {  // (smaller tiles have short last rounds)
@@ -607,13 +611,29 @@ static size_t plan_bytes(const LinearPlan& p, int rows) {
   return f.splits > 1 ? (size_t)f.splits * rows * parts_ld(f.channels) * sizeof(int32_t) : 0;
 }
 
+// The most workspace that a call of up to `rows` rows needs.  Within 64 rows
+// whose tiles are the same in number, only the cost of joining the splits grows
+// with the rows, so the first of them has the most splits; past the rows whose
+// largest tiles fill half the chip there are none.
+static size_t most_bytes(int rows, int n_out, int d_in) {
+  const Tile8& t = kTiles[0];
+  const int64_t end = (int64_t)64 * t.tt * (kChipCus / 2 / ceil_div(n_out, 64 * t.tn));
+  size_t most = 0;
+  for (int r = 0; r < rows && r < end; r += 64) {
+    const int first = r == 0 && streams(1, n_out) ? kStreamRows + 1 : r + 1;
+    if (first > rows) break;
+    most = max(most, plan_bytes(plan(first, n_out, d_in), min(rows, r + 64)));
+  }
+  return most;
+}
+
 }  // namespace moe
 
 using namespace moe;
 
 extern "C" size_t moe_linear_q8_workspace_bytes(const moe_linear_t* L, int rows) {
   if (linear_check(L) != MOE_OK || rows < 1) return 0;
-  return plan_bytes(plan(rows, L->n_out, L->d_in), rows);
+  return most_bytes(rows, L->n_out, L->d_in);
 }
 
 extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_q,
