@@ -169,6 +169,11 @@ def _workspace(ws, gpu):
     return ws.data_ptr(), n
 
 
+def _kept(*tensors):
+    """The tensors' memory as it is now, kept alive (assigning to a tensor's .data leaves it)."""
+    return tuple(None if t is None else t.detach() for t in tensors)
+
+
 # --------------------------------------------------------------------- norms
 class Norm:
     """moe_norm_t with its weights (f32 [d_model] or None): pre_w of the norm
@@ -176,7 +181,7 @@ class Norm:
 
     def __init__(self, d_model, pre_w=None, post_w=None, post_norm=True, eps=1e-6,
                  residual_scale=1.0):
-        self.tensors = (pre_w, post_w)  # keep alive
+        self.tensors = _kept(pre_w, post_w)
         self.d_model = d_model
         self.gpu = gpu = _gpu(pre_w, post_w)
         self.c = moe_norm_t(_int("d_model", d_model), int(post_norm), eps, residual_scale,
@@ -318,7 +323,7 @@ class RouterRule:
         if score not in _SCORE or group_score not in _GROUP:
             raise ValueError(f"score {score!r} / group_score {group_score!r}: need one of "
                              f"{list(_SCORE)} / {list(_GROUP)}")
-        self.tensors = (bias,)  # keep alive
+        self.tensors = _kept(bias)
         self.n_experts, self.top_k, self.gpu = n_experts, top_k, _gpu(bias)
         top_groups = n_groups if top_groups is None else top_groups
         self.c = moe_router_rule_t(_int("n_experts", n_experts), _int("top_k", top_k),
@@ -459,7 +464,7 @@ class Linear:
     [n_out] or None."""
 
     def __init__(self, w, w_scales, bias=None):
-        self.tensors = (w, w_scales, bias)  # keep alive
+        self.tensors = _kept(w, w_scales, bias)
         self.n_out, self.d_in = w.shape
         self.gpu = gpu = w.get_device()
         self.c = moe_linear_t(self.n_out, self.d_in, *_codes("w", w, gpu),

@@ -302,3 +302,18 @@ def test_rules_that_c_would_cut_are_refused(kw):
         m.RouterRule(**{"n_experts": 64, "top_k": 4, **kw})
     with pytest.raises(ValueError):
         m.Norm(BIG)
+
+
+# ------------------------------------------------------------- descriptors
+def test_descriptors_keep_the_memory_they_were_made_from(lib):
+    """A weight whose data is replaced afterwards leaves the descriptor on live memory."""
+    w, w2, bias, q, s, y = (on(0, 64), on(0, 64), on(0, 64), on(0, 64, 64, dtype=I8), on(0, 64),
+                            on(0, 64))
+    made = [m.Norm(64, pre_w=w, post_w=w2), m.RouterRule(64, 4, bias=bias), m.Linear(q, s, y)]
+    for t in (w, w2, bias, s, y):
+        t.data = torch.ones(64)
+    q.data = torch.ones(64, 64, dtype=I8)
+    fields = [("pre_w", "post_w"), ("bias",), ("w", "w_scales", "bias")]
+    for d, names in zip(made, fields):
+        assert [t.data_ptr() for t in d.tensors] == [getattr(d.c, n) for n in names]
+        assert all((t == 0).all() for t in d.tensors)
