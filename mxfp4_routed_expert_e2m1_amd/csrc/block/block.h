@@ -6,17 +6,6 @@
 
 namespace moe {
 
-template <typename T>
-struct ElemType;
-template <>
-struct ElemType<float> {
-  static constexpr int id = MOE_TYPE_F32;
-};
-template <>
-struct ElemType<__bf16> {
-  static constexpr int id = MOE_TYPE_BF16;
-};
-
 inline bool type_ok(int t) { return t == MOE_TYPE_F32 || t == MOE_TYPE_BF16; }
 inline size_t type_size(int t) { return t == MOE_TYPE_F32 ? 4 : 2; }
 

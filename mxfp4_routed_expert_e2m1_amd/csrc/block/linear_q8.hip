@@ -406,9 +406,10 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
   const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
   const int n0 = blockIdx.x * 16, r = lane & 15, slot = lane >> 4;
   const int have_n = min(16, a.n_out - n0);
-  const auto ws = buf_rsrc(a.w + uniform((int64_t)n0 * a.ld_w),
-                           (uint32_t)((have_n - 1) * a.ld_w + piece_end(a.d_in)));
-  const auto qs = buf_rsrc(a.q, (uint32_t)((a.rows - 1) * a.ld_q + piece_end(a.d_in)));
+  [[maybe_unused]] const auto ws = buf_rsrc(a.w + uniform((int64_t)n0 * a.ld_w),
+                                            (uint32_t)((have_n - 1) * a.ld_w + piece_end(a.d_in)));
+  [[maybe_unused]] const auto qs =
+      buf_rsrc(a.q, (uint32_t)((a.rows - 1) * a.ld_q + piece_end(a.d_in)));
   // this wave's steps [s0, s1)
   const int steps = (a.d_in + kStreamK - 1) / kStreamK;
   const int s0 = wave * steps / kStreamWaves, s1 = (wave + 1) * steps / kStreamWaves;
