@@ -541,7 +541,8 @@ size_t moe_linear_q8_workspace_bytes(const moe_linear_t* L, int rows);
  *   qs f32 [rows] (device)
  *   y  f32/bf16 [rows][ld_y] (device, out), n_out <= ld_y <= 2^22
  *   ws workspace (device, 16-byte aligned; NULL where 0 bytes are needed)
- * rows >= 0 (0: a no-op), from one decoded token to prefill chunks. */
+ * 0 <= rows < 2^31 - 255 (0: a no-op), from one decoded token to prefill
+ * chunks. */
 int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_q, const float* qs,
                   int rows, void* y, int y_type, int64_t ld_y, void* ws, size_t ws_bytes,
                   void* stream);

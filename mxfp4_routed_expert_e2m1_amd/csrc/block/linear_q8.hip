@@ -498,6 +498,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
 
 // ------------------------------------------------------------- host side
 constexpr int64_t kMaxLd = 1 << 22;  // 256 rows of any operand within 32-bit offsets
+constexpr int kMaxRows = 0x7FFFFFFF - 255;  // the rows of the last tile have numbers too
 
 static int linear_check(const moe_linear_t* L) {
   if (!L || !L->w || !L->w_scales) return MOE_ERR_INVALID_ARG;
@@ -644,6 +645,7 @@ extern "C" int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_
   if (rc != MOE_OK) return rc;
   if (rows < 0 || !type_ok(y_type)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
+  if (rows > kMaxRows) return MOE_ERR_SHAPE;
   if (!q || !qs || !y) return MOE_ERR_INVALID_ARG;
   if (ld_q < L->d_in || ld_y < L->n_out || ld_q > kMaxLd || ld_y > kMaxLd) return MOE_ERR_STRIDE;
   if (!aligned(q, 16) || ld_q % 16 != 0 || !aligned(qs, 4) || !aligned(y, type_size(y_type)))

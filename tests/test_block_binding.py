@@ -317,3 +317,12 @@ def test_descriptors_keep_the_memory_they_were_made_from(lib):
     for d, names in zip(made, fields):
         assert [t.data_ptr() for t in d.tensors] == [getattr(d.c, n) for n in names]
         assert all((t == 0).all() for t in d.tensors)
+
+
+def test_linear_rows_whose_last_tile_passes_31_bits_are_refused():
+    """The library itself: a tile's rows are numbered past the last one, up to 255 further."""
+    A, SHAPE = 0x100000, -2
+    lay = b.moe_linear_t(1, 16, A, 16, A, None)
+    for rows in (2**31 - 255, 2**31 - 100, 2**31 - 1):
+        # (y is misaligned, so that no call gets further than the checks)
+        assert m.lib().moe_linear_q8(lay, A, 16, A, rows, A + 1, 0, 1, A, 1 << 30, None) == SHAPE
