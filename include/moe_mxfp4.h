@@ -421,10 +421,10 @@ typedef struct moe_norm {
  *       MOE_QUANT_ROW    qs f32 [rows], row r's scale at qs[r * ld_qs]
  *       q int8 [rows][ld_q], 8-byte aligned, ld_q % 8 == 0; bytes of a row
  *       past d_model are left alone.  MOE_QUANT_NONE: q and qs are not read.
- * h or codes (or both) must be asked for.  Squares are summed in fp32 in an
- * order set by d_model alone, so a row's bits do not depend on the rows that
- * share a call, on strides or on alignment; |x| up to 2^56 does not
- * overflow.  A row with an infinity or a NaN gives what the formula gives,
+ * h or codes (or both) must be asked for.  Squares are summed in fp32 (the
+ * last additions in fp64) in an order set by d_model alone, so a row's bits do
+ * not depend on the rows that share a call, on strides or on alignment; |x| up
+ * to 2^56 does not overflow.  A row with an infinity or a NaN gives what the formula gives,
  * for that row alone, and its MOE_QUANT_ROW scale is NaN (MOE_QUANT_BLOCK:
  * outside the contract, as in moe_quant_act_q8).  Rows need no alignment
  * beyond their elements' (16 bytes and d_model % 8 == 0 are the fast form).

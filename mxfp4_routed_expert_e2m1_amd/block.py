@@ -177,7 +177,8 @@ def _kept(*tensors):
 # --------------------------------------------------------------------- norms
 class Norm:
     """moe_norm_t with its weights (f32 [d_model] or None): pre_w of the norm
-    before a block, post_w and post_norm of the norm after one."""
+    before a block, post_w and post_norm of the norm after one.  Like the
+    other descriptors it reads its tensors' memory as it was given."""
 
     def __init__(self, d_model, pre_w=None, post_w=None, post_norm=True, eps=1e-6,
                  residual_scale=1.0):

@@ -160,9 +160,12 @@ struct RowsOut {
 };
 typedef u32x4 any_u32x4 __attribute__((aligned(2)));
 
-// STREAM: results of large calls, far more than the L2s hold, are written past
-// them, which leaves the operands there (4096 rows of 14336 x 4096: 239 -> 227
-// us).
+// STREAM: the two larger tiles, whose calls are the larger ones, write their
+// results past the L2s, which leaves the operands there.  Without and with it, us:
+//   rows x channels x codes   the call     with a norm of its results after it
+//   2048 x 4096 x 4096        48.9, 47.4   69.3, 70.1
+//   4096 x 4096 x 4096        73.0, 70.0   113.2, 110.6
+//   4096 x 14336 x 4096       253, 240     419, 417
 template <int TN, bool STREAM, typename T>
 __device__ inline void store_rows(const RowsOut& o, i32x16 (&c)[TN], int t0, int n0, float qs,
                                   const float* ws, const float* bias, T* buf) {
@@ -393,7 +396,9 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a, int spli
 // slot l / 16 and receives token column l % 16, element i at channel row
 // 4 (l / 16) + i.  Piece p of a row sits in LDS at p ^ (row / 2 & 7), so the 16
 // rows of a read lie in different banks.  The waves' sums, exact in int32, meet
-// in LDS at the end.  16 rows of 4096 x 14336 take 11.9 us, 4.9 TB/s.
+// in LDS at the end.  16 rows of 4096 x 14336 take 14.1 us with the weights from
+// memory, 4.2 TB/s (one row 12.6); 11.4 us where they rotate over three sets, which
+// the last-level cache can hold.
 constexpr int kStreamWaves = 4, kStreamK = 128;
 
 __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
@@ -537,7 +542,9 @@ struct LinearPlan {
 static int ceil_div(int64_t a, int b) { return (int)((a + b - 1) / b); }
 
 // Estimated time of `tiles` tiles of `steps` K steps each: full rounds over the
-// chip, then the tiles that are left.
+// chip, then the tiles that are left.  (It orders the tile sizes; it knows nothing
+// of memory, so for few rows, where the weights' bytes take longer, it is less
+// than what the call takes.)
 static double rounds_us(const Tile8& t, int64_t tiles, double steps) {
   const double left = (double)(tiles % kChipCus) / kChipCus;
   const double full = (double)(tiles / kChipCus) * (steps * t.full_us + t.ends_us);
@@ -570,8 +577,17 @@ static LinearPart best_part(int rows, int channels, int d_in, int most_splits, d
 }
 
 // Up to 16 rows the weight stream, unless there are channels enough for small
-// tiles to fill the chip (16 rows of 14336 x 4096: tiles 11.1 us, stream 13.2;
-// one row of 4096 x 4096: 8.2 and 5.8).  Otherwise the best tile; or, where its
+// tiles to fill the chip.  Stream and tiles, weights from memory, us:
+//   channels x codes   1 row        16 rows
+//   4096 x 4096        6.4, 11.2    6.9, 11.5
+//   8192 x 4096        9.4, 13.5    9.9, 12.8
+//   10240 x 4096       12.4, 14.0   13.4, 12.9
+//   12288 x 4096       14.1, 14.5   14.7, 13.8
+//   14336 x 4096       15.4, 15.2   16.9, 14.7
+// The row's length moves the point where they meet, which the rule leaves out: at
+// 1024 codes it is near 8192 channels (10240: 8.0, 5.8), at 14336 codes one row is
+// faster in the stream at 12288 channels too (31.2, 35.8; 16 rows 37.1, 37.0).
+// Otherwise the best tile; or, where its
 // last round would leave much of the chip idle, whole rounds of it and a second
 // launch with the best tile for the channels left.
 constexpr int kStreamRows = 16;

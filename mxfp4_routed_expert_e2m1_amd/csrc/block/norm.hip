@@ -9,10 +9,14 @@
 // One workgroup holds one row in registers, 8 consecutive elements per thread
 // and unit, so every input is read once and every output written once; a row
 // statistic is a sum per thread, per wave, then over the waves through LDS.
-// Few rows are bound by a launch and one memory round trip (one row of 4096:
-// 2.0 us of GPU time; 16 rows after a block, with the next norm and its codes:
-// 3.9 us), many by memory (4096 such rows of 4096: 34.0 us, 4.9 TB/s, a large
-// copy's rate; 26.6 us where the rows are in the last-level cache).
+// Few rows are bound by a launch and one memory round trip (one row of 4096 f32
+// before a block: 2.0 us of GPU time; 16 f32 rows after a block, a gate per
+// channel, with the next norm: 3.9 us), many by memory (4096 rows of 4096, y f32,
+// residual and next norm bf16, a gate per token: 34 us, 4.9 TB/s, a large copy's
+// rate; 26.6 us where the rows are in the last-level cache).  Codes cost a
+// reduction more and their bytes: with the next norm, all f32, 16 rows take 4.1
+// us without codes, 4.9 with a scale per row, 4.6 with one per 32 elements; 4096
+// rows from memory 52.8, 59.0 and 59.2 us (268, 285 and 287 MB).
 #include "block.h"
 
 #include <math.h>
@@ -145,7 +149,8 @@ __device__ inline float stored(float v) {
 // +-127, 0 for d = 0.  The quotient by way of the reciprocal is off by less
 // than 127 * 3 * 2^-24 < 2^-15, so it rounds to the same code unless it lies
 // within 2^-12 of a midpoint; a wave that holds such a value (or a scale whose
-// reciprocal is not safe) divides.  4096 rows of 4096 bf16: 14.8 -> 12.9 us.
+// reciprocal is not safe) divides.  4096 rows of 4096 bf16 in the last-level
+// cache: 14.8 -> 12.9 us.
 __device__ inline u32x2 row_codes(const float (&v)[8], float d) {
   const float inv = 1.0f / d;
   const bool safe = d > 0x1p-100f && d < 0x1p100f;
@@ -538,7 +543,7 @@ extern "C" int moe_quant_row_q8(const void* x, int x_type, int64_t ld_x, int row
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
   const int n = (int)(((int64_t)cols + 7) / 8);
   // (two units per thread keep more loads on their way: 4096 rows of 4096 bf16
-  // 15.7 -> 12.9 us)
+  // in the last-level cache 15.7 -> 12.9 us; from memory it is 15.1)
   const int threads = min(kQuantThreads, ((n + 1) / 2 + 63) / 64 * 64);
   hipStream_t s = (hipStream_t)stream;
   auto go = [&](auto kernel, auto* p) {

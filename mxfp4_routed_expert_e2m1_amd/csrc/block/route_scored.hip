@@ -15,9 +15,11 @@
 // all of it in one workgroup.  Larger ones take two launches: the first
 // counts each expert in every run of rows, the second turns the counts of the
 // earlier runs into first positions and places its own rows, 64 at a time.
-// All of it is bound by latency, of launches and of the picks' chain (0.18 us a
-// pick), not by its bytes: one row of 256 experts, top 6, takes 4.6 us, 777 rows
-// of 160, top 6, 5.3 + 5.7 us, 4096 rows of 256, top 8, 7.6 + 5.8 us.
+// Up to about a thousand rows it is bound by latency, of launches and of the
+// picks' chain (0.18 us a pick), not by its bytes: one row of 256 experts, top 6,
+// takes 4.6 us, 777 rows of 160, top 6, 5.3 + 5.7 us.  At 4096 rows of 256, top 8
+// (7.6 + 5.8 us), four waves share each SIMD in the first launch and the picks'
+// instructions count too.
 #include "block.h"
 
 #include <math.h>
