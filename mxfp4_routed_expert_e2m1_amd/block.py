@@ -374,6 +374,7 @@ def route_outputs(rows, n_experts, top_k, device="cuda"):
 
 
 def moe_route_scored_workspace_bytes(rule, rows):
+    """Bytes that serve moe_route_scored for any number of rows up to `rows`."""
     return int((_lib or _load()).moe_route_scored_workspace_bytes(rule.ref, _int("rows", rows)))
 
 
@@ -475,6 +476,7 @@ class Linear:
 
 
 def moe_linear_q8_workspace_bytes(linear, rows):
+    """Bytes that serve moe_linear_q8 for any number of rows up to `rows`."""
     return int((_lib or _load()).moe_linear_q8_workspace_bytes(linear.ref, _int("rows", rows)))
 
 
