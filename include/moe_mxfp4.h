@@ -547,6 +547,134 @@ int moe_linear_q8(const moe_linear_t* L, const int8_t* q, int64_t ld_q, const fl
                   int rows, void* y, int y_type, int64_t ld_y, void* ws, size_t ws_bytes,
                   void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Attention over a cache held in 4 bits: rotary positions, the cache's writing
+ * and reading, and the attention itself.
+ *
+ * Rows of heads are [rows][n_heads][head_dim] with a stride `ld` between rows
+ * and `hs` between heads, in elements (the channels of a head are contiguous):
+ * a slice of a fused projection's rows, or heads before rows.  With more than
+ * one head hs >= head_dim, with more than one row ld >= head_dim, and neither
+ * runs into the other.  Rows need no alignment beyond their elements'.
+ *
+ * Rotary positions with one or several axes (text: one; images and video:
+ * time, height, width).  Pair i of a head is channels (i, i + rot_dim/2), or
+ * (2i, 2i+1) with `interleaved`; its angle is the position on its axis times
+ * its frequency:
+ *   (a, b) -> scale (a cos - b sin, b cos + a sin)
+ * Channels from rot_dim on are copied.  Frequencies are given as turns per
+ * position in units of 2^-64, round(frequency / (2 pi) 2^64), so that a whole
+ * position times it, modulo 2^64, is the angle to within position * 2^-65
+ * turns, however far the position is. */
+typedef struct moe_rope {
+  int rot_dim;           /* even, >= 2 */
+  int n_axes;            /* 1..8 */
+  int interleaved;       /* 0 or 1 */
+  float scale;           /* finite */
+  const uint64_t* steps; /* [rot_dim/2] (device) */
+  const uint8_t* axes;   /* [rot_dim/2] (device) axis of each pair, < n_axes; NULL: axis 0 */
+} moe_rope_t;
+
+/*   x    f32/bf16 [rows][n_heads][head_dim] (device), rot_dim <= head_dim <= 1024
+ *   pos  int32 [n_axes][ld_pos] (device): any 32-bit value; ld_pos >= rows
+ *        with more than one axis
+ *   out  of x's type (device, out); may be x itself with the same strides
+ * Query and key heads that are neighbours in a fused projection take one call.
+ * One rounding at the end; rows == 0 or n_heads == 0 is a no-op. */
+int moe_rope(const moe_rope_t* R, const void* x, int x_type, int64_t ld_x, int64_t hs_x,
+             int rows, int n_heads, int head_dim, const int32_t* pos, int64_t ld_pos, void* out,
+             int64_t ld_out, int64_t hs_out, void* stream);
+
+/* A cache of keys and values in pages of `page` tokens: per token, head and 32
+ * channels 16 bytes of E2M1 codes and one scale byte u, as the experts' weights
+ * are held.  For the block's largest magnitude amax
+ *   u    = the exponent byte of amax times 2^-2, one more where amax's significand
+ *          is 1.75 or more (so that amax / 2^(u-127) is 3.5..7 and rounds to 4 or
+ *          6), kept in 2..252
+ *   code = the E2M1 value nearest to x / 2^(u-127), ties to the even code,
+ *          at most 6
+ * A block with an infinity or a NaN has u = 255: its 32 channels read as NaN.
+ * What is in the cache can be written again without change.  Slot s of the
+ * cache is token s % page of page s / page. */
+typedef struct moe_kv_cache {
+  int n_heads;  /* key heads, 1..1024 */
+  int head_dim; /* 64, 128 or 256 */
+  int page;     /* 16, 32, 64, 128 or 256 tokens */
+  int n_pages;  /* >= 1, n_pages * page < 2^31 */
+  void* data;   /* moe_kv_cache_bytes() bytes (device, 16-byte aligned), in the library's order */
+} moe_kv_cache_t;
+
+/* Bytes of a cache's data: n_pages * page * n_heads * 2 * (head_dim/2 + head_dim/32); 0 for
+ * sizes that the calls reject (`data` is not looked at). */
+size_t moe_kv_cache_bytes(const moe_kv_cache_t* C);
+
+/* Keys and values of new rows into their slots.
+ *   k, v   f32/bf16 [rows][n_heads][head_dim] (device), one type
+ *   slots  int32 [rows] (device); a row whose slot is negative or past the cache is
+ *          skipped.  Two rows of one call with the same slot leave a mix of both
+ *          in it.
+ * Other slots are left as they are. */
+int moe_kv_write(const moe_kv_cache_t* C, const void* k, int64_t ld_k, int64_t hs_k,
+                 const void* v, int64_t ld_v, int64_t hs_v, int type, int rows,
+                 const int32_t* slots, void* stream);
+
+/* Keys and values of given slots, in any order and as often as wanted:
+ *   k, v  f32/bf16 [rows][n_heads][head_dim] (device, out), one type
+ * A row whose slot is negative or past the cache becomes 0. */
+int moe_kv_read(const moe_kv_cache_t* C, const int32_t* slots, int rows, void* k, int64_t ld_k,
+                int64_t hs_k, void* v, int64_t ld_v, int64_t hs_v, int type, void* stream);
+
+/* Attention of a ragged batch's rows over their sequences' cached tokens.
+ * Query head g reads key head g / (n_heads / cache heads).  A sequence of n
+ * cached tokens and m rows has its rows at the places n - m .. n - 1 (a call
+ * follows the moe_kv_write of its own rows).  Row at place i, token j:
+ *   s    = scale * q . k_j
+ *   s    = softcap * tanh(s / softcap)          (softcap > 0)
+ *   s   -= slopes[head] * |i - j|               (slopes not NULL)
+ *   sees j where j < n, (j <= i or j < prefix), and i - j < window (window > 0)
+ *   out  = sum_j softmax(s)_j v_j over what it sees
+ * A row that sees nothing (a request without tokens, a place below 0 and no
+ * prefix) is 0. */
+typedef struct moe_attn {
+  int n_heads;         /* query heads, a multiple of the cache's heads, <= 65536 */
+  int window;          /* 0: none */
+  float scale;         /* finite */
+  float softcap;       /* 0: none; finite, >= 0 */
+  const float* slopes; /* f32 [n_heads] (device) or NULL */
+} moe_attn_t;
+
+/* Bytes of workspace that serve moe_attn_cache for any number of rows up to
+ * `rows` and sequences up to `n_seqs`: never less for more of either, so one
+ * workspace for the largest batch serves all (0 for sizes that it rejects).
+ * Depends on the current GPU's number of compute units. */
+size_t moe_attn_cache_workspace_bytes(const moe_attn_t* A, const moe_kv_cache_t* C, int rows,
+                                      int n_seqs);
+
+/*   q         f32/bf16 [rows][n_heads][head_dim] (device)
+ *   q_offsets int32 [n_seqs + 1] (device): sequence s has rows q_offsets[s] ..
+ *             q_offsets[s+1] - 1; rows in no sequence are left as they are in
+ *             out.  NULL: one row per sequence, rows == n_seqs.
+ *   kv_lens   int32 [n_seqs] (device): cached tokens, the new rows among them
+ *   table     int32 [n_seqs][ld_table] (device): a sequence's pages in order,
+ *             max_pages <= ld_table of them readable (NULL with 0).  Entries past a
+ *             sequence's last page are not looked at.
+ *   prefix    int32 [n_seqs] (device) or NULL
+ *   out       of q's type (device, out), not q
+ *   ws        workspace (device, 16-byte aligned; NULL where 0 bytes are needed)
+ * Lengths are read on the GPU, so a captured call replays with others.  What
+ * they hold is kept within the arguments: offsets within 0..rows, lengths within
+ * 0..max_pages * page; a token whose table entry is no page of the cache counts as
+ * NaN.  Masked tokens change nothing, whatever the cache holds there.
+ * Scores, softmax and sums are fp32; q is exact (f32: in three bf16 parts), as
+ * the cache's values are; softmax weights enter the second product as bf16 (f32:
+ * in three parts).  rows * (n_heads / cache heads) < 2^28, max_pages * page <
+ * 2^30, n_seqs <= 2^24; rows == 0 or n_seqs == 0 is a no-op. */
+int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, const void* q, int type,
+                   int64_t ld_q, int64_t hs_q, int rows, const int32_t* q_offsets, int n_seqs,
+                   const int32_t* kv_lens, const int32_t* table, int64_t ld_table, int max_pages,
+                   const int32_t* prefix, void* out, int64_t ld_out, int64_t hs_out, void* ws,
+                   size_t ws_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* moe_status_string(int status);
 

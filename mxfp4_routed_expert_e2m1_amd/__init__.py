@@ -13,7 +13,10 @@ import os
 
 import torch
 
-from . import block
+from . import attention, block
+from .attention import (  # noqa: F401
+    Attention, KVCache, Rope, moe_attn_cache, moe_attn_cache_workspace_bytes, moe_kv_read,
+    moe_kv_write, moe_rope)
 from .block import (  # noqa: F401
     Linear, Norm, RouteOutputs, RouterRule, codes_buffer, moe_linear_q8, moe_linear_q8_workspace_bytes,
     moe_norm_post, moe_norm_pre, moe_quant_row_q8, moe_route_scored,
@@ -33,7 +36,7 @@ EXPORTS = [
     "moe_ffn_stages",
     "moe_matvec_mxfp4",
     "moe_debug_block_dots", "moe_status_string",
-] + block.EXPORTS
+] + block.EXPORTS + attention.EXPORTS
 
 MOE_STAGE_GATE_UP, MOE_STAGE_DOWN, MOE_STAGE_ALL, MOE_STAGE_REUSE_ACTS = 1, 2, 3, 4
 
@@ -97,6 +100,7 @@ def lib():
             if f not in ("moe_packed_bytes", "moe_ffn_workspace_bytes", "moe_status_string"):
                 getattr(L, f).restype = I
         block.declare(L)
+        attention.declare(L)
         _lib = L
     return _lib
 
