@@ -13,7 +13,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["status.cpp", "pack.hip", "quant.hip", "route.hip", "ffn.hip", "stream.hip",
            "prefill.hip", "down_rows.hip", "router.hip", "block/norm.hip",
            "block/route_scored.hip", "block/linear_q8.hip", "block/rope.hip",
-           "block/kv_cache.hip", "block/attn.hip"]
+           "block/kv_cache.hip", "block/attn.hip", "block/attn_chunk.hip"]
 # Packed-fp32 VALU ops are disabled: only scalar fp32 FMAs are emitted.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

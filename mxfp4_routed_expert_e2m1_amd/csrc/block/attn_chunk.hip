@@ -1,0 +1,429 @@
+// attn_chunk.hip -- attention of many rows of a sequence over the 4-bit cache, bf16.
+//
+// A workgroup has 32 rows a wave, in 32 x 32 tiles of the matrix core; the tokens pass 128 at a
+// time.  The pass is attn.hip's, in other operands:
+//   scores: the keys' codes and scale bytes go to the scaled instruction as they lie in the cache,
+//     without conversion (32 x 32 x 64: a lane's 32 channels are one block).  The other operand is
+//     q in two E4M3 planes with a scale for 32 channels: q rounded to 4 significant bits, and the
+//     rest, which is exact in 4 more, so the planes hold all 8 bits of a bf16 number (and drop what
+//     lies 2^-22 below the block's largest).  The planes cost what one bf16 product would.
+//   out: a thread turns 4 tokens' codes of D/16 channels into bf16 once for the workgroup, through
+//     LDS, in the order in which the lanes read them as operands.  Two buffers, one barrier per
+//     128 tokens; the reads take half of LDS's rate, where the keys the same way would fill it.
+// A row's base of the exponential is raised when its maximum has grown by 2^8 (or is the first):
+// weights of up to 2^8 are as exact as those up to 1, and the accumulators are rarely rescaled.
+#include "attn.h"
+
+namespace moe {
+
+constexpr int kStage = 128;  // tokens between barriers
+
+__device__ inline float max2(float v) {  // over lanes l and l ^ 32
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ inline float sum2(float v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// 16 channels of a query row in two E4M3 planes, x = 2^(e - 127) (hi + 2^-5 lo), where e puts the
+// largest magnitude of the block (bits `most`) at 128 .. 256.
+__device__ inline int plane_exponent(uint32_t most) {
+  const int e = (int)(most >> 23) - 7;
+  return e < 16 ? 16 : e;
+}
+template <int AT>
+__device__ inline void e4m3_planes(const float (&x)[16], int e, v8i32& hi, v8i32& lo) {
+  const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int h = 0, l = 0;
+    float r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = x[4 * i + k] * down;
+    h = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], h, false);
+    h = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], h, true);
+    r[0] = (r[0] - __builtin_amdgcn_cvt_f32_fp8(h, 0)) * 32.f;
+    r[1] = (r[1] - __builtin_amdgcn_cvt_f32_fp8(h, 1)) * 32.f;
+    r[2] = (r[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 32.f;
+    r[3] = (r[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 32.f;
+    l = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], l, false);
+    l = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], l, true);
+    hi[AT + i] = h;
+    lo[AT + i] = l;
+  }
+}
+__device__ inline uint32_t most_bits(const float (&x)[16]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
+template <int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a) {
+  constexpr int NB = D / 32, NI = (NB + 1) / 2, NC = D / 16, RB = 32 / NC;
+  constexpr int THREADS = 64 * WAVES, PER = kStage * 4 / THREADS;  // quads of a thread per stage
+  constexpr int BUF = kStage * D * 2;
+  typedef uint32_t VRaw __attribute__((ext_vector_type(NB)));
+  constexpr int LD = 33;  // floats of a row in the rows' way out
+  constexpr int OUT = WAVES * 32 * LD * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t vbuf[2 * BUF > OUT ? 2 * BUF : OUT];
+  __shared__ uint32_t over[2][WAVES];
+
+  const int wave = uniform((int)(threadIdx.x >> 6)), lane = lane_id();
+  const int q32 = lane & 31, h = lane >> 5;
+  const int64_t item = blockIdx.x / a.kv_heads;
+  const int kvh = (int)(blockIdx.x - item * a.kv_heads);
+
+  int cut = 0x40000000;
+  Found f;
+  if (a.target) {
+    cut = piece_tokens(a);
+    if (!find_piece(a, cut, item, -1, f)) return;
+  } else {
+    if (!find_tile(a, item, f)) return;
+  }
+  const Seq& sq = f.seq;
+  const int local = (int)(item - f.first_item);
+  // the last rows first: they see the most tokens
+  const int tile = sq.tiles(a) - 1 - local / f.pieces, piece = local % f.pieces;
+  const int rows_here = sq.m * a.group;
+  const int tile0 = tile * a.tile_rows, row0 = tile0 + 32 * wave;
+
+  // this lane's row, and what it sees
+  const int r = row0 + q32;
+  const bool real = r < rows_here;
+  const int tok = (real ? r : 0) / a.group;
+  const int head = kvh * a.group + (real ? r : 0) - tok * a.group;
+  Sight see = sight_of(a, sq, tok);
+  if (!real) see = {0, 0};
+  const float slope = a.slopes && real ? a.slopes[head] * kLog2e : 0.f;
+  const int place = sq.n - sq.m + tok;
+
+  v8i32 qh[NI], ql[NI];
+  int e0[NI], e1[NI];
+  {
+    // an 8-bit operand's lane has channels 16 h .. of both of its blocks, 32 (2i) + and 32 (2i + 1) +
+    const __bf16* qp = (const __bf16*)a.q + (int64_t)(sq.row0 + tok) * a.ld_q + head * a.hs_q + 16 * h;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      int e[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float x[16] = {};
+        if (real) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v[8];
+            to_f32<__bf16>(load8(qp + 32 * (2 * i + b) + 8 * k), v);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[8 * k + n] = v[n];
+          }
+        }
+        const uint32_t own = most_bits(x);
+        const auto other = __builtin_amdgcn_permlane32_swap(own, own, false, false);
+        const uint32_t most = other[0] > other[1] ? other[0] : other[1];
+        e[b] = plane_exponent(most);
+        if (b == 0) e4m3_planes<0>(x, e[b], qh[i], ql[i]);
+        else e4m3_planes<4>(x, e[b], qh[i], ql[i]);
+        if (most >= 0x7F800000u) e[b] = 255;  // infinite or NaN: so are all of its products
+      }
+      e0[i] = h ? e[1] : e[0];
+      e1[i] = e0[i] == 255 ? 255 : e0[i] - 5;
+    }
+  }
+
+  // the tokens of the workgroup's rows, of this wave's, and those that all of the wave's rows see
+  const auto row_sight = [&](int row) {
+    return sight_of(a, sq, (row < rows_here ? row : rows_here - 1) / a.group);
+  };
+  const int64_t p0 = sq.first(a) + (int64_t)piece * cut;
+  const int wg_lo0 = row_sight(tile0).lo, wg_hi0 = row_sight(tile0 + a.tile_rows - 1).hi;
+  const int wg_lo = p0 > wg_lo0 ? (int)p0 : wg_lo0 & ~(kStep - 1);
+  const int wg_hi = p0 + cut < wg_hi0 ? (int)(p0 + cut) : wg_hi0;
+  const bool any = row0 < rows_here;
+  const Sight s0 = row_sight(row0), s1 = row_sight(row0 + 31);
+  const int lo = s0.lo, hi = any ? s1.hi : 0;
+  const int all_lo = s1.lo, all_hi = row0 + 31 < rows_here ? s0.hi : 0;
+
+  const KvUnit<D> unit{1 << a.page_log};
+  const int32_t* pages = a.table + f.at * a.ld_table;
+  const int in_page = (1 << a.page_log) - 1;
+  // a token's piece of the cache; a page that is none: the first, and `bad`
+  const auto piece_of = [&](int page, bool& bad) {
+    bad = page < 0 || page >= a.n_pages;
+    return a.data + ((int64_t)(bad ? 0 : page) * a.kv_heads + kvh) * unit.bytes();
+  };
+  const int last = wg_hi - 1;
+
+  // ---- values: global memory -> registers -> LDS
+  VRaw vr[PER];
+  uint32_t vs[PER];
+  const auto v_load = [&](int t0) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const int id = threadIdx.x + p * THREADS, run = id & 15;
+      int t = t0 + 4 * (id >> 4);
+      t = t < last ? t : last;
+      bool bad;
+      const uint8_t* at = piece_of(pages[t >> a.page_log], bad);
+      const int quad = (t & in_page) >> 2;
+      __builtin_memcpy(&vr[p], at + unit.v_codes() + (quad * 16 + run) * 4 * NB, 4 * NB);
+      __builtin_memcpy(&vs[p], at + unit.v_scales() + (quad * NB + run * NB / 16) * 4, 4);
+    }
+  };
+  // Unit of 16 bytes: 8 tokens of a channel, [block][16 tokens][half of the lanes][32 channels].
+  // Channel j of run o of its block is at place RB j + o, xor a number of the block and half, so
+  // that a wave's 8-byte stores of one j spread over the banks.
+  const auto v_store = [&](int buf) {
+    uint32_t flagged = 0;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const int id = threadIdx.x + p * THREADS, run = id & 15, quad = id >> 4;
+      const int blk = run * NB / 16, o = run % RB;
+      const int s = quad >> 2, hh = quad & 1, half = (quad >> 1) & 1;
+      const uint32_t ov = over_bytes(vs[p]);
+      flagged |= ov;
+      uint32_t sc = vs[p];
+      if (ov) {  // NaN (or, behind the last token, anything): 0 here
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (((sc >> (8 * b)) & 0xFF) > kMaxScaleByte) sc &= ~(0xFFu << (8 * b));
+      }
+      uint8_t* dst = vbuf + buf * BUF + ((blk * (kStage / 16) + s) * 2 + hh) * 512 + half * 8;
+      const int swz = RB * ((2 * blk + hh) & (NC - 1));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int byte = e * NB + b;
+          const uint32_t w = vr[p][byte / 4];
+          const float k = scale_byte(sc, e);
+          bf16x2 y;
+          switch (byte & 3) {
+            case 0: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 0); break;
+            case 1: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 1); break;
+            case 2: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 2); break;
+            default: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 3); break;
+          }
+          x[e] = __builtin_bit_cast(uint32_t, y);
+        }
+        *(u32x2*)(dst + (((RB * 2 * b + o) ^ swz) * 16)) =
+            u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x05040100), __builtin_amdgcn_perm(x[3], x[2], 0x05040100)};
+        *(u32x2*)(dst + (((RB * (2 * b + 1) + o) ^ swz) * 16)) =
+            u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x07060302), __builtin_amdgcn_perm(x[3], x[2], 0x07060302)};
+      }
+    }
+    const bool f2 = __ballot(flagged != 0) != 0;
+    if (lane == 0) over[buf][wave] = f2;
+  };
+
+  // ---- keys: 64 tokens, in registers as they are
+  u32x4 kr[2][NI];
+  uint32_t ks[2][NI];
+  const auto k_load = [&](int t0) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      int t = t0 + 32 * u + q32;
+      t = t < last ? t : last;
+      bool bad;
+      const uint8_t* at = piece_of(pages[t >> a.page_log], bad);
+      const int in = t & in_page;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        __builtin_memcpy(&kr[u][i], at + in * (D / 2) + 16 * (2 * i + h), 16);
+        const uint32_t b = at[unit.k_scales() + in * NB + 2 * i + h];
+        ks[u][i] = bad || b > kMaxScaleByte ? 255u : b;
+      }
+    }
+  };
+
+  float m = -__builtin_inff(), l = 0.f;
+  f32x16 acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = f32x16{};
+
+  const bool plain = a.softcap == 0.f && !a.slopes && a.scale > 0.f;
+  const float qk_scale = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
+  const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+  const float unit_scale = plain ? qk_scale : 1.f;
+
+  if (wg_lo < wg_hi) {
+    v_load(wg_lo);
+    v_store(0);
+    lds_barrier();
+  }
+  int buf = 0;
+  for (int t0 = wg_lo; t0 < wg_hi; t0 += kStage, buf ^= 1) {
+    const bool more = t0 + kStage < wg_hi;
+    if (more) v_load(t0 + kStage);
+    uint32_t nan_here = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) nan_here |= over[buf][w];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int t = t0 + 64 * half;
+      if (t >= hi || t + 64 <= lo || t >= wg_hi) continue;
+      k_load(t);
+      // ---- scores
+      f32x16 s[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        s[u] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const v8i32 k = {(int)kr[u][i][0], (int)kr[u][i][1], (int)kr[u][i][2], (int)kr[u][i][3], 0, 0, 0, 0};
+          s[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, qh[i], s[u], 4, 0, 0, (int)ks[u][i], 0, e0[i]);
+          s[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, ql[i], s[u], 4, 0, 0, (int)ks[u][i], 0, e1[i]);
+        }
+      }
+      if (!plain) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x = s[u][e] * qk_scale;
+            if (a.softcap > 0.f) x = capped(x, a.softcap, inv_cap) * kLog2e;
+            const int j = t + 32 * u + 8 * (e >> 2) + 4 * h + (e & 3);
+            if (a.slopes) x -= slope * (float)abs(place - j);
+            s[u][e] = x;
+          }
+      }
+      if (t < all_lo || t + 64 > all_hi) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = t + 32 * u + 8 * (e >> 2) + 4 * h + (e & 3);
+            s[u][e] = j >= see.lo && j < see.hi ? s[u][e] : -__builtin_inff();
+          }
+      }
+      // ---- softmax
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
+      top = max2(top) * unit_scale;
+      if (__ballot(top > m + 8.f)) {
+        const float next = fmaxf(m, top);
+        const float base = next == -__builtin_inff() ? 0.f : next;
+        const float old = exp2_fast(m - base);
+        l *= old;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[b][e] *= old;
+        m = next;
+      }
+      const float base = m == -__builtin_inff() ? 0.f : m;
+      bf16x8 p[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float w = exp2_fast(fmaf(s[u][e], unit_scale, -base));
+          l += w;
+          p[2 * u + (e >> 3)][e & 7] = (__bf16)w;
+        }
+      // ---- values that are NaN: in the channels of the rows that see them
+      if (nan_here) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            bf16x8 nan, seen;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              int j = t + 16 * c + 8 * (e >> 2) + 4 * h + (e & 3);
+              seen[e] = (__bf16)(j >= see.lo && j < see.hi ? 1.f : 0.f);
+              j = j < last ? j : last;
+              bool bad;
+              const uint8_t* at = piece_of(pages[j >> a.page_log], bad);
+              const int quad = (j & in_page) >> 2;
+              const uint32_t u = at[unit.v_scales() + (quad * NB + b) * 4 + (j & 3)];
+              nan[e] = (__bf16)(u > kMaxScaleByte ? 1.f : 0.f);
+            }
+            f32x16 n = {};
+            n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(nan, seen, n, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (n[e] > 0.f) acc[b][e] = __builtin_nanf("");
+          }
+      }
+      // ---- out
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int swz = RB * ((2 * b + h) & (NC - 1));
+          const bf16x8 v = *(const bf16x8*)(vbuf + buf * BUF + ((b * (kStage / 16) + 4 * half + c) * 2 + h) * 512 + (q32 ^ swz) * 16);
+          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[c], acc[b], 0, 0, 0);
+        }
+    }
+    if (more) v_store(buf ^ 1);
+    lds_barrier();
+  }
+  l = sum2(l);
+
+  // ---- rows out: through LDS, a block of channels at a time, so that they leave in order
+  const bool sees = see.lo < see.hi;
+  const bool part = f.pieces > 1;
+  const float inv = part ? 1.f : sees ? 1.f / l : 0.f;
+  const int64_t slot0 = ((int64_t)item * a.kv_heads + kvh) * a.tile_rows + 32 * wave;
+  if (part && real && h == 0) {
+    a.part[a.ml_at + 2 * (slot0 + q32)] = m;
+    a.part[a.ml_at + 2 * (slot0 + q32) + 1] = l;
+  }
+  float* mine = (float*)vbuf + wave * 32 * LD;
+  const int orow = lane >> 1, oc = (lane & 1) * 16;
+  const int orr = row0 + orow, otok = (orr < rows_here ? orr : 0) / a.group;
+  const int ohead = kvh * a.group + (orr < rows_here ? orr : 0) - otok * a.group;
+  __bf16* dst = (__bf16*)a.out + (int64_t)(sq.row0 + otok) * a.ld_out + ohead * a.hs_out + oc;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int place_in = 8 * (e >> 2) + 4 * h + (e & 3);  // RB j + o
+      const int ch = (place_in % RB) * NC + place_in / RB;
+      mine[q32 * LD + ch] = part ? acc[b][e] : sees ? acc[b][e] * inv : 0.f;
+    }
+    __builtin_amdgcn_wave_barrier();
+    float o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = mine[orow * LD + oc + i];
+    __builtin_amdgcn_wave_barrier();
+    if (orr < rows_here) {
+      if (part) {
+        __builtin_memcpy(a.part + (slot0 + orow) * D + 32 * b + oc, o, sizeof(o));
+      } else {
+        __bf16 res[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) res[i] = (__bf16)o[i];
+        __builtin_memcpy(dst + 32 * b, res, sizeof(res));
+      }
+    }
+  }
+}
+
+template <int D, int WAVES>
+static void launch_one(const AttnArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((attn_chunk_kernel<D, WAVES>), dim3((unsigned)(a.items * a.kv_heads)),
+                     dim3(64 * WAVES), 0, stream, a);
+}
+
+void attn_chunk_launch(const AttnArgs& a, int head_dim, int waves, hipStream_t stream) {
+  switch (head_dim) {
+    case 64: waves == 8 ? launch_one<64, 8>(a, stream) : launch_one<64, 4>(a, stream); break;
+    case 128: waves == 8 ? launch_one<128, 8>(a, stream) : launch_one<128, 4>(a, stream); break;
+    default: launch_one<256, 4>(a, stream); break;
+  }
+}
+
+}  // namespace moe
