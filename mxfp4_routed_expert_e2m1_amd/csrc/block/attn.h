@@ -7,8 +7,7 @@
 namespace moe {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kStep = 64;       // tokens of an iteration
-constexpr int kLeastPart = 256; // tokens that are worth a workgroup: an iteration for each wave
+constexpr int kStep = 64;  // tokens to which pieces and the start of a pass are aligned
 
 struct AttnArgs {
   const void* q;
@@ -25,6 +24,7 @@ struct AttnArgs {
   int rows, n_seqs, n_heads, kv_heads, group, page_log, n_pages, max_pages, window;
   int target;    // pieces that fill the chip (0: tokens are not cut)
   int64_t items; // of the grid
+  int quantum;   // tokens of a piece: a multiple of this
   int tile_rows; // rows of a tile
   float scale, softcap;
 };
@@ -57,35 +57,6 @@ struct Seq {
     return (int)(((int64_t)m * a.group + a.tile_rows - 1) / a.tile_rows);
   }
 };
-
-__device__ inline int64_t wave_sum_i64(int64_t v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
-// Tokens of a piece: all of them, or as many as cut the batch's work into `target` pieces.
-__device__ inline int piece_tokens(const AttnArgs& a) {
-  int64_t work = 0;
-  for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
-    const int s = s0 + lane_id();
-    if (s < a.n_seqs) {
-      Seq q;
-      q.load(a, s);
-      work += (int64_t)q.tiles(a) * (q.n - q.first(a));
-    }
-  }
-  work = wave_sum_i64(work);
-  int64_t c = (work + a.target - 1) / a.target;
-  c = (c + kStep - 1) / kStep * kStep;
-  c = c < kLeastPart ? kLeastPart : c > 0x40000000 ? 0x40000000 : c;
-  return uniform((int)c);
-}
-
-__device__ inline int pieces_of(const AttnArgs& a, const Seq& s, int cut) {
-  const int span = s.n - s.first(a);
-  return span <= cut ? 1 : (span + cut - 1) / cut;
-}
 
 // A sequence, its place in the batch, and where its items (pieces of tiles) begin.
 struct Found {
@@ -126,22 +97,59 @@ __device__ inline bool find_tile(const AttnArgs& a, int64_t item, Found& f) {
   return item >= f.first_item && item - f.first_item < f.seq.tiles(a);
 }
 
-// Cut calls (few tiles, so few sequences): items are counted over the sequences.  The sequence of
-// an item, or with `row` >= 0 of that row.
-constexpr int kMostItems = 1 << 24;  // of one sequence (offsets that overlap could make it more)
-__device__ inline bool find_piece(const AttnArgs& a, int cut, int64_t item, int row, Found& f) {
-  int64_t before = 0;
-  for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
-    const int s = s0 + lane_id();
-    Seq q = {0, 0, 0, 0};
-    int pieces = 1, items = 0;
-    if (s < a.n_seqs) {
-      q.load(a, s);
-      pieces = pieces_of(a, q, cut);
-      const int64_t all = (int64_t)q.tiles(a) * pieces;
-      items = all < kMostItems ? (int)all : kMostItems;
+__device__ inline int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_incl_scan(v), 63); }
+
+// Cut calls (few tiles, so few sequences): a piece has `cut` tokens, as many for every sequence, and
+// items are counted over the sequences.  The cut is the batch's work over `target` pieces where
+// that makes no more than `target` of them (a sequence's last piece is a whole one there), or over
+// fewer pieces by half a piece, or a whole one, for each tile.  Finds the sequence of an item, or
+// with `row` >= 0 of that row.  (Counts of one sequence are kept below 2^24 or 2^25, so that offsets
+// that overlap cannot make a sum of 64 overflow.)
+__device__ inline bool find_piece(const AttnArgs& a, int64_t item, int row, Found& f, int& cut) {
+  const int lane = lane_id();
+  Seq q = {0, 0, 0, 0};
+  int tiles = 0, span = 0;
+  const auto take = [&](int s0) {
+    q = {0, 0, 0, 0};
+    tiles = span = 0;
+    if (s0 + lane < a.n_seqs) {
+      q.load(a, s0 + lane);
+      tiles = q.tiles(a);
+      tiles = tiles < (1 << 24) ? tiles : 1 << 24;
+      span = q.n - q.first(a);
     }
-    const int scan = wave_incl_scan(items);
+  };
+  const auto steps = [&] {
+    const int64_t w = (int64_t)tiles * ((span + kStep - 1) / kStep);
+    return w < (1 << 25) ? (int)w : (1 << 25) - 1;
+  };
+  const auto items_of = [&](int pieces) {
+    const int64_t n = (int64_t)tiles * pieces;
+    return n < (1 << 24) ? (int)n : 1 << 24;
+  };
+  take(0);
+  int64_t work = wave_sum(steps()), all = wave_sum(tiles);
+  const bool one = a.n_seqs <= 64;
+  if (!one) {
+    for (int s0 = 64; s0 < a.n_seqs; s0 += 64) {
+      take(s0);
+      work += wave_sum(steps());
+      all += wave_sum(tiles);
+    }
+    take(0);
+  }
+  for (int k = one ? 0 : 2;; ++k) {
+    int64_t over = a.target - all * k / 2;
+    over = over > a.target / 2 ? over : a.target / 2 > 0 ? a.target / 2 : 1;
+    int64_t c = (work * kStep + over - 1) / over;
+    c = (c + a.quantum - 1) / a.quantum * a.quantum;
+    cut = uniform((int)(c < a.quantum ? a.quantum : c > 0x40000000 ? 0x40000000 : c));
+    if (k == 2 || wave_sum(items_of(span <= cut ? 1 : (span + cut - 1) / cut)) <= a.target) break;
+  }
+  int64_t before = 0;
+  for (int s0 = 0;;) {
+    const int pieces = span <= cut ? 1 : (span + cut - 1) / cut;
+    const int items = items_of(pieces), scan = wave_incl_scan(items);
     const int64_t end = before + scan;
     const bool mine = row >= 0 ? row >= q.row0 && row < q.row0 + q.m : item < end && item >= end - items;
     const uint64_t who = __ballot(mine);
@@ -157,8 +165,16 @@ __device__ inline bool find_piece(const AttnArgs& a, int cut, int64_t item, int 
       return true;
     }
     before += __builtin_amdgcn_readlane(scan, 63);
+    s0 += 64;
+    if (s0 >= a.n_seqs) return false;
+    take(s0);
   }
-  return false;
+}
+
+// The item of a workgroup (false: there is none), the tokens of a piece.
+__device__ inline bool find_item(const AttnArgs& a, int64_t item, Found& f, int& cut) {
+  cut = 0x40000000;
+  return a.target ? find_piece(a, item, -1, f, cut) : find_tile(a, item, f);
 }
 
 // The tokens that a row sees: lo <= j < hi.
@@ -224,6 +240,43 @@ __device__ inline void split(float x, __bf16 (&p)[PARTS]) {
     p[1] = (__bf16)r;
     p[2] = (__bf16)(r - (float)p[1]);
   }
+}
+
+// 16 channels of a query row in two E4M3 planes, x = 2^(e - 127) (hi + 2^-5 lo), where e puts the
+// largest magnitude of the block (bits `most`) at 128 .. 256.
+__device__ inline int plane_exponent(uint32_t most) {
+  const int e = (int)(most >> 23) - 7;
+  return e < 16 ? 16 : e;
+}
+template <int AT>
+__device__ inline void e4m3_planes(const float (&x)[16], int e, v8i32& hi, v8i32& lo) {
+  const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int h = 0, l = 0;
+    float r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = x[4 * i + k] * down;
+    h = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], h, false);
+    h = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], h, true);
+    r[0] = (r[0] - __builtin_amdgcn_cvt_f32_fp8(h, 0)) * 32.f;
+    r[1] = (r[1] - __builtin_amdgcn_cvt_f32_fp8(h, 1)) * 32.f;
+    r[2] = (r[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 32.f;
+    r[3] = (r[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 32.f;
+    l = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], l, false);
+    l = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], l, true);
+    hi[AT + i] = h;
+    lo[AT + i] = l;
+  }
+}
+__device__ inline uint32_t most_bits(const float (&x)[16]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 // 256 rows or fewer of a sequence and one key head at a time, bf16 (attn_chunk.hip).

@@ -29,27 +29,31 @@
 namespace moe {
 
 // ------------------------------------------------------------------- the pass
-// SHARED: the four waves of a workgroup have one tile of 16 NQ rows and take its tokens in turn,
-// joined in LDS at the end; otherwise each wave has a tile of its own among the workgroup's 64 NQ.
-template <typename T, int D, int NQ, bool SHARED>
-__global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
-  constexpr int NB = D / 32, NC = D / 16, PARTS = sizeof(T) == 4 ? 3 : 1;
-  constexpr int SUB = kStep / 16;
-  typedef uint32_t KRaw __attribute__((ext_vector_type(NB)));
+// SHARED: the waves of a workgroup have one tile of 16 NQ rows and take its tokens in turn, 32 each,
+// joined in LDS at the end; otherwise each wave has a tile of its own among the workgroup's.
+// A wave's next 32 tokens are on their way from memory while it works on 32.
+constexpr int resident(bool f32, int dim, int nq) {  // workgroups of 4 waves that a CU holds
+  if (dim == 256) return 1;
+  if (dim == 128) return f32 ? 2 : nq == 1 ? 3 : 1;
+  return f32 ? 3 : nq == 1 ? 4 : 2;
+}
+template <typename T, int D, int NQ, int WAVES, bool SHARED>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D, NQ) : 1) void attn_rows_kernel(const AttnArgs a) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int NB = D / 32, NC = D / 16, NI = (D + 127) / 128, PARTS = F32 ? 3 : 1;
+  constexpr int STEP = 32, STRIDE = SHARED ? STEP * WAVES : STEP;
+  typedef uint32_t VRaw __attribute__((ext_vector_type(NB)));
   const int wave = uniform((int)(threadIdx.x >> 6)), lane = lane_id();
   const int r16 = lane & 15, g = lane >> 4;
-  const int kvh = blockIdx.y;
+  const int64_t item = blockIdx.x / a.kv_heads;
+  const int kvh = (int)(blockIdx.x - item * a.kv_heads);
 
-  int cut = 0x40000000;
+  int cut;
   Found f;
-  if (a.target) {
-    cut = piece_tokens(a);
-    if (!find_piece(a, cut, blockIdx.x, -1, f)) return;
-  } else {
-    if (!find_tile(a, blockIdx.x, f)) return;
-  }
+  if (!find_item(a, item, f, cut)) return;
   const Seq& sq = f.seq;
-  const int local = (int)(blockIdx.x - f.first_item);
+  const int local = (int)(item - f.first_item);
+  // the last rows first: they see the most tokens
   const int tile = sq.tiles(a) - 1 - local / f.pieces, piece = local % f.pieces;
   const int trow0 = tile * a.tile_rows + (SHARED ? 0 : wave * 16 * NQ);
   const int rows_here = sq.m * a.group;  // (row, head) pairs of the sequence and key head
@@ -59,7 +63,12 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
   bool real[NQ];
   Sight see[NQ];
   float slope[NQ];
-  bf16x8 q[NQ][PARTS][NB];
+  // q as the matrix core takes it: bf16 calls in two E4M3 planes (128 channels an instruction, of
+  // which a lane has 16 g .. and 64 + 16 g ..), f32 calls in three bf16 parts (32 channels, 8 of
+  // each of a lane's blocks 4 i + g)
+  v8i32 qh[NQ][NI], ql[NQ][NI];
+  int e0[NQ][NI], e1[NQ][NI];
+  bf16x8 q[NQ][NI][4][PARTS];
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) {
     const int r = trow0 + 16 * nq + r16;
@@ -70,31 +79,66 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
     see[nq] = sight_of(a, sq, tok[nq]);
     if (!real[nq]) see[nq] = {0, 0};
     slope[nq] = a.slopes && real[nq] ? a.slopes[head[nq]] * kLog2e : 0.f;
-    const T* qp = (const T*)a.q + (sq.row0 + tok[nq]) * a.ld_q + head[nq] * a.hs_q;
+    const T* qp = (const T*)a.q + (int64_t)(sq.row0 + tok[nq]) * a.ld_q + head[nq] * a.hs_q;
+    if constexpr (F32) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      float v[8] = {};
-      if (real[nq]) to_f32<T>(load8(qp + 8 * (g * NB + i)), v);
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        __bf16 p[PARTS];
-        split<PARTS>(v[e], p);
+        for (int n = 0; n < 4; ++n) {
+          float v[8] = {};
+          const int c = 32 * (4 * i + g) + 8 * n;
+          if (real[nq] && c < D) to_f32<T>(load8(qp + c), v);
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) q[nq][k][i][e] = p[k];
+          for (int e = 0; e < 8; ++e) {
+            __bf16 p[PARTS];
+            split<PARTS>(v[e], p);
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) q[nq][i][n][k][e] = p[k];
+          }
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        int e[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float x[16] = {};
+          const int c = 128 * i + 64 * b + 16 * g;
+          if (real[nq] && c < D) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float v[8];
+              to_f32<T>(load8(qp + c + 8 * k), v);
+#pragma unroll
+              for (int n = 0; n < 8; ++n) x[8 * k + n] = v[n];
+            }
+          }
+          const uint32_t own = most_bits(x);  // (half of block 4 i + 2 b + g / 2)
+          const auto other = __builtin_amdgcn_permlane16_swap(own, own, false, false);
+          const uint32_t most = other[0] > other[1] ? other[0] : other[1];
+          e[b] = plane_exponent(most);
+          if (b == 0) e4m3_planes<0>(x, e[b], qh[nq][i], ql[nq][i]);
+          else e4m3_planes<4>(x, e[b], qh[nq][i], ql[nq][i]);
+          if (most >= 0x7F800000u) e[b] = 255;  // infinite or NaN: so are all of its products
+        }
+        // the scale of block 4 i + g goes with lanes g
+        const int first = __shfl(e[0], r16 + 32 * (g & 1)), second = __shfl(e[1], r16 + 32 * (g & 1));
+        e0[nq][i] = g < 2 ? first : second;
+        e1[nq][i] = e0[nq][i] == 255 ? 255 : e0[nq][i] - 5;
       }
     }
   }
 
-  // the tile's tokens: what its first row (window) and its last (causal) see
-  const int last_row = trow0 + 16 * NQ - 1 < rows_here - 1 ? trow0 + 16 * NQ - 1 : rows_here - 1;
+  // the tile's tokens: what its first row (window) and its last (causal) see, and all of them
+  const auto row_sight = [&](int row) {
+    return sight_of(a, sq, (row < rows_here ? row : rows_here - 1) / a.group);
+  };
   const bool any = trow0 < rows_here;
-  const Sight s0 = sight_of(a, sq, any ? trow0 / a.group : 0);
-  const Sight s1 = sight_of(a, sq, any ? last_row / a.group : 0);
-  // (rows all see what lies in [s1.lo, s0.hi))
+  const Sight s0 = row_sight(any ? trow0 : 0), s1 = row_sight(trow0 + 16 * NQ - 1);
   const int64_t p0 = sq.first(a) + (int64_t)piece * cut;
-  int lo = p0 > s0.lo ? (int)p0 : s0.lo & ~(kStep - 1);
-  int hi = p0 + cut < s1.hi ? (int)(p0 + cut) : s1.hi;
-  if (!any) hi = lo;
+  const int lo = p0 > s0.lo ? (int)p0 : s0.lo & ~(kStep - 1);
+  const int hi = !any ? 0 : p0 + cut < s1.hi ? (int)(p0 + cut) : s1.hi;
+  const int all_lo = s1.lo, all_hi = s0.hi;
 
   float m[NQ], l[NQ];
   f32x4 acc[NQ][NC];
@@ -108,193 +152,242 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
 
   const KvUnit<D> unit{1 << a.page_log};
   const int32_t* pages = a.table + f.at * a.ld_table;
+  const bool plain = a.softcap == 0.f && !a.slopes && a.scale > 0.f;
   const float qk_scale = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
   const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+  const float unit_scale = plain ? qk_scale : 1.f;
 
-  for (int t0 = lo + (SHARED ? wave * kStep : 0); t0 < hi; t0 += SHARED ? 4 * kStep : kStep) {
-    // ---- loads
-    KRaw kr[SUB];
-    uint32_t ks[SUB][NB > 4 ? 2 : 1];
-    KRaw vr[SUB];
-    uint32_t vs[SUB];
-    bool bad[SUB];
+  // 16 tokens lie in one page; those past the last are taken as the last 16 and masked
+  struct Raw {
+    u32x4 k[2][NI];
+    uint32_t ks[2][NI];
+    VRaw v[2];
+    uint32_t vs[2];
+  };
+  const int last16 = (hi - 1) & ~15;
+  const auto sub_of = [&](int t, int u) { return t + 16 * u < last16 ? t + 16 * u : last16; };
+  const auto page_of = [&](int t, int u) { return uniform(pages[sub_of(t, u) >> a.page_log]); };
+  const uint32_t k_off = r16 * (D / 2) + (D == 64 ? (g & 1) : g) * 16;
+  const uint32_t ks_off = unit.k_scales() + r16 * NB + (D == 64 ? (g & 1) : g);
+  const uint32_t v_off = unit.v_codes() + (g * 16 + r16) * 4 * NB;
+  const uint32_t vs_off = unit.v_scales() + (g * NB + r16 * NB / 16) * 4;
+  const auto load = [&](Raw& w, int t, int pg0, int pg1) {
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      const int t = t0 + 16 * u;
-      bad[u] = false;
-      kr[u] = KRaw{};
-      vr[u] = KRaw{};
-      vs[u] = 0;
-      ks[u][0] = 0;
-      if constexpr (NB > 4) ks[u][1] = 0;
-      if (t < hi) {
-        int pg = uniform(pages[t >> a.page_log]);
-        bad[u] = pg < 0 || pg >= a.n_pages;
-        pg = bad[u] ? 0 : pg;
-        const uint8_t* at = a.data + ((int64_t)pg * a.kv_heads + kvh) * unit.bytes();
-        const int in = t & ((1 << a.page_log) - 1);
-        __builtin_memcpy(&kr[u], at + (in + r16) * (D / 2) + g * (4 * NB), 4 * NB);
-        const uint8_t* sc = at + unit.k_scales() + (in + r16) * NB;
-        if constexpr (NB == 2) ks[u][0] = sc[g >> 1];
-        if constexpr (NB == 4) ks[u][0] = sc[g];
-        if constexpr (NB == 8) {
-          ks[u][0] = sc[2 * g];
-          ks[u][1] = sc[2 * g + 1];
-        }
-        const int quad = (in >> 2) + g;
-        __builtin_memcpy(&vr[u], at + unit.v_codes() + (quad * 16 + r16) * 4 * NB, 4 * NB);
-        __builtin_memcpy(&vs[u], at + unit.v_scales() + (quad * NB + r16 * NB / 16) * 4, 4);
+    for (int u = 0; u < 2; ++u) {
+      const int pg = u ? pg1 : pg0;
+      const bool bad = pg < 0 || pg >= a.n_pages;
+      const int in = sub_of(t, u) & ((1 << a.page_log) - 1);
+      const uint8_t* at = a.data + ((int64_t)(bad ? 0 : pg) * a.kv_heads + kvh) * unit.bytes();
+      const uint8_t* kc = at + in * (D / 2);
+      const uint8_t* sc = at + in * NB;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        __builtin_memcpy(&w.k[u][i], kc + k_off + 64 * i, 16);
+        const uint32_t b = sc[ks_off + 4 * i];
+        w.ks[u][i] = bad ? 255u : b;
       }
+      __builtin_memcpy(&w.v[u], kc + v_off, 4 * NB);
+      __builtin_memcpy(&w.vs[u], sc + vs_off, 4);
+    }
+  };
+
+  int t = lo + (SHARED ? wave * STEP : 0);
+  Raw raw;
+  int pg0 = 0, pg1 = 0;
+  if (t < hi) {
+    load(raw, t, page_of(t, 0), page_of(t, 1));
+    pg0 = page_of(t + STRIDE, 0);
+    pg1 = page_of(t + STRIDE, 1);
+  }
+  for (; t < hi; t += STRIDE) {
+    Raw next = raw;
+    if (t + STRIDE < hi) {
+      load(next, t + STRIDE, pg0, pg1);
+      pg0 = page_of(t + 2 * STRIDE, 0);
+      pg1 = page_of(t + 2 * STRIDE, 1);
     }
 
     // ---- scores
-    float s[NQ][SUB][4];
+    float s[NQ][2][4];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
+    for (int u = 0; u < 2; ++u) {
       f32x4 c[NQ];
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) c[nq] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const uint32_t sb = ks[u][NB > 4 ? i / 4 : 0];
-        bf16x8 k = fp4x8_to_bf16x8(kr[u][i], __uint_as_float(sb << 23));
-        if (sb > kMaxScaleByte || bad[u]) {
+      for (int i = 0; i < NI; ++i) {
+        const u32x4 kk = raw.k[u][i];
+        const uint32_t sb = raw.ks[u][i];
+        if constexpr (F32) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) k[e] = (__bf16)__builtin_nanf("");
+          for (int n = 0; n < 4; ++n) {
+            bf16x8 k = fp4x8_to_bf16x8(kk[n], __uint_as_float(sb << 23));
+            if (sb > kMaxScaleByte) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) k[e] = (__bf16)__builtin_nanf("");
+            }
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+              for (int p = 0; p < PARTS; ++p)
+                c[nq] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[nq][i][n][p], c[nq], 0, 0, 0);
+          }
+        } else {
+          const v8i32 k = {(int)kk[0], (int)kk[1], (int)kk[2], (int)kk[3], 0, 0, 0, 0};
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq) {
+            c[nq] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, qh[nq][i], c[nq], 4, 0, 0, (int)sb, 0, e0[nq][i]);
+            c[nq] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, ql[nq][i], c[nq], 4, 0, 0, (int)sb, 0, e1[nq][i]);
+          }
         }
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p)
-            c[nq] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[nq][p][i], c[nq], 0, 0, 0);
       }
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = c[nq][e] * qk_scale;
-          if (a.softcap > 0.f) x = capped(x, a.softcap, inv_cap) * kLog2e;
-          const int j = t0 + 16 * u + 4 * g + e;
-          if (a.slopes) x -= slope[nq] * (float)abs(sq.n - sq.m + tok[nq] - j);
-          s[nq][u][e] = j >= see[nq].lo && j < see[nq].hi ? x : -__builtin_inff();
-        }
+        for (int e = 0; e < 4; ++e) s[nq][u][e] = c[nq][e];
+    }
+    if (!plain) {
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = s[nq][u][e] * qk_scale;
+            if (a.softcap > 0.f) x = capped(x, a.softcap, inv_cap) * kLog2e;
+            const int j = t + 16 * u + 4 * g + e;
+            if (a.slopes) x -= slope[nq] * (float)abs(sq.n - sq.m + tok[nq] - j);
+            s[nq][u][e] = x;
+          }
+    }
+    if (t < all_lo || t + STEP > all_hi) {
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = t + 16 * u + 4 * g + e;
+            s[nq][u][e] = j >= see[nq].lo && j < see[nq].hi ? s[nq][u][e] : -__builtin_inff();
+          }
     }
 
     // ---- values that are NaN (or, behind the last token, anything): 0 in the product, and NaN
     // in the channels of the rows that see them
-    uint32_t over = 0;
+    if (__ballot((over_bytes(raw.vs[0]) | over_bytes(raw.vs[1])) != 0)) {
+      bf16x8 nan;
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) over |= over_bytes(vs[u]);
-    if (__ballot(over != 0)) {
+      for (int e = 0; e < 8; ++e)
+        nan[e] = (__bf16)(((raw.vs[e / 4] >> (8 * (e & 3))) & 0xFF) > kMaxScaleByte ? 1.f : 0.f);
 #pragma unroll
-      for (int h = 0; h < SUB / 2; ++h) {
-        bf16x8 nan;
+      for (int nq = 0; nq < NQ; ++nq) {
+        bf16x8 seen;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int u = 2 * h + e / 4;
-          nan[e] = (__bf16)(((vs[u] >> (8 * (e & 3))) & 0xFF) > kMaxScaleByte ? 1.f : 0.f);
+          const int j = t + 16 * (e / 4) + 4 * g + (e & 3);
+          seen[e] = (__bf16)(j >= see[nq].lo && j < see[nq].hi ? 1.f : 0.f);
         }
+        f32x4 c = {0.f, 0.f, 0.f, 0.f};
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nan, seen, c, 0, 0, 0);
+        // (c: of the runs of channels 4g + e, which a block's scale covers whole)
 #pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-          bf16x8 seen;
+        for (int e = 0; e < 4; ++e)
+          if (c[e] > 0.f) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int u = 2 * h + e / 4, j = t0 + 16 * u + 4 * g + (e & 3);
-            seen[e] = (__bf16)(j >= see[nq].lo && j < see[nq].hi ? 1.f : 0.f);
+            for (int j = 0; j < NC; ++j) acc[nq][j][e] = __builtin_nanf("");
           }
-          f32x4 c = {0.f, 0.f, 0.f, 0.f};
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nan, seen, c, 0, 0, 0);
-          // (c: of the runs of channels 4g + e, which a block's scale covers whole)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c[e] > 0.f) {
-#pragma unroll
-              for (int j = 0; j < NC; ++j) acc[nq][j][e] = __builtin_nanf("");
-            }
-        }
       }
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          if (((vs[u] >> (8 * b)) & 0xFF) > kMaxScaleByte) vs[u] &= ~(0xFFu << (8 * b));
+          if (((raw.vs[u] >> (8 * b)) & 0xFF) > kMaxScaleByte) raw.vs[u] &= ~(0xFFu << (8 * b));
     }
 
-    // ---- softmax
-    bf16x8 p[NQ][PARTS][SUB / 2];
+    // ---- softmax.  A row's base is raised when its maximum has grown by 2^8 (or is the first):
+    // weights of up to 2^8 are as exact as those up to 1.
+    bf16x8 p[NQ][PARTS];
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
-      float top = m[nq];
+      float top = -__builtin_inff();
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = fmaxf(top, s[nq][u][e]);
-      top = max16(top);
-      const float base = top == -__builtin_inff() ? 0.f : top;
-      const float old = exp2_fast(m[nq] - base);
-      if (__ballot(top > m[nq])) {
+      top = max16(top) * unit_scale;
+      if (__ballot(top > m[nq] + 8.f)) {
+        const float up = fmaxf(m[nq], top);
+        const float old = exp2_fast(m[nq] - (up == -__builtin_inff() ? 0.f : up));
         l[nq] *= old;
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[nq][j][e] *= old;
+        m[nq] = up;
       }
-      m[nq] = top;
+      const float base = m[nq] == -__builtin_inff() ? 0.f : m[nq];
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float w = exp2_fast(s[nq][u][e] - base);
+          const float w = exp2_fast(fmaf(s[nq][u][e], unit_scale, -base));
           l[nq] += w;
           __bf16 part[PARTS];
           split<PARTS>(w, part);
 #pragma unroll
-          for (int k = 0; k < PARTS; ++k) p[nq][k][u / 2][(u & 1) * 4 + e] = part[k];
+          for (int k = 0; k < PARTS; ++k) p[nq][k][4 * u + e] = part[k];
         }
     }
 
     // ---- out
+    float sc[8];
 #pragma unroll
-    for (int h = 0; h < SUB / 2; ++h) {
+    for (int e = 0; e < 8; ++e) sc[e] = scale_byte(raw.vs[e / 4], e & 3);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        // channels 2b and 2b + 1 of the lane's run, 8 tokens
-        bf16x8 v0, v1;
+    for (int b = 0; b < NB; ++b) {
+      // channels 2b and 2b + 1 of the lane's run, 8 tokens
+      uint32_t x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int u = 2 * h + e / 4, byte = (e & 3) * NB + b;  // of the 4 NB loaded
-          const float sc = scale_byte(vs[u], e & 3);
-          const uint32_t w = vr[u][byte / 4];
-          bf16x2 x;
-          switch (byte & 3) {
-            case 0: x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0); break;
-            case 1: x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1); break;
-            case 2: x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2); break;
-            default: x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3); break;
-          }
-          v0[e] = x[0];
-          v1[e] = x[1];
+      for (int e = 0; e < 8; ++e) {
+        const int byte = (e & 3) * NB + b;  // of the 4 NB loaded
+        const uint32_t w = raw.v[e / 4][byte / 4];
+        bf16x2 y;
+        switch (byte & 3) {
+          case 0: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc[e], 0); break;
+          case 1: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc[e], 1); break;
+          case 2: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc[e], 2); break;
+          default: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc[e], 3); break;
         }
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-          for (int k = 0; k < PARTS; ++k) {
-            acc[nq][2 * b] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[nq][k][h], acc[nq][2 * b], 0, 0, 0);
-            acc[nq][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[nq][k][h],
-                                                                         acc[nq][2 * b + 1], 0, 0, 0);
-          }
+        x[e] = __builtin_bit_cast(uint32_t, y);
       }
+      u32x4 even, odd;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        even[e] = __builtin_amdgcn_perm(x[2 * e + 1], x[2 * e], 0x05040100);
+        odd[e] = __builtin_amdgcn_perm(x[2 * e + 1], x[2 * e], 0x07060302);
+      }
+      const bf16x8 v0 = __builtin_bit_cast(bf16x8, even), v1 = __builtin_bit_cast(bf16x8, odd);
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+          acc[nq][2 * b] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[nq][k], acc[nq][2 * b], 0, 0, 0);
+          acc[nq][2 * b + 1] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[nq][k], acc[nq][2 * b + 1], 0, 0, 0);
+        }
     }
+    raw = next;
   }
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) l[nq] = sum16(l[nq]);
 
   // ---- the waves' parts into one
+  const int64_t slot0 = (item * a.kv_heads + kvh) * a.tile_rows + (SHARED ? 0 : wave * 16 * NQ);
   if constexpr (SHARED) {
-    constexpr int LD = D + 4;
-    __shared__ float joined[4][16][LD];
-    __shared__ float ml[4][16][2];
+    constexpr int LD = D + 4, LANES = 4 * WAVES, PER = D / LANES;  // threads of a row, their channels
+    __shared__ __attribute__((aligned(16))) float joined[WAVES][16][LD];
+    __shared__ float ml[WAVES][16][2];
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
       if (nq) __syncthreads();
@@ -309,28 +402,26 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
           *(f32x4*)&joined[wave][r16][NC * (4 * g + e) + j] =
               f32x4{acc[nq][j][e], acc[nq][j + 1][e], acc[nq][j + 2][e], acc[nq][j + 3][e]};
       __syncthreads();
-      // thread: row t / 16, channels D/16 (t % 16) ..
-      const int row = threadIdx.x >> 4, ch = (threadIdx.x & 15) * NC;
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][row][0]);
-      const float base = top == -__builtin_inff() ? 0.f : top;
-      float sum = 0.f, o[NC] = {};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float lw = ml[w][row][1], k = exp2_fast(ml[w][row][0] - base);
-        if (lw == 0.f) continue;
-        sum += lw * k;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) o[j] += joined[w][row][ch + j] * k;
-      }
+      const int row = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * PER;
       const int r = trow0 + 16 * nq + row;
       if (r >= rows_here) continue;
-      if (f.pieces > 1) {
-        const int64_t slot = ((int64_t)blockIdx.x * a.kv_heads + kvh) * a.tile_rows + 16 * nq + row;
-        float* po = a.part + slot * D + ch;
+      float top = -__builtin_inff();
 #pragma unroll
-        for (int j = 0; j < NC; ++j) po[j] = o[j];
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, ml[w][row][0]);
+      const float base = top == -__builtin_inff() ? 0.f : top;
+      float sum = 0.f, o[PER] = {};
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        // (a wave without weights has nothing to add, and its base is no number to take an
+        // exponential with)
+        const float lw = ml[w][row][1], k = lw == 0.f ? 0.f : exp2_fast(ml[w][row][0] - base);
+        sum += lw * k;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) o[j] += joined[w][row][ch + j] * k;
+      }
+      if (f.pieces > 1) {
+        const int64_t slot = slot0 + 16 * nq + row;
+        __builtin_memcpy(a.part + slot * D + ch, o, sizeof(o));
         if (ch == 0) {
           a.part[a.ml_at + 2 * slot] = top;
           a.part[a.ml_at + 2 * slot + 1] = sum;
@@ -338,11 +429,12 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
       } else {
         const int token = r / a.group, hd = kvh * a.group + r - token * a.group;
         const Sight sg = sight_of(a, sq, token);
-        const float inv = sg.lo < sg.hi ? 1.f / sum : 0.f;
-        T res[NC];
+        const bool sees = sg.lo < sg.hi;
+        const float inv = 1.f / sum;
+        T res[PER];
 #pragma unroll
-        for (int j = 0; j < NC; ++j) res[j] = (T)(sg.lo < sg.hi ? o[j] * inv : 0.f);
-        T* dst = (T*)a.out + (sq.row0 + token) * a.ld_out + hd * a.hs_out + ch;
+        for (int j = 0; j < PER; ++j) res[j] = (T)(sees ? o[j] * inv : 0.f);
+        T* dst = (T*)a.out + (int64_t)(sq.row0 + token) * a.ld_out + hd * a.hs_out + ch;
         __builtin_memcpy(dst, res, sizeof(res));
       }
     }
@@ -351,44 +443,44 @@ __global__ __launch_bounds__(256) void attn_kernel(const AttnArgs a) {
     for (int nq = 0; nq < NQ; ++nq) {
       if (!real[nq]) continue;
       const bool sees = see[nq].lo < see[nq].hi;
-      if (f.pieces > 1) {
-        const int64_t slot = ((int64_t)blockIdx.x * a.kv_heads + kvh) * a.tile_rows +
-                             wave * 16 * NQ + 16 * nq + r16;
+      const int64_t slot = slot0 + 16 * nq + r16;
+      const float inv = 1.f / l[nq];
+      T* dst = (T*)a.out + (int64_t)(sq.row0 + tok[nq]) * a.ld_out + head[nq] * a.hs_out;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4; ++e) {
+        const int ch = NC * (4 * g + e);
+        float o[NC];
+        T res[NC];
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            a.part[slot * D + NC * (4 * g + e) + j] = acc[nq][j][e];
-        if (g == 0) {
-          a.part[a.ml_at + 2 * slot] = m[nq];
-          a.part[a.ml_at + 2 * slot + 1] = l[nq];
+        for (int j = 0; j < NC; ++j) o[j] = acc[nq][j][e];
+        if (f.pieces > 1) {
+          __builtin_memcpy(a.part + slot * D + ch, o, sizeof(o));
+        } else {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) res[j] = (T)(sees ? o[j] * inv : 0.f);
+          __builtin_memcpy(dst + ch, res, sizeof(res));
         }
-      } else {
-        const float inv = sees ? 1.f / l[nq] : 0.f;
-        T* dst = (T*)a.out + (sq.row0 + tok[nq]) * a.ld_out + head[nq] * a.hs_out;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          T res[NC];
-#pragma unroll
-          for (int j = 0; j < NC; ++j) res[j] = (T)(sees ? acc[nq][j][e] * inv : 0.f);
-          __builtin_memcpy(dst + NC * (4 * g + e), res, sizeof(res));
-        }
+      }
+      if (f.pieces > 1 && g == 0) {
+        a.part[a.ml_at + 2 * slot] = m[nq];
+        a.part[a.ml_at + 2 * slot + 1] = l[nq];
       }
     }
   }
 }
 
-// Pieces into rows: a wave for each (row, head).
+// Pieces into rows: a wave for each (row, head), a lane for each piece's base and sum, then for each
+// D/64 channels.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
-  constexpr int PER = D / 64;
+  constexpr int PER = D / 64, BATCH = 8;
   const int lane = lane_id();
   const int64_t at = (int64_t)blockIdx.x * 4 + uniform((int)(threadIdx.x >> 6));
   if (at >= (int64_t)a.rows * a.n_heads) return;
-  const int row = (int)(at / a.n_heads), head = (int)(at - (int64_t)row * a.n_heads);
-  const int cut = piece_tokens(a);
+  const int row = uniform((int)(at / a.n_heads)), head = uniform((int)(at - (int64_t)row * a.n_heads));
+  int cut;
   Found f;
-  if (!find_piece(a, cut, 0, row, f) || f.pieces == 1) return;
+  if (!find_piece(a, 0, row, f, cut) || f.pieces == 1) return;
   const int kvh = head / a.group, token = row - f.seq.row0;
   const int r = token * a.group + head - kvh * a.group;
   const int tile = r / a.tile_rows;
@@ -397,34 +489,57 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
   const int64_t slot0 = (item0 * a.kv_heads + kvh) * a.tile_rows + (r - tile * a.tile_rows);
   const int64_t step = (int64_t)a.kv_heads * a.tile_rows;
   const float* ml = a.part + a.ml_at;
-  float top = -__builtin_inff();
-  for (int p = lane; p < f.pieces; p += 64) top = fmaxf(top, ml[2 * (slot0 + p * step)]);
-  top = wave_max(top);
-  const float base = top == -__builtin_inff() ? 0.f : top;
-  float sum = 0.f, o[PER] = {};
-  for (int p = 0; p < f.pieces; ++p) {
-    const int64_t slot = slot0 + p * step;
-    const float lp = ml[2 * slot + 1], k = exp2_fast(ml[2 * slot] - base);
-    if (lp == 0.f) continue;
-    sum += lp * k;
+  float top = -__builtin_inff(), sum = 0.f, o[PER] = {};
+  for (int p0 = 0; p0 < f.pieces; p0 += 64) {  // (more than 64: the rest with a base of its own)
+    const int n = f.pieces - p0 < 64 ? f.pieces - p0 : 64;
+    float mine = -__builtin_inff(), lp = 0.f;
+    if (lane < n) {
+      mine = ml[2 * (slot0 + (p0 + lane) * step)];
+      lp = ml[2 * (slot0 + (p0 + lane) * step) + 1];
+    }
+    const float up = fmaxf(top, wave_max(mine)), base = up == -__builtin_inff() ? 0.f : up;
+    // (a piece without weights has nothing to add, and may hold no numbers)
+    const float k = lp == 0.f ? 0.f : exp2_fast(mine - base);
+    const float old = exp2_fast(top - base);
+    sum = sum * old + wave_sum(lp == 0.f ? 0.f : lp * k);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) o[j] += a.part[slot * D + lane * PER + j] * k;
+    for (int j = 0; j < PER; ++j) o[j] *= old;
+    top = up;
+    const float* src = a.part + (slot0 + p0 * step) * D + lane * PER;
+    const bool skip = lp == 0.f;
+    const uint64_t skips = __ballot(skip);
+    for (int p = 0; p < n; p += BATCH) {
+      float v[BATCH][PER];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int at_p = p + i < n ? p + i : n - 1;
+        __builtin_memcpy(v[i], src + at_p * step * D, sizeof(v[i]));
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        if (p + i >= n || ((skips >> (p + i)) & 1)) continue;
+        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k), p + i));
+#pragma unroll
+        for (int j = 0; j < PER; ++j) o[j] += v[i][j] * w;
+      }
+    }
   }
   const Sight sg = sight_of(a, f.seq, token);
   const bool sees = sg.lo < sg.hi;
   const float inv = 1.f / sum;
-  T* dst = (T*)a.out + row * a.ld_out + head * a.hs_out + lane * PER;
+  T res[PER];
 #pragma unroll
-  for (int j = 0; j < PER; ++j) dst[j] = (T)(sees ? o[j] * inv : 0.f);
+  for (int j = 0; j < PER; ++j) res[j] = (T)(sees ? o[j] * inv : 0.f);
+  __builtin_memcpy((T*)a.out + (int64_t)row * a.ld_out + head * a.hs_out + lane * PER, res, sizeof(res));
 }
 
 // ------------------------------------------------------------------ the host side
 // How a call runs: the kernel and the rows of its tiles, the pieces to cut into.
 struct AttnPlan {
-  int chunk_waves; // 0: attn_kernel
-  int nq;          // of attn_kernel
-  bool shared;
-  int tile_rows;
+  int chunk_waves; // 0: attn_rows_kernel
+  int nq;          // of attn_rows_kernel
+  bool shared, wide;
+  int tile_rows, quantum;
   int64_t tiles;   // at most, over all sequences
   int target;      // 0: tokens are not cut
   int64_t items;   // of the grid
@@ -435,7 +550,7 @@ static int64_t tiles_of(int64_t rows, int64_t group, int64_t n_seqs, int tile_ro
 }
 
 static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32, int64_t rows,
-                          int64_t n_seqs, int cus) {
+                          int64_t n_seqs, int64_t tokens, int cus) {
   AttnPlan p;
   const int64_t group = A->n_heads / C->n_heads;
   const int64_t each = (rows * group + n_seqs - 1) / n_seqs;  // rows of a sequence, on average
@@ -443,7 +558,9 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
   p.nq = f32 || each <= 16 ? 1 : 2;
   p.chunk_waves = f32 || p.shared ? 0 : 4;
   p.tile_rows = p.shared ? 16 * p.nq : f32 ? 64 : 128;
-  int64_t full = 2 * cus;
+  p.quantum = p.shared ? 128 : 64;
+  // workgroups that the chip holds at once
+  int64_t full = (p.chunk_waves ? 2 : resident(f32, C->head_dim, p.nq)) * cus;
   if (p.chunk_waves && C->head_dim < 256 &&
       tiles_of(rows, group, n_seqs, 256) * C->n_heads >= cus) {
     p.chunk_waves = 8;
@@ -451,7 +568,10 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
     full = cus;
   }
   p.tiles = tiles_of(rows, group, n_seqs, p.tile_rows);
-  p.target = p.tiles * C->n_heads >= full ? 0 : (int)((full + C->n_heads - 1) / C->n_heads);
+  p.wide = p.shared && tokens <= 2048 && p.tiles * C->n_heads <= cus;
+  p.target = p.tiles * C->n_heads >= full || p.wide || tokens <= p.quantum
+                 ? 0
+                 : (int)((full + C->n_heads - 1) / C->n_heads);
   p.items = p.tiles + p.target;
   return p;
 }
@@ -469,13 +589,20 @@ static void attn_launch(const AttnArgs& a, const AttnPlan& p, hipStream_t stream
   if (p.chunk_waves) {
     attn_chunk_launch(a, D, p.chunk_waves, stream);
   } else {
-    const dim3 grid((unsigned)p.items, (unsigned)a.kv_heads);
+    const dim3 grid((unsigned)(p.items * a.kv_heads));
+    // (16 waves have 128 registers each)
+    constexpr int WIDE = sizeof(T) == 4 || D == 256 ? 8 : 16;
     if constexpr (sizeof(T) == 4) {
-      auto k = p.shared ? attn_kernel<T, D, 1, true> : attn_kernel<T, D, 1, false>;
-      hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, a);
+      auto k = !p.shared  ? attn_rows_kernel<T, D, 1, 4, false>
+               : p.wide   ? attn_rows_kernel<T, D, 1, WIDE, true>
+                          : attn_rows_kernel<T, D, 1, 4, true>;
+      hipLaunchKernelGGL(k, grid, dim3(p.shared && p.wide ? 64 * WIDE : 256), 0, stream, a);
     } else {
-      auto k = p.nq == 1 ? attn_kernel<T, D, 1, true> : attn_kernel<T, D, 2, true>;
-      hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, a);
+      auto k = p.nq == 1 ? (p.wide ? attn_rows_kernel<T, D, 1, WIDE, true>
+                                   : attn_rows_kernel<T, D, 1, 4, true>)
+                         : (p.wide ? attn_rows_kernel<T, D, 2, 8, true>
+                                   : attn_rows_kernel<T, D, 2, 4, true>);
+      hipLaunchKernelGGL(k, grid, dim3(!p.wide ? 256 : p.nq == 1 ? 64 * WIDE : 512), 0, stream, a);
     }
   }
   if (p.target) {
@@ -496,14 +623,14 @@ extern "C" size_t moe_attn_cache_workspace_bytes(const moe_attn_t* A, const moe_
   if (cus <= 0) cus = 256;
   // Cut calls have fewer than `full` tiles over all heads, so at most that many and their target
   // pieces: no fewer rows or sequences need more.
-  const int64_t full = 2 * cus, heads = C->n_heads;
+  const int64_t heads = C->n_heads;
   const int64_t group = A->n_heads / heads;
-  const int64_t target = (full + heads - 1) / heads;
   int64_t most = 0;
   for (int tile_rows : {16, 32, 64, 128, 256}) {
-    int64_t tiles = ((int64_t)rows * group + tile_rows - 1) / tile_rows + n_seqs;
-    const int64_t cap = (full + heads - 1) / heads;
-    if (tiles > cap) tiles = cap;
+    const int64_t full = (tile_rows <= 64 ? 4 : tile_rows == 128 ? 2 : 1) * cus;
+    const int64_t target = (full + heads - 1) / heads;
+    int64_t tiles = tiles_of(rows, group, n_seqs, tile_rows);
+    tiles = tiles < target ? tiles : target;
     const int64_t n = part_floats(C, tiles + target, tile_rows);
     most = n > most ? n : most;
   }
@@ -540,8 +667,8 @@ extern "C" int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, cons
     return MOE_ERR_ALIGNMENT;
   int cus = device_cu_count();
   if (cus <= 0) cus = 256;
-  AttnPlan p = attn_plan(A, C, type == MOE_TYPE_F32, rows, n_seqs, cus);
-  if ((int64_t)max_pages * C->page <= kLeastPart) p.items -= p.target, p.target = 0;
+  const AttnPlan p = attn_plan(A, C, type == MOE_TYPE_F32, rows, n_seqs,
+                               (int64_t)max_pages * C->page, cus);
   const int64_t need = p.target ? 4 * part_floats(C, p.items, p.tile_rows) : 0;
   if (need && !ws) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < (size_t)need) return MOE_ERR_WORKSPACE;
@@ -575,6 +702,7 @@ extern "C" int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, cons
   a.target = p.target;
   a.items = p.items;
   a.tile_rows = p.tile_rows;
+  a.quantum = p.quantum;
   a.scale = A->scale;
   a.softcap = A->softcap;
   const hipStream_t st = (hipStream_t)stream;

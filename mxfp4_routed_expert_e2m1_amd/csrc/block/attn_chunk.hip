@@ -27,43 +27,6 @@ __device__ inline float sum2(float v) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
-// 16 channels of a query row in two E4M3 planes, x = 2^(e - 127) (hi + 2^-5 lo), where e puts the
-// largest magnitude of the block (bits `most`) at 128 .. 256.
-__device__ inline int plane_exponent(uint32_t most) {
-  const int e = (int)(most >> 23) - 7;
-  return e < 16 ? 16 : e;
-}
-template <int AT>
-__device__ inline void e4m3_planes(const float (&x)[16], int e, v8i32& hi, v8i32& lo) {
-  const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    int h = 0, l = 0;
-    float r[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = x[4 * i + k] * down;
-    h = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], h, false);
-    h = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], h, true);
-    r[0] = (r[0] - __builtin_amdgcn_cvt_f32_fp8(h, 0)) * 32.f;
-    r[1] = (r[1] - __builtin_amdgcn_cvt_f32_fp8(h, 1)) * 32.f;
-    r[2] = (r[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 32.f;
-    r[3] = (r[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 32.f;
-    l = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], l, false);
-    l = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], l, true);
-    hi[AT + i] = h;
-    lo[AT + i] = l;
-  }
-}
-__device__ inline uint32_t most_bits(const float (&x)[16]) {
-  uint32_t most = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-    most = b > most ? b : most;
-  }
-  return most;
-}
-
 template <int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a) {
   constexpr int NB = D / 32, NI = (NB + 1) / 2, NC = D / 16, RB = 32 / NC;
@@ -80,14 +43,9 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
   const int64_t item = blockIdx.x / a.kv_heads;
   const int kvh = (int)(blockIdx.x - item * a.kv_heads);
 
-  int cut = 0x40000000;
+  int cut;
   Found f;
-  if (a.target) {
-    cut = piece_tokens(a);
-    if (!find_piece(a, cut, item, -1, f)) return;
-  } else {
-    if (!find_tile(a, item, f)) return;
-  }
+  if (!find_item(a, item, f, cut)) return;
   const Seq& sq = f.seq;
   const int local = (int)(item - f.first_item);
   // the last rows first: they see the most tokens
@@ -149,7 +107,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
   const bool any = row0 < rows_here;
   const Sight s0 = row_sight(row0), s1 = row_sight(row0 + 31);
   const int lo = s0.lo, hi = any ? s1.hi : 0;
-  const int all_lo = s1.lo, all_hi = row0 + 31 < rows_here ? s0.hi : 0;
+  const int all_lo = s1.lo, all_hi = s0.hi;
 
   const KvUnit<D> unit{1 << a.page_log};
   const int32_t* pages = a.table + f.at * a.ld_table;
