@@ -636,7 +636,7 @@ int moe_kv_read(const moe_kv_cache_t* C, const int32_t* slots, int rows, void* k
  * A row that sees nothing (a request without tokens, a place below 0 and no
  * prefix) is 0. */
 typedef struct moe_attn {
-  int n_heads;         /* query heads, a multiple of the cache's heads, <= 65536 */
+  int n_heads;         /* query heads, a multiple of the cache's heads, <= 16384 */
   int window;          /* 0: none */
   float scale;         /* finite */
   float softcap;       /* 0: none; finite, >= 0 */

@@ -6,6 +6,8 @@
 
 namespace moe {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kStep = 64;  // tokens to which pieces and the start of a pass are aligned
 
@@ -20,13 +22,29 @@ struct AttnArgs {
   const float* slopes;
   float* part;  // partial results, NULL: tokens are not cut
   int64_t ld_q, hs_q, ld_out, hs_out, ld_table;
-  int64_t ml_at;  // floats from `part` to the maxima and sums
+  int64_t ml_at, rec_at;  // floats from `part` to the pieces' bases and sums, to the rows' records
   int rows, n_seqs, n_heads, kv_heads, group, page_log, n_pages, max_pages, window;
   int target;    // pieces that fill the chip (0: tokens are not cut)
   int64_t items; // of the grid
-  int quantum;   // tokens of a piece: a multiple of this
-  int tile_rows; // rows of a tile
+  int quantum;   // tokens of a piece: a multiple of this power of two
+  int tile_log;  // rows of a tile, as a power of two
+  uint32_t group_inv;  // 2^32 / group + 1
   float scale, softcap;
+};
+
+// (token, head of the group) of rows near a tile's first, whose division is done once.
+struct RowSplit {
+  int tok0, rem0;
+  __device__ RowSplit(const AttnArgs& a, int row) {
+    tok0 = uniform((int)((uint32_t)row / (uint32_t)a.group));
+    rem0 = row - tok0 * a.group;
+  }
+  // of row + i, where (group + i) * group < 2^32: i < 256 and groups of up to 2^14
+  __device__ void at(const AttnArgs& a, int i, int& tok, int& head) const {
+    const uint32_t x = rem0 + i, t = a.group == 1 ? x : __umulhi(x, a.group_inv);
+    tok = tok0 + (int)t;
+    head = (int)(x - t * a.group);
+  }
 };
 
 // A sequence's numbers, kept within what the arguments allow.
@@ -53,25 +71,24 @@ struct Seq {
     const int64_t f = a.window > 0 ? (int64_t)n - m - a.window + 1 : 0;
     return f > 0 ? (int)f & ~(kStep - 1) : 0;
   }
-  __device__ int tiles(const AttnArgs& a) const {
-    return (int)(((int64_t)m * a.group + a.tile_rows - 1) / a.tile_rows);
+  __device__ int tiles(const AttnArgs& a) const {  // (rows * group < 2^28)
+    return (m * a.group + (1 << a.tile_log) - 1) >> a.tile_log;
   }
 };
 
 // A sequence, its place in the batch, and where its items (pieces of tiles) begin.
 struct Found {
   Seq seq;
-  int at, pieces;
-  int64_t first_item;
+  int at, pieces, first_item;
 };
 
-// Uncut calls: sequence s has its tiles from item q_offsets[s] * group / tile_rows + s on, which
+// Uncut calls: sequence s has its tiles from item q_offsets[s] * group / (tile's rows) + s on, which
 // leaves room for a last tile that is not full; the item's sequence by 64 probes at a time.
-__device__ inline bool find_tile(const AttnArgs& a, int64_t item, Found& f) {
+__device__ inline bool find_tile(const AttnArgs& a, int item, Found& f) {
   f.pieces = 1;
   if (!a.q_offsets) {  // a row each
-    const int64_t each = ((int64_t)a.group + a.tile_rows - 1) / a.tile_rows;
-    f.at = (int)(item / each);
+    const int each = (a.group + (1 << a.tile_log) - 1) >> a.tile_log;
+    f.at = each == 1 ? item : item / each;
     f.first_item = f.at * each;
     if (f.at >= a.n_seqs) return false;
     f.seq.load(a, f.at);
@@ -84,7 +101,7 @@ __device__ inline bool find_tile(const AttnArgs& a, int64_t item, Found& f) {
     if (step * lane_id() < n) {
       int r0 = a.q_offsets[s];
       r0 = r0 < 0 ? 0 : r0 > a.rows ? a.rows : r0;
-      before = (int64_t)r0 * a.group / a.tile_rows + s <= item;
+      before = ((r0 * a.group) >> a.tile_log) + s <= item;
     }
     const uint64_t b = __ballot(before);
     const int l = b ? 63 - __builtin_clzll(b) : 0;
@@ -93,7 +110,7 @@ __device__ inline bool find_tile(const AttnArgs& a, int64_t item, Found& f) {
   }
   f.at = lo;
   f.seq.load(a, lo);
-  f.first_item = (int64_t)f.seq.row0 * a.group / a.tile_rows + lo;
+  f.first_item = ((f.seq.row0 * a.group) >> a.tile_log) + lo;
   return item >= f.first_item && item - f.first_item < f.seq.tiles(a);
 }
 
@@ -102,10 +119,9 @@ __device__ inline int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_in
 // Cut calls (few tiles, so few sequences): a piece has `cut` tokens, as many for every sequence, and
 // items are counted over the sequences.  The cut is the batch's work over `target` pieces where
 // that makes no more than `target` of them (a sequence's last piece is a whole one there), or over
-// fewer pieces by half a piece, or a whole one, for each tile.  Finds the sequence of an item, or
-// with `row` >= 0 of that row.  (Counts of one sequence are kept below 2^24 or 2^25, so that offsets
+// fewer pieces by half a piece, or a whole one, for each tile.  (Counts of one sequence are kept below 2^24 or 2^25, so that offsets
 // that overlap cannot make a sum of 64 overflow.)
-__device__ inline bool find_piece(const AttnArgs& a, int64_t item, int row, Found& f, int& cut) {
+__device__ inline bool find_piece(const AttnArgs& a, int item, Found& f, int& cut) {
   const int lane = lane_id();
   Seq q = {0, 0, 0, 0};
   int tiles = 0, span = 0;
@@ -139,11 +155,12 @@ __device__ inline bool find_piece(const AttnArgs& a, int64_t item, int row, Foun
     take(0);
   }
   for (int k = one ? 0 : 2;; ++k) {
-    int64_t over = a.target - all * k / 2;
-    over = over > a.target / 2 ? over : a.target / 2 > 0 ? a.target / 2 : 1;
-    int64_t c = (work * kStep + over - 1) / over;
-    c = (c + a.quantum - 1) / a.quantum * a.quantum;
-    cut = uniform((int)(c < a.quantum ? a.quantum : c > 0x40000000 ? 0x40000000 : c));
+    int over = all < a.target ? a.target - (int)all * k / 2 : 0;
+    over = over > a.target / 2 ? over : (a.target + 1) / 2;
+    const uint32_t w = work < 0x7FFFFFFF ? (uint32_t)work : 0x7FFFFFFFu;
+    const int64_t c = (int64_t)((w + over - 1) / (uint32_t)over) * kStep;
+    const int64_t up = (c + a.quantum - 1) & ~(int64_t)(a.quantum - 1);
+    cut = uniform((int)(up < a.quantum ? a.quantum : up > 0x40000000 ? 0x40000000 : up));
     if (k == 2 || wave_sum(items_of(span <= cut ? 1 : (span + cut - 1) / cut)) <= a.target) break;
   }
   int64_t before = 0;
@@ -151,12 +168,12 @@ __device__ inline bool find_piece(const AttnArgs& a, int64_t item, int row, Foun
     const int pieces = span <= cut ? 1 : (span + cut - 1) / cut;
     const int items = items_of(pieces), scan = wave_incl_scan(items);
     const int64_t end = before + scan;
-    const bool mine = row >= 0 ? row >= q.row0 && row < q.row0 + q.m : item < end && item >= end - items;
+    const bool mine = item < end && item >= end - items;
     const uint64_t who = __ballot(mine);
     if (who) {
       const int l = __builtin_ctzll(who);
       f.at = s0 + l;
-      f.first_item = before + __builtin_amdgcn_readlane(scan - items, l);
+      f.first_item = (int)before + __builtin_amdgcn_readlane(scan - items, l);
       f.pieces = __builtin_amdgcn_readlane(pieces, l);
       f.seq.row0 = __builtin_amdgcn_readlane(q.row0, l);
       f.seq.m = __builtin_amdgcn_readlane(q.m, l);
@@ -171,10 +188,20 @@ __device__ inline bool find_piece(const AttnArgs& a, int64_t item, int row, Foun
   }
 }
 
+// Workgroups: key heads first, so that with 8 of them (or a multiple) each XCD's L2 has the tokens of
+// its own; then items, in two dimensions.
+constexpr unsigned kItemsY = 32768;
+__device__ inline int block_item() { return (int)(blockIdx.z * kItemsY + blockIdx.y); }
+inline dim3 item_grid(int64_t items, int kv_heads) {
+  const int64_t y = items < kItemsY ? items : kItemsY;
+  return dim3((unsigned)kv_heads, (unsigned)y, (unsigned)((items + y - 1) / y));
+}
+
 // The item of a workgroup (false: there is none), the tokens of a piece.
-__device__ inline bool find_item(const AttnArgs& a, int64_t item, Found& f, int& cut) {
+__device__ inline bool find_item(const AttnArgs& a, int item, Found& f, int& cut) {
   cut = 0x40000000;
-  return a.target ? find_piece(a, item, -1, f, cut) : find_tile(a, item, f);
+  if (item >= a.items) return false;
+  return a.target ? find_piece(a, item, f, cut) : find_tile(a, item, f);
 }
 
 // The tokens that a row sees: lo <= j < hi.
@@ -192,6 +219,17 @@ __device__ inline Sight sight_of(const AttnArgs& a, const Seq& s, int token) {
   return v;
 }
 
+// What the joining launch has to know of a row; written by the workgroup of the sequence's first piece
+// and key head.
+struct RowRecord {
+  int first_item, pieces, tiles, row0;  // pieces negative: the row sees nothing
+};
+__device__ inline void put_record(const AttnArgs& a, const Found& f, int token, const Sight& see) {
+  RowRecord r = {f.first_item, see.lo < see.hi ? f.pieces : -f.pieces, f.seq.tiles(a), f.seq.row0};
+  if (f.pieces == 1) r.pieces = 1;
+  ((RowRecord*)(a.part + a.rec_at))[f.seq.row0 + token] = r;
+}
+
 __device__ inline float max16(float v) {  // over the lanes l % 16
   const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
@@ -207,19 +245,19 @@ __device__ inline float sum16(float v) {
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// softcap * tanh(s / softcap).  (1 - e^-2x) / (1 + e^-2x), its quotient refined once, loses a small
-// x beside the 1; below 1/4 Taylor's series to x^9 is within 2^-25 of x.
-__device__ inline float capped(float s, float cap, float inv) {
-  const float x = s * inv, z = x * x;
-  const float e = exp2_fast(-2.f * kLog2e * fabsf(x)), d = 1.f + e, rc = __builtin_amdgcn_rcpf(d);
-  float big = (1.f - e) * rc;
-  big = copysignf(fmaf(fmaf(-big, d, 1.f - e), rc, big), x);
-  float p = 62.f / 2835.f;
-  p = fmaf(p, z, -17.f / 315.f);
-  p = fmaf(p, z, 2.f / 15.f);
-  p = fmaf(p, z, -1.f / 3.f);
-  const float small = fmaf(x * z, p, x);
-  return cap * (fabsf(x) < 0.25f ? small : big);
+// softcap * tanh(s / softcap); k = 2 log2(e) / softcap.  For bf16
+// calls cap - 2 cap / (1 + e^2x); for f32 ones (1 - e^-2x) / (1 + e^-2x), the reciprocal refined:
+// off by at most 2^-24 of the cap, which is what a score near it is rounded to.
+template <bool F32>
+__device__ inline float capped(float s, float cap, float k) {
+  if constexpr (!F32) {
+    return fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + exp2_fast(s * k)), cap);
+  } else {
+    const float e = exp2_fast(-k * fabsf(s)), d = 1.f + e;
+    float r = __builtin_amdgcn_rcpf(d);
+    r = fmaf(fmaf(-d, r, 1.f), r, r);
+    return copysignf(cap * ((1.f - e) * r), s);
+  }
 }
 
 // 4 scale bytes, any above kMaxScaleByte (253..255)?
@@ -230,15 +268,32 @@ __device__ inline float scale_byte(uint32_t word, int b) {
   return __uint_as_float((b == 0 ? word << 23 : b == 3 ? word >> 1 : word >> (8 * b) << 23) & 0x7F800000u);
 }
 
-// x = sum of PARTS bf16 numbers (three hold every fp32 bit).
+// Eight numbers as sums of PARTS bf16 numbers.  Three hold every fp32 bit: the upper 8 bits of the
+// significand, the next 8 and the last, each cut off (the rest of an infinity is NaN).  One is
+// rounded to nearest.
 template <int PARTS>
-__device__ inline void split(float x, __bf16 (&p)[PARTS]) {
-  p[0] = (__bf16)x;
-  if constexpr (PARTS == 3) {
-    // (infinities and NaN: the first part has them, the others must not make NaN of infinity)
-    const float r = fabsf(x) < __builtin_inff() ? x - (float)p[0] : 0.f;
-    p[1] = (__bf16)r;
-    p[2] = (__bf16)(r - (float)p[1]);
+__device__ inline void split8(const float (&x)[2][4], bf16x8 (&p)[PARTS]) {
+  if constexpr (PARTS == 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[0][i] = (__bf16)x[i / 4][i % 4];
+  } else {
+    u32x4 w[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[3], b[3];  // of numbers 2i and 2i + 1
+      const auto cut = [](float v, uint32_t (&c)[3]) {
+        c[0] = __float_as_uint(v);
+        const float r = v - __uint_as_float(c[0] & 0xFFFF0000u);
+        c[1] = __float_as_uint(r);
+        c[2] = __float_as_uint(r - __uint_as_float(c[1] & 0xFFFF0000u));
+      };
+      cut(x[i / 2][2 * i % 4], a);
+      cut(x[i / 2][2 * i % 4 + 1], b);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) w[k][i] = __builtin_amdgcn_perm(b[k], a[k], 0x07060302);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) p[k] = __builtin_bit_cast(bf16x8, w[k]);
   }
 }
 

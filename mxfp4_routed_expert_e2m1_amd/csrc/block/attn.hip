@@ -31,31 +31,40 @@ namespace moe {
 // ------------------------------------------------------------------- the pass
 // SHARED: the waves of a workgroup have one tile of 16 NQ rows and take its tokens in turn, 32 each,
 // joined in LDS at the end; otherwise each wave has a tile of its own among the workgroup's.
-// A wave's next 32 tokens are on their way from memory while it works on 32.
-constexpr int resident(bool f32, int dim, int nq) {  // workgroups of 4 waves that a CU holds
-  if (dim == 256) return 1;
-  if (dim == 128) return f32 ? 2 : nq == 1 ? 3 : 1;
-  return f32 ? 3 : nq == 1 ? 4 : 2;
+// A wave's next keys are on their way from memory while it has the scores, its next values when they
+// are used up: registers for one step's codes, which leaves room for more waves.
+// Workgroups of 4 waves that a CU holds (by their registers and LDS).
+constexpr int resident(bool f32, int dim, int nq) {
+  if (dim == 256) return nq == 1 ? 2 : 1;
+  if (dim == 128) return nq == 1 ? 3 : 2;
+  return f32 || nq == 2 ? 3 : 4;
 }
 template <typename T, int D, int NQ, int WAVES, bool SHARED>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D, NQ) : 1) void attn_rows_kernel(const AttnArgs a) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int NB = D / 32, NC = D / 16, NI = (D + 127) / 128, PARTS = F32 ? 3 : 1;
   constexpr int STEP = 32, STRIDE = SHARED ? STEP * WAVES : STEP;
+  // a wave's step in LDS: keys' codes, values' codes, scale bytes
+  constexpr int STAGE = 32 * D + 256 * NI, RING = WAVES == 16 || D == 256 ? 2 : 3;
   typedef uint32_t VRaw __attribute__((ext_vector_type(NB)));
+  // (an array for each stage, so that reads of one wait for no copies into the others)
+  __shared__ __attribute__((aligned(1024))) uint8_t ring0[WAVES * STAGE], ring1[WAVES * STAGE],
+      ring2[RING > 2 ? WAVES * STAGE : 16];
+  uint8_t* const ring[3] = {ring0, ring1, ring2};
   const int wave = uniform((int)(threadIdx.x >> 6)), lane = lane_id();
   const int r16 = lane & 15, g = lane >> 4;
-  const int64_t item = blockIdx.x / a.kv_heads;
-  const int kvh = (int)(blockIdx.x - item * a.kv_heads);
+  const int item = block_item(), kvh = blockIdx.x;
 
   int cut;
   Found f;
   if (!find_item(a, item, f, cut)) return;
   const Seq& sq = f.seq;
-  const int local = (int)(item - f.first_item);
+  const int local = item - f.first_item;
   // the last rows first: they see the most tokens
-  const int tile = sq.tiles(a) - 1 - local / f.pieces, piece = local % f.pieces;
-  const int trow0 = tile * a.tile_rows + (SHARED ? 0 : wave * 16 * NQ);
+  const int up = f.pieces == 1 ? local : local / f.pieces, piece = local - up * f.pieces;
+  const int tile = sq.tiles(a) - 1 - up;
+  const int trow0 = (tile << a.tile_log) + (SHARED ? 0 : wave * 16 * NQ);
+  const RowSplit rs(a, trow0);
   const int rows_here = sq.m * a.group;  // (row, head) pairs of the sequence and key head
 
   // this lane's rows: trow0 + 16 nq + r16
@@ -63,78 +72,35 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   bool real[NQ];
   Sight see[NQ];
   float slope[NQ];
-  // q as the matrix core takes it: bf16 calls in two E4M3 planes (128 channels an instruction, of
-  // which a lane has 16 g .. and 64 + 16 g ..), f32 calls in three bf16 parts (32 channels, 8 of
-  // each of a lane's blocks 4 i + g)
-  v8i32 qh[NQ][NI], ql[NQ][NI];
-  int e0[NQ][NI], e1[NQ][NI];
-  bf16x8 q[NQ][NI][4][PARTS];
+  // q on its way: channel runs of 8, [i][n]; bf16 calls have 16 g .. and 64 + 16 g .. of 128
+  // channels in a lane, f32 calls its blocks 4 i + g
+  Raw8<T> qraw[NQ][NI][4];
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) {
-    const int r = trow0 + 16 * nq + r16;
-    real[nq] = r < rows_here;
-    const int rr = real[nq] ? r : 0;
-    tok[nq] = rr / a.group;
-    head[nq] = kvh * a.group + rr - tok[nq] * a.group;
+    real[nq] = trow0 + 16 * nq + r16 < rows_here;
+    rs.at(a, 16 * nq + r16, tok[nq], head[nq]);
+    if (!real[nq]) tok[nq] = head[nq] = 0;
+    head[nq] += kvh * a.group;
     see[nq] = sight_of(a, sq, tok[nq]);
     if (!real[nq]) see[nq] = {0, 0};
     slope[nq] = a.slopes && real[nq] ? a.slopes[head[nq]] * kLog2e : 0.f;
     const T* qp = (const T*)a.q + (int64_t)(sq.row0 + tok[nq]) * a.ld_q + head[nq] * a.hs_q;
-    if constexpr (F32) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          float v[8] = {};
-          const int c = 32 * (4 * i + g) + 8 * n;
-          if (real[nq] && c < D) to_f32<T>(load8(qp + c), v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            __bf16 p[PARTS];
-            split<PARTS>(v[e], p);
-#pragma unroll
-            for (int k = 0; k < PARTS; ++k) q[nq][i][n][k][e] = p[k];
-          }
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        int e[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float x[16] = {};
-          const int c = 128 * i + 64 * b + 16 * g;
-          if (real[nq] && c < D) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float v[8];
-              to_f32<T>(load8(qp + c + 8 * k), v);
-#pragma unroll
-              for (int n = 0; n < 8; ++n) x[8 * k + n] = v[n];
-            }
-          }
-          const uint32_t own = most_bits(x);  // (half of block 4 i + 2 b + g / 2)
-          const auto other = __builtin_amdgcn_permlane16_swap(own, own, false, false);
-          const uint32_t most = other[0] > other[1] ? other[0] : other[1];
-          e[b] = plane_exponent(most);
-          if (b == 0) e4m3_planes<0>(x, e[b], qh[nq][i], ql[nq][i]);
-          else e4m3_planes<4>(x, e[b], qh[nq][i], ql[nq][i]);
-          if (most >= 0x7F800000u) e[b] = 255;  // infinite or NaN: so are all of its products
-        }
-        // the scale of block 4 i + g goes with lanes g
-        const int first = __shfl(e[0], r16 + 32 * (g & 1)), second = __shfl(e[1], r16 + 32 * (g & 1));
-        e0[nq][i] = g < 2 ? first : second;
-        e1[nq][i] = e0[nq][i] == 255 ? 255 : e0[nq][i] - 5;
+      for (int n = 0; n < 4; ++n) {
+        const int c = F32 ? 32 * (4 * i + g) + 8 * n : 128 * i + 64 * (n >> 1) + 16 * g + 8 * (n & 1);
+        qraw[nq][i][n] = Raw8<T>{};
+        if (real[nq] && c < D) qraw[nq][i][n] = load8(qp + c);
       }
-    }
   }
 
   // the tile's tokens: what its first row (window) and its last (causal) see, and all of them
-  const auto row_sight = [&](int row) {
-    return sight_of(a, sq, (row < rows_here ? row : rows_here - 1) / a.group);
-  };
   const bool any = trow0 < rows_here;
-  const Sight s0 = row_sight(any ? trow0 : 0), s1 = row_sight(trow0 + 16 * NQ - 1);
+  int tok1, head1;
+  rs.at(a, 16 * NQ - 1, tok1, head1);
+  tok1 = tok1 < sq.m - 1 ? tok1 : sq.m - 1;
+  const Sight s0 = sight_of(a, sq, any ? rs.tok0 : 0), s1 = sight_of(a, sq, uniform(tok1));
   const int64_t p0 = sq.first(a) + (int64_t)piece * cut;
   const int lo = p0 > s0.lo ? (int)p0 : s0.lo & ~(kStep - 1);
   const int hi = !any ? 0 : p0 + cut < s1.hi ? (int)(p0 + cut) : s1.hi;
@@ -154,59 +120,144 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   const int32_t* pages = a.table + f.at * a.ld_table;
   const bool plain = a.softcap == 0.f && !a.slopes && a.scale > 0.f;
   const float qk_scale = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
-  const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+  const float cap_k = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
   const float unit_scale = plain ? qk_scale : 1.f;
 
-  // 16 tokens lie in one page; those past the last are taken as the last 16 and masked
-  struct Raw {
-    u32x4 k[2][NI];
-    uint32_t ks[2][NI];
-    VRaw v[2];
-    uint32_t vs[2];
-  };
+  // ---- tokens: a wave's steps of 32, copied straight into its part of LDS, RING - 1 steps ahead.  16
+  // tokens lie in one page; those past the last are taken as the last 16 and masked.
+  const int t_first = lo + (SHARED ? wave * STEP : 0);
+  const int n_steps = t_first < hi ? (hi - t_first + STRIDE - 1) / STRIDE : 0;
   const int last16 = (hi - 1) & ~15;
-  const auto sub_of = [&](int t, int u) { return t + 16 * u < last16 ? t + 16 * u : last16; };
-  const auto page_of = [&](int t, int u) { return uniform(pages[sub_of(t, u) >> a.page_log]); };
-  const uint32_t k_off = r16 * (D / 2) + (D == 64 ? (g & 1) : g) * 16;
-  const uint32_t ks_off = unit.k_scales() + r16 * NB + (D == 64 ? (g & 1) : g);
-  const uint32_t v_off = unit.v_codes() + (g * 16 + r16) * 4 * NB;
-  const uint32_t vs_off = unit.v_scales() + (g * NB + r16 * NB / 16) * 4;
-  const auto load = [&](Raw& w, int t, int pg0, int pg1) {
+  const auto sub_of = [&](int step, int u) {
+    const int t = t_first + step * STRIDE + 16 * u;
+    return t < last16 ? t : last16;
+  };
+  int pg[2];          // pages of the step to copy next
+  uint32_t bad = 0;   // two bits a step, the latest lowest: whether its pages are none
+  const auto load_pages = [&](int step) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) pg[u] = uniform(pages[sub_of(step, u) >> a.page_log]);
+  };
+  const auto copy = [&](uint8_t* to, int step) {
+    const uint8_t* at[2];
+    int in[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int pg = u ? pg1 : pg0;
-      const bool bad = pg < 0 || pg >= a.n_pages;
-      const int in = sub_of(t, u) & ((1 << a.page_log) - 1);
-      const uint8_t* at = a.data + ((int64_t)(bad ? 0 : pg) * a.kv_heads + kvh) * unit.bytes();
-      const uint8_t* kc = at + in * (D / 2);
-      const uint8_t* sc = at + in * NB;
+      const bool none = pg[u] < 0 || pg[u] >= a.n_pages;
+      bad = bad << 1 | none;
+      at[u] = a.data + ((int64_t)(none ? 0 : pg[u]) * a.kv_heads + kvh) * unit.bytes();
+      in[u] = sub_of(step, u) & ((1 << a.page_log) - 1);
+    }
+    load_pages(step + 1);
+    uint8_t* mine = to + wave * STAGE;
+    const int u5 = lane >> 5, l5 = lane & 31;
+    if constexpr (D == 64) {  // both halves of the step in one copy
+      const uint8_t* p = (u5 ? at[1] : at[0]) + (u5 ? in[1] : in[0]) * (D / 2);
+      load_to_lds(p + (l5 & 15) * (D / 2) + (l5 >> 4) * 16, mine, 16);
+      load_to_lds(p + unit.v_codes() + l5 * 16, mine + 16 * D, 16);
+    } else {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        __builtin_memcpy(&w.k[u][i], kc + k_off + 64 * i, 16);
-        const uint32_t b = sc[ks_off + 4 * i];
-        w.ks[u][i] = bad ? 255u : b;
-      }
-      __builtin_memcpy(&w.v[u], kc + v_off, 4 * NB);
-      __builtin_memcpy(&w.vs[u], sc + vs_off, 4);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          load_to_lds(at[u] + in[u] * (D / 2) + r16 * (D / 2) + 64 * i + 16 * g,
+                      mine + (u * NI + i) * 1024, 16);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          load_to_lds(at[u] + unit.v_codes() + in[u] * (D / 2) + 1024 * i + 16 * lane,
+                      mine + 16 * D + (u * NI + i) * 1024, 16);
+    }
+    // scale bytes: [keys, values][half of the step][4 NB dwords]
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int d = (64 * i + lane) % (16 * NB), u = d / (4 * NB) & 1;
+      load_to_lds((u ? at[1] : at[0]) + (d < 8 * NB ? unit.k_scales() : unit.v_scales()) +
+                      (u ? in[1] : in[0]) * NB + 4 * (d % (4 * NB)),
+                  mine + 32 * D + 256 * i, 4);
     }
   };
-
-  int t = lo + (SHARED ? wave * STEP : 0);
-  Raw raw;
-  int pg0 = 0, pg1 = 0;
-  if (t < hi) {
-    load(raw, t, page_of(t, 0), page_of(t, 1));
-    pg0 = page_of(t + STRIDE, 0);
-    pg1 = page_of(t + STRIDE, 1);
+  constexpr int COPIES = D == 64 ? 3 : 5 * NI;
+  if (n_steps) {
+    load_pages(0);
+#pragma unroll
+    for (int i = 0; i < RING - 1; ++i) copy(ring[i], i);
   }
-  for (; t < hi; t += STRIDE) {
-    Raw next = raw;
-    if (t + STRIDE < hi) {
-      load(next, t + STRIDE, pg0, pg1);
-      pg0 = page_of(t + 2 * STRIDE, 0);
-      pg1 = page_of(t + 2 * STRIDE, 1);
+
+  // q as the matrix core takes it: bf16 calls in two E4M3 planes (128 channels an instruction), f32
+  // calls in three bf16 parts (32 channels an instruction)
+  v8i32 qh[NQ][NI], ql[NQ][NI];
+  int e0[NQ][NI], e1[NQ][NI];
+  bf16x8 q[NQ][NI][4][PARTS];
+#pragma unroll
+  for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if constexpr (F32) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          float v[8], x[2][4];
+          to_f32<T>(qraw[nq][i][n], v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)  // (a row with an infinity has no finite score)
+            x[e / 4][e % 4] = fabsf(v[e]) < __builtin_inff() ? v[e] : __builtin_nanf("");
+          split8<PARTS>(x, q[nq][i][n]);
+        }
+      } else {
+        int e[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float x[16];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v[8];
+            to_f32<T>(qraw[nq][i][2 * b + k], v);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[8 * k + n] = v[n];
+          }
+          const uint32_t own = most_bits(x);  // (half of block 4 i + 2 b + g / 2)
+          const auto other = __builtin_amdgcn_permlane16_swap(own, own, false, false);
+          const uint32_t most = other[0] > other[1] ? other[0] : other[1];
+          e[b] = plane_exponent(most);
+          if (b == 0) e4m3_planes<0>(x, e[b], qh[nq][i], ql[nq][i]);
+          else e4m3_planes<4>(x, e[b], qh[nq][i], ql[nq][i]);
+          if (most >= 0x7F800000u) e[b] = 255;  // infinite or NaN: so are all of its products
+        }
+        // the scale of block 4 i + g goes with lanes g
+        const int first = __shfl(e[0], r16 + 32 * (g & 1)), second = __shfl(e[1], r16 + 32 * (g & 1));
+        e0[nq][i] = g < 2 ? first : second;
+        e1[nq][i] = e0[nq][i] == 255 ? 255 : e0[nq][i] - 5;
+      }
     }
 
+  // One step: the copies of step + RING - 1 into the stage that was read last, once those reads are
+  // done, then this step's tokens.
+  const auto pass = [&](int step, const uint8_t* stage, uint8_t* to) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0
+    asm volatile("" ::: "memory");
+    copy(to, step + RING - 1);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((RING - 1) * COPIES | 0xF70);  // vmcnt
+    asm volatile("" ::: "memory");
+    const int t = t_first + step * STRIDE;
+    const uint8_t* mine = stage + wave * STAGE;
+    u32x4 kr[2][NI];
+    VRaw vr[2];
+    uint32_t ks[2][NI], vs[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        kr[u][i] = *(const u32x4*)(mine + (D == 64 ? u * 512 + ((g & 1) * 16 + r16) * 16
+                                                   : (u * NI + i) * 1024 + lane * 16));
+        const uint32_t b = mine[32 * D + u * 16 * NB + r16 * NB + (D == 64 ? g & 1 : g) + 4 * i];
+        ks[u][i] = bad >> (2 * RING - 1 - u) & 1 ? 255u : b;
+      }
+      vr[u] = *(const VRaw*)(mine + 16 * D + u * 8 * D + lane * 4 * NB);
+      vs[u] = *(const uint32_t*)(mine + 32 * D + 32 * NB + u * 16 * NB + (g * NB + r16 * NB / 16) * 4);
+    }
     // ---- scores
     float s[NQ][2][4];
 #pragma unroll
@@ -216,16 +267,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
       for (int nq = 0; nq < NQ; ++nq) c[nq] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const u32x4 kk = raw.k[u][i];
-        const uint32_t sb = raw.ks[u][i];
+        const u32x4 kk = kr[u][i];
+        const uint32_t sb = ks[u][i];
         if constexpr (F32) {
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            bf16x8 k = fp4x8_to_bf16x8(kk[n], __uint_as_float(sb << 23));
-            if (sb > kMaxScaleByte) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) k[e] = (__bf16)__builtin_nanf("");
-            }
+            const bf16x8 k = fp4x8_to_bf16x8(kk[n], __uint_as_float(sb << 23));  // (255: NaN)
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
@@ -254,7 +301,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float x = s[nq][u][e] * qk_scale;
-            if (a.softcap > 0.f) x = capped(x, a.softcap, inv_cap) * kLog2e;
+            if (a.softcap > 0.f) x = capped<F32>(x, a.softcap, cap_k) * kLog2e;
             const int j = t + 16 * u + 4 * g + e;
             if (a.slopes) x -= slope[nq] * (float)abs(sq.n - sq.m + tok[nq] - j);
             s[nq][u][e] = x;
@@ -274,11 +321,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
 
     // ---- values that are NaN (or, behind the last token, anything): 0 in the product, and NaN
     // in the channels of the rows that see them
-    if (__ballot((over_bytes(raw.vs[0]) | over_bytes(raw.vs[1])) != 0)) {
+    if (__ballot((over_bytes(vs[0]) | over_bytes(vs[1])) != 0)) {
       bf16x8 nan;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        nan[e] = (__bf16)(((raw.vs[e / 4] >> (8 * (e & 3))) & 0xFF) > kMaxScaleByte ? 1.f : 0.f);
+        nan[e] = (__bf16)(((vs[e / 4] >> (8 * (e & 3))) & 0xFF) > kMaxScaleByte ? 1.f : 0.f);
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
         bf16x8 seen;
@@ -301,7 +348,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          if (((raw.vs[u] >> (8 * b)) & 0xFF) > kMaxScaleByte) raw.vs[u] &= ~(0xFFu << (8 * b));
+          if (((vs[u] >> (8 * b)) & 0xFF) > kMaxScaleByte) vs[u] &= ~(0xFFu << (8 * b));
     }
 
     // ---- softmax.  A row's base is raised when its maximum has grown by 2^8 (or is the first):
@@ -332,17 +379,15 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
         for (int e = 0; e < 4; ++e) {
           const float w = exp2_fast(fmaf(s[nq][u][e], unit_scale, -base));
           l[nq] += w;
-          __bf16 part[PARTS];
-          split<PARTS>(w, part);
-#pragma unroll
-          for (int k = 0; k < PARTS; ++k) p[nq][k][4 * u + e] = part[k];
+          s[nq][u][e] = w;
         }
+      split8<PARTS>(s[nq], p[nq]);
     }
 
     // ---- out
     float sc[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sc[e] = scale_byte(raw.vs[e / 4], e & 3);
+    for (int e = 0; e < 8; ++e) sc[e] = scale_byte(vs[e / 4], e & 3);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       // channels 2b and 2b + 1 of the lane's run, 8 tokens
@@ -350,7 +395,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int byte = (e & 3) * NB + b;  // of the 4 NB loaded
-        const uint32_t w = raw.v[e / 4][byte / 4];
+        const uint32_t w = vr[e / 4][byte / 4];
         bf16x2 y;
         switch (byte & 3) {
           case 0: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc[e], 0); break;
@@ -377,65 +422,97 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
               __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[nq][k], acc[nq][2 * b + 1], 0, 0, 0);
         }
     }
-    raw = next;
+  };
+  for (int step = 0; step < n_steps; step += RING) {
+#pragma unroll
+    for (int i = 0; i < RING; ++i) {
+      if (step + i >= n_steps) break;
+      pass(step + i, ring[i], ring[(i + RING - 1) % RING]);
+    }
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0: no copy is on its way into the stages
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) l[nq] = sum16(l[nq]);
 
+  if (a.target && piece == 0 && kvh == 0 && g == 0 && (!SHARED || wave == 0)) {
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+      if (real[nq] && head[nq] == 0) put_record(a, f, tok[nq], see[nq]);
+  }
+
   // ---- the waves' parts into one
-  const int64_t slot0 = (item * a.kv_heads + kvh) * a.tile_rows + (SHARED ? 0 : wave * 16 * NQ);
+  const int64_t slot0 =
+      (((int64_t)item * a.kv_heads + kvh) << a.tile_log) + (SHARED ? 0 : wave * 16 * NQ);
   if constexpr (SHARED) {
-    constexpr int LD = D + 4, LANES = 4 * WAVES, PER = D / LANES;  // threads of a row, their channels
-    __shared__ __attribute__((aligned(16))) float joined[WAVES][16][LD];
-    __shared__ float ml[WAVES][16][2];
+    // (through the first stage's memory, half of a run's channels at a time)
+    constexpr int HC = NC / 2, LD = D / 2 + 4, LANES = 4 * WAVES, PER = D / 2 / LANES;
+    static_assert(16 * LD * 4 <= STAGE && PER >= 1 && HC % PER == 0);
+    __shared__ float ml[NQ][WAVES][16][2];
+    float(*joined)[LD] = (float(*)[LD])(ring0 + wave * STAGE);
+    const int row = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * PER;  // of D/2
+    if (g == 0) {
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+        ml[nq][wave][r16][0] = m[nq];
+        ml[nq][wave][r16][1] = l[nq];
+      }
+    }
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
-      if (nq) __syncthreads();
-      if (g == 0) {
-        ml[wave][r16][0] = m[nq];
-        ml[wave][r16][1] = l[nq];
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int j = 0; j < NC; j += 4)
-          *(f32x4*)&joined[wave][r16][NC * (4 * g + e) + j] =
-              f32x4{acc[nq][j][e], acc[nq][j + 1][e], acc[nq][j + 2][e], acc[nq][j + 3][e]};
-      __syncthreads();
-      const int row = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * PER;
       const int r = trow0 + 16 * nq + row;
-      if (r >= rows_here) continue;
-      float top = -__builtin_inff();
+      int token, hd;
+      rs.at(a, 16 * nq + row, token, hd);
+      hd += kvh * a.group;
+      float top = -__builtin_inff(), sum = 0.f, k[WAVES];
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, ml[w][row][0]);
-      const float base = top == -__builtin_inff() ? 0.f : top;
-      float sum = 0.f, o[PER] = {};
+      for (int half = 0; half < 2; ++half) {
+        __syncthreads();
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) {
-        // (a wave without weights has nothing to add, and its base is no number to take an
-        // exponential with)
-        const float lw = ml[w][row][1], k = lw == 0.f ? 0.f : exp2_fast(ml[w][row][0] - base);
-        sum += lw * k;
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < PER; ++j) o[j] += joined[w][row][ch + j] * k;
-      }
-      if (f.pieces > 1) {
-        const int64_t slot = slot0 + 16 * nq + row;
-        __builtin_memcpy(a.part + slot * D + ch, o, sizeof(o));
-        if (ch == 0) {
-          a.part[a.ml_at + 2 * slot] = top;
-          a.part[a.ml_at + 2 * slot + 1] = sum;
+          for (int j = 0; j < HC; j += 2)
+            *(f32x2*)&joined[r16][HC * (4 * g + e) + j] =
+                f32x2{acc[nq][half * HC + j][e], acc[nq][half * HC + j + 1][e]};
+        __syncthreads();
+        if (half == 0) {
+#pragma unroll
+          for (int w = 0; w < WAVES; ++w) top = fmaxf(top, ml[nq][w][row][0]);
+          const float base = top == -__builtin_inff() ? 0.f : top;
+#pragma unroll
+          for (int w = 0; w < WAVES; ++w) {
+            // (a wave without weights has nothing to add, and its base is no number to take an
+            // exponential with)
+            const float lw = ml[nq][w][row][1];
+            k[w] = lw == 0.f ? 0.f : exp2_fast(ml[nq][w][row][0] - base);
+            sum += lw * k[w];
+          }
         }
-      } else {
-        const int token = r / a.group, hd = kvh * a.group + r - token * a.group;
-        const Sight sg = sight_of(a, sq, token);
-        const bool sees = sg.lo < sg.hi;
-        const float inv = 1.f / sum;
-        T res[PER];
+        float o[PER] = {};
 #pragma unroll
-        for (int j = 0; j < PER; ++j) res[j] = (T)(sees ? o[j] * inv : 0.f);
-        T* dst = (T*)a.out + (int64_t)(sq.row0 + token) * a.ld_out + hd * a.hs_out + ch;
-        __builtin_memcpy(dst, res, sizeof(res));
+        for (int w = 0; w < WAVES; ++w) {
+          const float* from = (const float*)(ring0 + w * STAGE) + row * LD + ch;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) o[j] += from[j] * k[w];
+        }
+        if (r >= rows_here) continue;
+        const int c = ch / HC * NC + half * HC + ch % HC;  // channel of the first
+        if (f.pieces > 1) {
+          const int64_t slot = slot0 + 16 * nq + row;
+          __builtin_memcpy(a.part + slot * D + c, o, sizeof(o));
+          if (ch == 0 && half == 0) {
+            a.part[a.ml_at + 2 * slot] = top;
+            a.part[a.ml_at + 2 * slot + 1] = sum;
+          }
+        } else {
+          const Sight sg = sight_of(a, sq, token);
+          const bool sees = sg.lo < sg.hi;
+          const float inv = 1.f / sum;
+          T res[PER];
+#pragma unroll
+          for (int j = 0; j < PER; ++j) res[j] = (T)(sees ? o[j] * inv : 0.f);
+          T* dst = (T*)a.out + (int64_t)(sq.row0 + token) * a.ld_out + hd * a.hs_out + c;
+          __builtin_memcpy(dst, res, sizeof(res));
+        }
       }
     }
   } else {
@@ -469,63 +546,87 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   }
 }
 
-// Pieces into rows: a wave for each (row, head), a lane for each piece's base and sum, then for each
-// D/64 channels.
-template <typename T, int D>
+// Pieces into rows: WAVES waves for each (row, head).  A lane has a piece's base and sum, then D/64
+// channels of pieces w, w + WAVES, ..
+template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
   constexpr int PER = D / 64, BATCH = 8;
-  const int lane = lane_id();
-  const int64_t at = (int64_t)blockIdx.x * 4 + uniform((int)(threadIdx.x >> 6));
-  if (at >= (int64_t)a.rows * a.n_heads) return;
-  const int row = uniform((int)(at / a.n_heads)), head = uniform((int)(at - (int64_t)row * a.n_heads));
-  int cut;
-  Found f;
-  if (!find_piece(a, 0, row, f, cut) || f.pieces == 1) return;
-  const int kvh = head / a.group, token = row - f.seq.row0;
-  const int r = token * a.group + head - kvh * a.group;
-  const int tile = r / a.tile_rows;
-  const int64_t item0 = f.first_item + (int64_t)(f.seq.tiles(a) - 1 - tile) * f.pieces;
-  if (item0 + f.pieces > a.items) return;  // (sequences that overlap)
-  const int64_t slot0 = (item0 * a.kv_heads + kvh) * a.tile_rows + (r - tile * a.tile_rows);
-  const int64_t step = (int64_t)a.kv_heads * a.tile_rows;
+  const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
+  const int row = blockIdx.x, head = WAVES == 1 ? blockIdx.y * 4 + wave : blockIdx.y;
+  const int w0 = WAVES == 1 ? 0 : wave;
+  if (head >= a.n_heads) return;
+  if (a.q_offsets && (row < a.q_offsets[0] || row >= a.q_offsets[a.n_seqs])) return;
+  const RowRecord rec = ((const RowRecord*)(a.part + a.rec_at))[row];
+  const bool sees = rec.pieces > 0;
+  const int pieces = sees ? rec.pieces : -rec.pieces;
+  if (pieces == 1) return;
+  const int kvh = head / a.group;
+  const int r = (row - rec.row0) * a.group + head - kvh * a.group, tile = r >> a.tile_log;
+  const int64_t item0 = rec.first_item + (int64_t)(rec.tiles - 1 - tile) * pieces;
+  if (pieces < 1 || item0 < 0 || item0 + pieces > a.items) return;  // (offsets that overlap)
+  const int64_t slot0 = ((item0 * a.kv_heads + kvh) << a.tile_log) + (r - (tile << a.tile_log));
+  const int64_t step = (int64_t)a.kv_heads << a.tile_log;
   const float* ml = a.part + a.ml_at;
   float top = -__builtin_inff(), sum = 0.f, o[PER] = {};
-  for (int p0 = 0; p0 < f.pieces; p0 += 64) {  // (more than 64: the rest with a base of its own)
-    const int n = f.pieces - p0 < 64 ? f.pieces - p0 : 64;
+  for (int p0 = 0; p0 < pieces; p0 += 64) {
+    const int n = pieces - p0 < 64 ? pieces - p0 : 64;
     float mine = -__builtin_inff(), lp = 0.f;
     if (lane < n) {
       mine = ml[2 * (slot0 + (p0 + lane) * step)];
       lp = ml[2 * (slot0 + (p0 + lane) * step) + 1];
     }
-    const float up = fmaxf(top, wave_max(mine)), base = up == -__builtin_inff() ? 0.f : up;
-    // (a piece without weights has nothing to add, and may hold no numbers)
-    const float k = lp == 0.f ? 0.f : exp2_fast(mine - base);
-    const float old = exp2_fast(top - base);
-    sum = sum * old + wave_sum(lp == 0.f ? 0.f : lp * k);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) o[j] *= old;
-    top = up;
     const float* src = a.part + (slot0 + p0 * step) * D + lane * PER;
-    const bool skip = lp == 0.f;
-    const uint64_t skips = __ballot(skip);
-    for (int p = 0; p < n; p += BATCH) {
+    float up = -__builtin_inff(), k = 0.f;
+    uint64_t skips = 0;
+    for (int p = w0; p < n; p += BATCH * WAVES) {
       float v[BATCH][PER];
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const int at_p = p + i < n ? p + i : n - 1;
+        const int at_p = p + i * WAVES < n ? p + i * WAVES : n - 1;
         __builtin_memcpy(v[i], src + at_p * step * D, sizeof(v[i]));
+      }
+      if (p == w0) {  // (while the first ones are on their way)
+        up = fmaxf(top, wave_max(mine));
+        const float base = up == -__builtin_inff() ? 0.f : up, old = exp2_fast(top - base);
+        // (a piece without weights has nothing to add, and may hold no numbers)
+        k = lp == 0.f ? 0.f : exp2_fast(mine - base);
+        skips = __ballot(lp == 0.f);
+        sum = sum * old + wave_sum(lp == 0.f ? 0.f : lp * k);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) o[j] *= old;
+        top = up;
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        if (p + i >= n || ((skips >> (p + i)) & 1)) continue;
-        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k), p + i));
+        const int at_p = p + i * WAVES;
+        if (at_p >= n || ((skips >> at_p) & 1)) continue;
+        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k), at_p));
 #pragma unroll
         for (int j = 0; j < PER; ++j) o[j] += v[i][j] * w;
       }
     }
+    if (w0 >= n) {  // (no piece for this wave among these: their base and sum all the same)
+      up = fmaxf(top, wave_max(mine));
+      const float base = up == -__builtin_inff() ? 0.f : up, old = exp2_fast(top - base);
+      sum = sum * old + wave_sum(lp == 0.f ? 0.f : lp * exp2_fast(mine - base));
+#pragma unroll
+      for (int j = 0; j < PER; ++j) o[j] *= old;
+      top = up;
+    }
   }
-  const Sight sg = sight_of(a, f.seq, token);
-  const bool sees = sg.lo < sg.hi;
+  if constexpr (WAVES > 1) {
+    __shared__ float others[WAVES - 1][64 * PER];
+    if (wave) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) others[wave - 1][lane * PER + j] = o[j];
+    }
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int w = 0; w < WAVES - 1; ++w)
+#pragma unroll
+      for (int j = 0; j < PER; ++j) o[j] += others[w][lane * PER + j];
+  }
   const float inv = 1.f / sum;
   T res[PER];
 #pragma unroll
@@ -561,6 +662,9 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
   p.quantum = p.shared ? 128 : 64;
   // workgroups that the chip holds at once
   int64_t full = (p.chunk_waves ? 2 : resident(f32, C->head_dim, p.nq)) * cus;
+#ifdef FILL
+  if (!p.chunk_waves) full = FILL * cus;
+#endif
   if (p.chunk_waves && C->head_dim < 256 &&
       tiles_of(rows, group, n_seqs, 256) * C->n_heads >= cus) {
     p.chunk_waves = 8;
@@ -576,12 +680,13 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
   return p;
 }
 
-static int64_t part_floats(const moe_kv_cache_t* C, int64_t items, int64_t tile_rows) {
-  return items * C->n_heads * tile_rows * (C->head_dim + 2);
+// Floats of a cut call's workspace: the pieces' rows, their bases and sums, the rows' records.
+static int64_t part_floats(const moe_kv_cache_t* C, int64_t items, int64_t tile_rows, int64_t rows) {
+  return items * C->n_heads * tile_rows * (C->head_dim + 2) + 4 * rows;
 }
 
 static bool attn_sizes_ok(const moe_attn_t* A, const moe_kv_cache_t* C) {
-  return A->n_heads >= 1 && A->n_heads <= 65536 && A->n_heads % C->n_heads == 0;
+  return A->n_heads >= 1 && A->n_heads <= 16384 && A->n_heads % C->n_heads == 0;
 }
 
 template <typename T, int D>
@@ -589,9 +694,9 @@ static void attn_launch(const AttnArgs& a, const AttnPlan& p, hipStream_t stream
   if (p.chunk_waves) {
     attn_chunk_launch(a, D, p.chunk_waves, stream);
   } else {
-    const dim3 grid((unsigned)(p.items * a.kv_heads));
-    // (16 waves have 128 registers each)
-    constexpr int WIDE = sizeof(T) == 4 || D == 256 ? 8 : 16;
+    const dim3 grid = item_grid(p.items, a.kv_heads);
+    // (16 waves have 128 registers each, 8 have 256)
+    constexpr int WIDE = sizeof(T) == 4 || D != 128 ? 8 : 16, WIDE2 = D == 256 ? 4 : 8;
     if constexpr (sizeof(T) == 4) {
       auto k = !p.shared  ? attn_rows_kernel<T, D, 1, 4, false>
                : p.wide   ? attn_rows_kernel<T, D, 1, WIDE, true>
@@ -600,15 +705,17 @@ static void attn_launch(const AttnArgs& a, const AttnPlan& p, hipStream_t stream
     } else {
       auto k = p.nq == 1 ? (p.wide ? attn_rows_kernel<T, D, 1, WIDE, true>
                                    : attn_rows_kernel<T, D, 1, 4, true>)
-                         : (p.wide ? attn_rows_kernel<T, D, 2, 8, true>
+                         : (p.wide ? attn_rows_kernel<T, D, 2, WIDE2, true>
                                    : attn_rows_kernel<T, D, 2, 4, true>);
-      hipLaunchKernelGGL(k, grid, dim3(!p.wide ? 256 : p.nq == 1 ? 64 * WIDE : 512), 0, stream, a);
+      hipLaunchKernelGGL(k, grid, dim3(64 * (!p.wide ? 4 : p.nq == 1 ? WIDE : WIDE2)), 0, stream, a);
     }
   }
   if (p.target) {
-    const int64_t waves = (int64_t)a.rows * a.n_heads;
-    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0,
-                       stream, a);
+    // a workgroup for each row's head while they are few
+    const bool many = (int64_t)a.rows * a.n_heads > 2048;
+    const dim3 grid((unsigned)a.rows, (unsigned)(many ? (a.n_heads + 3) / 4 : a.n_heads));
+    auto join = many ? attn_join_kernel<T, D, 1> : attn_join_kernel<T, D, 4>;
+    hipLaunchKernelGGL(join, grid, dim3(256), 0, stream, a);
   }
 }
 
@@ -631,7 +738,8 @@ extern "C" size_t moe_attn_cache_workspace_bytes(const moe_attn_t* A, const moe_
     const int64_t target = (full + heads - 1) / heads;
     int64_t tiles = tiles_of(rows, group, n_seqs, tile_rows);
     tiles = tiles < target ? tiles : target;
-    const int64_t n = part_floats(C, tiles + target, tile_rows);
+    const int64_t most_rows = target * tile_rows;
+    const int64_t n = part_floats(C, tiles + target, tile_rows, rows < most_rows ? rows : most_rows);
     most = n > most ? n : most;
   }
   return (size_t)most * 4;
@@ -669,7 +777,7 @@ extern "C" int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, cons
   if (cus <= 0) cus = 256;
   const AttnPlan p = attn_plan(A, C, type == MOE_TYPE_F32, rows, n_seqs,
                                (int64_t)max_pages * C->page, cus);
-  const int64_t need = p.target ? 4 * part_floats(C, p.items, p.tile_rows) : 0;
+  const int64_t need = p.target ? 4 * part_floats(C, p.items, p.tile_rows, rows) : 0;
   if (need && !ws) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < (size_t)need) return MOE_ERR_WORKSPACE;
   if (need && !aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
@@ -690,6 +798,7 @@ extern "C" int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, cons
   a.hs_out = hs_out;
   a.ld_table = n_seqs > 1 ? ld_table : 0;
   a.ml_at = p.items * C->n_heads * p.tile_rows * C->head_dim;
+  a.rec_at = a.ml_at + 2 * p.items * C->n_heads * p.tile_rows;
   a.rows = rows;
   a.n_seqs = n_seqs;
   a.n_heads = A->n_heads;
@@ -701,7 +810,8 @@ extern "C" int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, cons
   a.window = A->window;
   a.target = p.target;
   a.items = p.items;
-  a.tile_rows = p.tile_rows;
+  a.tile_log = __builtin_ctz((unsigned)p.tile_rows);
+  a.group_inv = (uint32_t)((((uint64_t)1 << 32) / (uint32_t)a.group) + 1);
   a.quantum = p.quantum;
   a.scale = A->scale;
   a.softcap = A->softcap;

@@ -40,24 +40,27 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
 
   const int wave = uniform((int)(threadIdx.x >> 6)), lane = lane_id();
   const int q32 = lane & 31, h = lane >> 5;
-  const int64_t item = blockIdx.x / a.kv_heads;
-  const int kvh = (int)(blockIdx.x - item * a.kv_heads);
+  const int item = block_item(), kvh = blockIdx.x;
 
   int cut;
   Found f;
   if (!find_item(a, item, f, cut)) return;
   const Seq& sq = f.seq;
-  const int local = (int)(item - f.first_item);
+  const int local = item - f.first_item;
   // the last rows first: they see the most tokens
-  const int tile = sq.tiles(a) - 1 - local / f.pieces, piece = local % f.pieces;
+  const int up = f.pieces == 1 ? local : local / f.pieces, piece = local - up * f.pieces;
+  const int tile = sq.tiles(a) - 1 - up;
   const int rows_here = sq.m * a.group;
-  const int tile0 = tile * a.tile_rows, row0 = tile0 + 32 * wave;
+  const int tile0 = tile << a.tile_log, row0 = tile0 + 32 * wave;
+  const RowSplit rs(a, tile0);
 
   // this lane's row, and what it sees
   const int r = row0 + q32;
   const bool real = r < rows_here;
-  const int tok = (real ? r : 0) / a.group;
-  const int head = kvh * a.group + (real ? r : 0) - tok * a.group;
+  int tok, head;
+  rs.at(a, 32 * wave + q32, tok, head);
+  if (!real) tok = head = 0;
+  head += kvh * a.group;
   Sight see = sight_of(a, sq, tok);
   if (!real) see = {0, 0};
   const float slope = a.slopes && real ? a.slopes[head] * kLog2e : 0.f;
@@ -97,15 +100,17 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
   }
 
   // the tokens of the workgroup's rows, of this wave's, and those that all of the wave's rows see
-  const auto row_sight = [&](int row) {
-    return sight_of(a, sq, (row < rows_here ? row : rows_here - 1) / a.group);
+  const auto row_sight = [&](int i) {
+    int t, hd;
+    rs.at(a, i, t, hd);
+    return sight_of(a, sq, uniform(t < sq.m - 1 ? t : sq.m - 1));
   };
   const int64_t p0 = sq.first(a) + (int64_t)piece * cut;
-  const int wg_lo0 = row_sight(tile0).lo, wg_hi0 = row_sight(tile0 + a.tile_rows - 1).hi;
+  const int wg_lo0 = row_sight(0).lo, wg_hi0 = row_sight(32 * WAVES - 1).hi;
   const int wg_lo = p0 > wg_lo0 ? (int)p0 : wg_lo0 & ~(kStep - 1);
   const int wg_hi = p0 + cut < wg_hi0 ? (int)(p0 + cut) : wg_hi0;
   const bool any = row0 < rows_here;
-  const Sight s0 = row_sight(row0), s1 = row_sight(row0 + 31);
+  const Sight s0 = row_sight(32 * wave), s1 = row_sight(32 * wave + 31);
   const int lo = s0.lo, hi = any ? s1.hi : 0;
   const int all_lo = s1.lo, all_hi = s0.hi;
 
@@ -209,7 +214,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
 
   const bool plain = a.softcap == 0.f && !a.slopes && a.scale > 0.f;
   const float qk_scale = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
-  const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+  const float cap_k = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
   const float unit_scale = plain ? qk_scale : 1.f;
 
   if (wg_lo < wg_hi) {
@@ -247,7 +252,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float x = s[u][e] * qk_scale;
-            if (a.softcap > 0.f) x = capped(x, a.softcap, inv_cap) * kLog2e;
+            if (a.softcap > 0.f) x = capped<false>(x, a.softcap, cap_k) * kLog2e;
             const int j = t + 32 * u + 8 * (e >> 2) + 4 * h + (e & 3);
             if (a.slopes) x -= slope * (float)abs(place - j);
             s[u][e] = x;
@@ -330,20 +335,24 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
   }
   l = sum2(l);
 
+  if (a.target && piece == 0 && kvh == 0 && h == 0 && real && head == 0) put_record(a, f, tok, see);
+
   // ---- rows out: through LDS, a block of channels at a time, so that they leave in order
   const bool sees = see.lo < see.hi;
   const bool part = f.pieces > 1;
   const float inv = part ? 1.f : sees ? 1.f / l : 0.f;
-  const int64_t slot0 = ((int64_t)item * a.kv_heads + kvh) * a.tile_rows + 32 * wave;
+  const int64_t slot0 = (((int64_t)item * a.kv_heads + kvh) << a.tile_log) + 32 * wave;
   if (part && real && h == 0) {
     a.part[a.ml_at + 2 * (slot0 + q32)] = m;
     a.part[a.ml_at + 2 * (slot0 + q32) + 1] = l;
   }
   float* mine = (float*)vbuf + wave * 32 * LD;
   const int orow = lane >> 1, oc = (lane & 1) * 16;
-  const int orr = row0 + orow, otok = (orr < rows_here ? orr : 0) / a.group;
-  const int ohead = kvh * a.group + (orr < rows_here ? orr : 0) - otok * a.group;
-  __bf16* dst = (__bf16*)a.out + (int64_t)(sq.row0 + otok) * a.ld_out + ohead * a.hs_out + oc;
+  const int orr = row0 + orow;
+  int otok, ohead;
+  rs.at(a, 32 * wave + orow, otok, ohead);
+  __bf16* dst = (__bf16*)a.out + (int64_t)(sq.row0 + otok) * a.ld_out +
+                (int64_t)(kvh * a.group + ohead) * a.hs_out + oc;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -372,7 +381,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
 
 template <int D, int WAVES>
 static void launch_one(const AttnArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_chunk_kernel<D, WAVES>), dim3((unsigned)(a.items * a.kv_heads)),
+  hipLaunchKernelGGL((attn_chunk_kernel<D, WAVES>), item_grid(a.items, a.kv_heads),
                      dim3(64 * WAVES), 0, stream, a);
 }
 
