@@ -27,6 +27,23 @@ struct KvUnit {
   __host__ __device__ int v_scales() const { return page * (D + NB); }
 };
 
+// 8 consecutive elements of a row, rounded once; PAST: past the L2s, for results of large calls.
+template <typename T, bool PAST>
+__device__ inline void store8(T* p, const float (&v)[8]) {
+  T o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = (T)v[i];
+  if constexpr (PAST) {
+    typedef u32x4 piece __attribute__((aligned(2)));  // (rows need their elements' alignment alone)
+    u32x4 w[sizeof(o) / 16];
+    __builtin_memcpy(w, o, sizeof(o));
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(o) / 16); ++i) __builtin_nontemporal_store(w[i], (piece*)p + i);
+  } else {
+    __builtin_memcpy(p, o, sizeof(o));
+  }
+}
+
 // The largest scale byte that a write leaves; what lies above reads as NaN.
 constexpr uint32_t kMaxScaleByte = 252;
 

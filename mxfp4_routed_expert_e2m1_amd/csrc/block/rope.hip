@@ -47,33 +47,31 @@ __device__ inline void load_some(const T* p, int n, float (&v)[8]) {
     to_f32<T>(r, v);
   }
 }
-template <typename T>
+template <typename T, bool PAST>
 __device__ inline void store_some(T* p, int n, const float (&v)[8]) {
-  T o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = (T)v[i];
   if (n == 8) {
-    __builtin_memcpy(p, o, sizeof(o));
+    store8<T, PAST>(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = o[i];
+      if (i < n) p[i] = (T)v[i];
   }
 }
 
 // A thread's chunk: 8 pairs (the last chunk of a head fewer), or, from `pair_chunks` on, 8
-// channels to copy.  Chunks of a (row, group of `hpt` heads) lie side by side.
-template <typename T, bool INTERLEAVED>
+// channels to copy.  Chunks of a (row, group of `hpt` heads) lie side by side, in a power of two of
+// threads.
+template <typename T, bool INTERLEAVED, bool PAST>
 __global__ __launch_bounds__(256) void rope_kernel(
-    const T* __restrict__ x, int64_t ld_x, int64_t hs_x, int64_t threads, int n_heads, int dim,
-    int half, int pair_chunks, int chunks, int hpt, int groups, const int32_t* __restrict__ pos,
+    const T* __restrict__ x, int64_t ld_x, int64_t hs_x, int rows, int n_heads, int dim, int half,
+    int pair_chunks, int chunks, int chunk_log, int hpt, int groups, const int32_t* __restrict__ pos,
     int64_t ld_pos, const uint64_t* __restrict__ steps, const uint8_t* __restrict__ axes,
     int n_axes, float scale, T* __restrict__ out, int64_t ld_out, int64_t hs_out) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= threads) return;
-  const int64_t rg = t / chunks;
-  const int c = (int)(t - rg * chunks);
-  const int64_t row = rg / groups;
+  const int64_t rg = t >> chunk_log;
+  const int c = (int)(t - (rg << chunk_log));
+  const int64_t row = groups == 1 ? rg : (int64_t)((uint32_t)rg / (uint32_t)groups);
+  if (row >= rows || c >= chunks) return;
   const int h0 = (int)(rg - row * groups) * hpt;
   const int h1 = h0 + hpt < n_heads ? h0 + hpt : n_heads;
   x += row * ld_x;
@@ -84,22 +82,39 @@ __global__ __launch_bounds__(256) void rope_kernel(
     for (int h = h0; h < h1; ++h) {
       float v[8];
       load_some<T>(x + h * hs_x + at, n, v);
-      store_some<T>(out + h * hs_out + at, n, v);
+      store_some<T, PAST>(out + h * hs_out + at, n, v);
     }
     return;
   }
   const int i0 = 8 * c, n = half - i0 < 8 ? half - i0 : 8;
+  // everything that the angles are made of in one round of loads: positions of up to 4 axes, of
+  // which each pair takes its own
+  uint64_t step[8];
+  uint8_t axis[8] = {};
+  if (n == 8) {
+    __builtin_memcpy(step, steps + i0, sizeof(step));
+    if (axes) __builtin_memcpy(axis, axes + i0, sizeof(axis));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      step[i] = i < n ? steps[i0 + i] : 0;
+      axis[i] = axes && i < n ? axes[i0 + i] : 0;
+    }
+  }
+  int32_t at[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) at[k] = pos[(k < n_axes ? k : 0) * ld_pos + row];
   float sn[8], cs[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int p = i0 + (i < n ? i : 0);
-    int a = axes ? axes[p] : 0;
-    a = a < n_axes ? a : 0;
-    const int64_t at = pos[a * ld_pos + row];
-    sincos_turns((uint64_t)at * steps[p], sn[i], cs[i]);
+    const int k = axis[i];
+    int64_t p = k == 1 ? at[1] : k == 2 ? at[2] : k == 3 ? at[3] : at[0];
+    if (k > 3 && k < n_axes) p = pos[k * ld_pos + row];
+    sincos_turns((uint64_t)p * step[i], sn[i], cs[i]);
     sn[i] *= scale;
     cs[i] *= scale;
   }
+#pragma unroll 2
   for (int h = h0; h < h1; ++h) {
     const T* xp = x + h * hs_x;
     T* op = out + h * hs_out;
@@ -129,8 +144,8 @@ __global__ __launch_bounds__(256) void rope_kernel(
         f[2 * i] = u[4 + i];
         f[2 * i + 1] = w[4 + i];
       }
-      store_some<T>(op + 2 * i0, n0, e);
-      if (n1) store_some<T>(op + 2 * i0 + 8, n1, f);
+      store_some<T, PAST>(op + 2 * i0, n0, e);
+      if (n1) store_some<T, PAST>(op + 2 * i0 + 8, n1, f);
     } else {
       load_some<T>(xp + i0, n, a);
       load_some<T>(xp + half + i0, n, b);
@@ -139,8 +154,8 @@ __global__ __launch_bounds__(256) void rope_kernel(
         u[i] = a[i] * cs[i] - b[i] * sn[i];
         w[i] = b[i] * cs[i] + a[i] * sn[i];
       }
-      store_some<T>(op + i0, n, u);
-      store_some<T>(op + half + i0, n, w);
+      store_some<T, PAST>(op + i0, n, u);
+      store_some<T, PAST>(op + half + i0, n, w);
     }
   }
 }
@@ -152,17 +167,23 @@ static void rope_launch(const moe_rope_t* R, const void* x, int64_t ld_x, int64_
   const int half = R->rot_dim / 2, pair_chunks = (half + 7) / 8;
   const bool in_place = x == out;
   const int chunks = pair_chunks + (in_place ? 0 : (dim - R->rot_dim + 7) / 8);
-  // a head per thread until that fills the chip, then up to 8
-  const int64_t full = (int64_t)256 * 2048;
+  // a head per thread until there are two workgroups for each CU, then up to 8 (4096 rows of 40 heads
+  // of 128, bf16: 17.0 us; 4 heads 18.1, 2 heads 28.5)
+  const int64_t full = (int64_t)256 * 512;
   int hpt = (int)((int64_t)rows * n_heads * chunks / full);
   hpt = hpt < 1 ? 1 : hpt > 8 ? 8 : hpt;
   const int groups = (n_heads + hpt - 1) / hpt;
-  const int64_t threads = (int64_t)rows * groups * chunks;
+  int chunk_log = 0;
+  while ((1 << chunk_log) < chunks) ++chunk_log;
+  const int64_t threads = ((int64_t)rows * groups) << chunk_log;
   const dim3 grid((unsigned)((threads + 255) / 256));
-  auto k = R->interleaved ? rope_kernel<T, true> : rope_kernel<T, false>;
-  hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, (const T*)x, ld_x, hs_x, threads, n_heads, dim,
-                     half, pair_chunks, chunks, hpt, groups, pos, ld_pos, R->steps, R->axes,
-                     R->n_axes, R->scale, (T*)out, ld_out, hs_out);
+  // (results of a call that fills the chip leave past the L2s)
+  const bool past = hpt > 1;
+  auto k = R->interleaved ? (past ? rope_kernel<T, true, true> : rope_kernel<T, true, false>)
+                          : (past ? rope_kernel<T, false, true> : rope_kernel<T, false, false>);
+  hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, (const T*)x, ld_x, hs_x, rows, n_heads, dim,
+                     half, pair_chunks, chunks, chunk_log, hpt, groups, pos, ld_pos, R->steps,
+                     R->axes, R->n_axes, R->scale, (T*)out, ld_out, hs_out);
 }
 
 }  // namespace moe
@@ -190,8 +211,8 @@ extern "C" int moe_rope(const moe_rope_t* R, const void* x, int x_type, int64_t 
   const size_t size = type_size(x_type);
   if (!aligned(x, size) || !aligned(out, size) || !aligned(pos, 4) || !aligned(R->steps, 8))
     return MOE_ERR_ALIGNMENT;
-  // (threads of a launch: a chunk of 8 channels of a row's head each)
-  if ((int64_t)rows * n_heads > ((int64_t)1 << 40) / head_dim) return MOE_ERR_SHAPE;
+  // (rows' groups of heads and workgroups of a launch)
+  if ((int64_t)rows * n_heads >= ((int64_t)1 << 32)) return MOE_ERR_SHAPE;
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
   if (x_type == MOE_TYPE_F32)
     rope_launch<float>(R, x, ld_x, hs_x, rows, n_heads, head_dim, pos, ld_pos, out, ld_out, hs_out,

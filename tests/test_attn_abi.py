@@ -93,8 +93,6 @@ def test_write_and_read_validation(write):
         assert call(**{k: MIS4}) == ALIGN
     for kw in (dict(ldk=63), dict(ldk=255), dict(hsk=63), dict(ldv=255), dict(hsv=63)):
         assert call(**kw) == STRIDE, kw
-    wide = dict(hsk=256, hsv=256, ldk=2**18, ldv=2**18)
-    assert call(K=cache(heads=1024, dim=256), rows=2**23, **wide) == SHAPE
 
 
 def attn(heads=8, window=0, scale=1.0, softcap=0.0, slopes=0):
