@@ -35,12 +35,12 @@ struct AttnArgs {
 // (token, head of the group) of rows near a tile's first, whose division is done once.
 struct RowSplit {
   int tok0, rem0;
-  __device__ RowSplit(const AttnArgs& a, int row) {
+  __device__ __forceinline__ RowSplit(const AttnArgs& a, int row) {
     tok0 = uniform((int)((uint32_t)row / (uint32_t)a.group));
     rem0 = row - tok0 * a.group;
   }
   // of row + i, where (group + i) * group < 2^32: i < 256 and groups of up to 2^14
-  __device__ void at(const AttnArgs& a, int i, int& tok, int& head) const {
+  __device__ __forceinline__ void at(const AttnArgs& a, int i, int& tok, int& head) const {
     const uint32_t x = rem0 + i, t = a.group == 1 ? x : __umulhi(x, a.group_inv);
     tok = tok0 + (int)t;
     head = (int)(x - t * a.group);
@@ -50,7 +50,7 @@ struct RowSplit {
 // A sequence's numbers, kept within what the arguments allow.
 struct Seq {
   int row0, m, n, prefix;  // first row, rows, cached tokens, prefix
-  __device__ void load(const AttnArgs& a, int s) {
+  __device__ __forceinline__ void load(const AttnArgs& a, int s) {
     if (a.q_offsets) {
       int r0 = a.q_offsets[s], r1 = a.q_offsets[s + 1];
       r0 = r0 < 0 ? 0 : r0 > a.rows ? a.rows : r0;
@@ -67,11 +67,11 @@ struct Seq {
     prefix = a.prefix ? a.prefix[s] : 0;
   }
   // tokens that any row sees lie from here (a multiple of kStep) to n
-  __device__ int first(const AttnArgs& a) const {
+  __device__ __forceinline__ int first(const AttnArgs& a) const {
     const int64_t f = a.window > 0 ? (int64_t)n - m - a.window + 1 : 0;
     return f > 0 ? (int)f & ~(kStep - 1) : 0;
   }
-  __device__ int tiles(const AttnArgs& a) const {  // (rows * group < 2^28)
+  __device__ __forceinline__ int tiles(const AttnArgs& a) const {  // (rows * group < 2^28)
     return (m * a.group + (1 << a.tile_log) - 1) >> a.tile_log;
   }
 };
@@ -84,7 +84,7 @@ struct Found {
 
 // Uncut calls: sequence s has its tiles from item q_offsets[s] * group / (tile's rows) + s on, which
 // leaves room for a last tile that is not full; the item's sequence by 64 probes at a time.
-__device__ inline bool find_tile(const AttnArgs& a, int item, Found& f) {
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int item, Found& f) {
   f.pieces = 1;
   if (!a.q_offsets) {  // a row each
     const int each = (a.group + (1 << a.tile_log) - 1) >> a.tile_log;
@@ -114,14 +114,14 @@ __device__ inline bool find_tile(const AttnArgs& a, int item, Found& f) {
   return item >= f.first_item && item - f.first_item < f.seq.tiles(a);
 }
 
-__device__ inline int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_incl_scan(v), 63); }
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_incl_scan(v), 63); }
 
 // Cut calls (few tiles, so few sequences): a piece has `cut` tokens, as many for every sequence, and
 // items are counted over the sequences.  The cut is the batch's work over `target` pieces where
 // that makes no more than `target` of them (a sequence's last piece is a whole one there), or over
 // fewer pieces by half a piece, or a whole one, for each tile.  (Counts of one sequence are kept below 2^24 or 2^25, so that offsets
 // that overlap cannot make a sum of 64 overflow.)
-__device__ inline bool find_piece(const AttnArgs& a, int item, Found& f, int& cut) {
+__device__ __forceinline__ bool find_piece(const AttnArgs& a, int item, Found& f, int& cut) {
   const int lane = lane_id();
   Seq q = {0, 0, 0, 0};
   int tiles = 0, span = 0;
@@ -191,14 +191,14 @@ __device__ inline bool find_piece(const AttnArgs& a, int item, Found& f, int& cu
 // Workgroups: key heads first, so that with 8 of them (or a multiple) each XCD's L2 has the tokens of
 // its own; then items, in two dimensions.
 constexpr unsigned kItemsY = 32768;
-__device__ inline int block_item() { return (int)(blockIdx.z * kItemsY + blockIdx.y); }
+__device__ __forceinline__ int block_item() { return (int)(blockIdx.z * kItemsY + blockIdx.y); }
 inline dim3 item_grid(int64_t items, int kv_heads) {
   const int64_t y = items < kItemsY ? items : kItemsY;
   return dim3((unsigned)kv_heads, (unsigned)y, (unsigned)((items + y - 1) / y));
 }
 
 // The item of a workgroup (false: there is none), the tokens of a piece.
-__device__ inline bool find_item(const AttnArgs& a, int item, Found& f, int& cut) {
+__device__ __forceinline__ bool find_item(const AttnArgs& a, int item, Found& f, int& cut) {
   cut = 0x40000000;
   if (item >= a.items) return false;
   return a.target ? find_piece(a, item, f, cut) : find_tile(a, item, f);
@@ -208,7 +208,7 @@ __device__ inline bool find_item(const AttnArgs& a, int item, Found& f, int& cut
 struct Sight {
   int lo, hi;
 };
-__device__ inline Sight sight_of(const AttnArgs& a, const Seq& s, int token) {
+__device__ __forceinline__ Sight sight_of(const AttnArgs& a, const Seq& s, int token) {
   const int i = s.n - s.m + token;  // the row's place
   Sight v;
   v.hi = i + 1 > s.prefix ? i + 1 : s.prefix;
@@ -224,32 +224,32 @@ __device__ inline Sight sight_of(const AttnArgs& a, const Seq& s, int token) {
 struct RowRecord {
   int first_item, pieces, tiles, row0;  // pieces negative: the row sees nothing
 };
-__device__ inline void put_record(const AttnArgs& a, const Found& f, int token, const Sight& see) {
+__device__ __forceinline__ void put_record(const AttnArgs& a, const Found& f, int token, const Sight& see) {
   RowRecord r = {f.first_item, see.lo < see.hi ? f.pieces : -f.pieces, f.seq.tiles(a), f.seq.row0};
   if (f.pieces == 1) r.pieces = 1;
   ((RowRecord*)(a.part + a.rec_at))[f.seq.row0 + token] = r;
 }
 
-__device__ inline float max16(float v) {  // over the lanes l % 16
+__device__ __forceinline__ float max16(float v) {  // over the lanes l % 16
   const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
   const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(t[0]), __uint_as_float(t[1]));
 }
-__device__ inline float sum16(float v) {
+__device__ __forceinline__ float sum16(float v) {
   const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
   const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(t[0]) + __uint_as_float(t[1]);
 }
 
-__device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // softcap * tanh(s / softcap); k = 2 log2(e) / softcap.  For bf16
 // calls cap - 2 cap / (1 + e^2x); for f32 ones (1 - e^-2x) / (1 + e^-2x), the reciprocal refined:
 // off by at most 2^-24 of the cap, which is what a score near it is rounded to.
 template <bool F32>
-__device__ inline float capped(float s, float cap, float k) {
+__device__ __forceinline__ float capped(float s, float cap, float k) {
   if constexpr (!F32) {
     return fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + exp2_fast(s * k)), cap);
   } else {
@@ -261,10 +261,10 @@ __device__ inline float capped(float s, float cap, float k) {
 }
 
 // 4 scale bytes, any above kMaxScaleByte (253..255)?
-__device__ inline uint32_t over_bytes(uint32_t x) {
+__device__ __forceinline__ uint32_t over_bytes(uint32_t x) {
   return ((x & 0x7F7F7F7Fu) + 0x03030303u) & x & 0x80808080u;
 }
-__device__ inline float scale_byte(uint32_t word, int b) {
+__device__ __forceinline__ float scale_byte(uint32_t word, int b) {
   return __uint_as_float((b == 0 ? word << 23 : b == 3 ? word >> 1 : word >> (8 * b) << 23) & 0x7F800000u);
 }
 
@@ -272,7 +272,7 @@ __device__ inline float scale_byte(uint32_t word, int b) {
 // significand, the next 8 and the last, each cut off (the rest of an infinity is NaN).  One is
 // rounded to nearest.
 template <int PARTS>
-__device__ inline void split8(const float (&x)[2][4], bf16x8 (&p)[PARTS]) {
+__device__ __forceinline__ void split8(const float (&x)[2][4], bf16x8 (&p)[PARTS]) {
   if constexpr (PARTS == 1) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[0][i] = (__bf16)x[i / 4][i % 4];
@@ -299,12 +299,12 @@ __device__ inline void split8(const float (&x)[2][4], bf16x8 (&p)[PARTS]) {
 
 // 16 channels of a query row in two E4M3 planes, x = 2^(e - 127) (hi + 2^-5 lo), where e puts the
 // largest magnitude of the block (bits `most`) at 128 .. 256.
-__device__ inline int plane_exponent(uint32_t most) {
+__device__ __forceinline__ int plane_exponent(uint32_t most) {
   const int e = (int)(most >> 23) - 7;
   return e < 16 ? 16 : e;
 }
 template <int AT>
-__device__ inline void e4m3_planes(const float (&x)[16], int e, v8i32& hi, v8i32& lo) {
+__device__ __forceinline__ void e4m3_planes(const float (&x)[16], int e, v8i32& hi, v8i32& lo) {
   const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -324,7 +324,7 @@ __device__ inline void e4m3_planes(const float (&x)[16], int e, v8i32& hi, v8i32
     lo[AT + i] = l;
   }
 }
-__device__ inline uint32_t most_bits(const float (&x)[16]) {
+__device__ __forceinline__ uint32_t most_bits(const float (&x)[16]) {
   uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {

@@ -662,9 +662,6 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
   p.quantum = p.shared ? 128 : 64;
   // workgroups that the chip holds at once
   int64_t full = (p.chunk_waves ? 2 : resident(f32, C->head_dim, p.nq)) * cus;
-#ifdef FILL
-  if (!p.chunk_waves) full = FILL * cus;
-#endif
   if (p.chunk_waves && C->head_dim < 256 &&
       tiles_of(rows, group, n_seqs, 256) * C->n_heads >= cus) {
     p.chunk_waves = 8;
@@ -672,10 +669,16 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
     full = cus;
   }
   p.tiles = tiles_of(rows, group, n_seqs, p.tile_rows);
-  p.wide = p.shared && tokens <= 2048 && p.tiles * C->n_heads <= cus;
-  p.target = p.tiles * C->n_heads >= full || p.wide || tokens <= p.quantum
-                 ? 0
-                 : (int)((full + C->n_heads - 1) / C->n_heads);
+  // Cutting shortens a workgroup's pass by the chip's idle part of it, and costs the joining launch
+  // (5 us: the time of 1024 tokens for few rows, of 2048 for many, which also have more to join).
+  const int64_t groups = p.tiles * C->n_heads;
+  int64_t span = tokens;  // that a tile's rows see at most
+  if (A->window > 0 && A->window + p.tile_rows / group + 1 < span)
+    span = A->window + p.tile_rows / group + 1;
+  p.wide = p.shared && span <= 2048 && groups <= cus;
+  const bool cut = !p.wide && groups < full &&
+                   span * (full - groups) / full >= (p.chunk_waves ? 2048 : 1024);
+  p.target = cut ? (int)((full + C->n_heads - 1) / C->n_heads) : 0;
   p.items = p.tiles + p.target;
   return p;
 }

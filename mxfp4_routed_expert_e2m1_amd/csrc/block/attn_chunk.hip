@@ -1,41 +1,51 @@
 // attn_chunk.hip -- attention of many rows of a sequence over the 4-bit cache, bf16.
 //
-// A workgroup has 32 rows a wave, in 32 x 32 tiles of the matrix core; the tokens pass 128 at a
-// time.  The pass is attn.hip's, in other operands:
+// A workgroup has 32 rows a wave, in 32 x 32 tiles of the matrix core; the tokens pass 16 a wave
+// at a time, in two buffers with one barrier.  The pass is attn.hip's, in other operands:
 //   scores: the keys' codes and scale bytes go to the scaled instruction as they lie in the cache,
 //     without conversion (32 x 32 x 64: a lane's 32 channels are one block).  The other operand is
 //     q in two E4M3 planes with a scale for 32 channels: q rounded to 4 significant bits, and the
 //     rest, which is exact in 4 more, so the planes hold all 8 bits of a bf16 number (and drop what
-//     lies 2^-22 below the block's largest).  The planes cost what one bf16 product would.
+//     lies 2^-22 below the block's largest).  The planes cost what one bf16 product would.  Codes and
+//     scale bytes are copied to LDS in the order of the operands' lanes, while the stage before is
+//     worked on.
 //   out: a thread turns 4 tokens' codes of D/16 channels into bf16 once for the workgroup, through
-//     LDS, in the order in which the lanes read them as operands.  Two buffers, one barrier per
-//     128 tokens; the reads take half of LDS's rate, where the keys the same way would fill it.
+//     LDS, in the order in which the lanes read them as operands.  The reads take half of LDS's
+//     rate, where the keys the same way would fill it.
 // A row's base of the exponential is raised when its maximum has grown by 2^8 (or is the first):
 // weights of up to 2^8 are as exact as those up to 1, and the accumulators are rarely rescaled.
 #include "attn.h"
 
 namespace moe {
 
-constexpr int kStage = 128;  // tokens between barriers
-
-__device__ inline float max2(float v) {  // over lanes l and l ^ 32
+__device__ __forceinline__ float max2(float v) {  // over lanes l and l ^ 32
   const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
-__device__ inline float sum2(float v) {
+__device__ __forceinline__ float sum2(float v) {
   const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// S += K Q^T for 32 tokens, 32 rows, 64 channels; byte J of `scales` is the lane's block's.
+template <int J>
+__device__ __forceinline__ f32x16 scores_32(v8i32 k, v8i32 q, f32x16 s, uint32_t scales, int e) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, q, s, 4, 0, J, (int)scales, 0, e);
+}
+
 template <int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a) {
-  constexpr int NB = D / 32, NI = (NB + 1) / 2, NC = D / 16, RB = 32 / NC;
-  constexpr int THREADS = 64 * WAVES, PER = kStage * 4 / THREADS;  // quads of a thread per stage
-  constexpr int BUF = kStage * D * 2;
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kernel(const AttnArgs a) {
+  constexpr int NB = D / 32, NI = NB / 2, NC = D / 16, RB = 32 / NC;
+  constexpr int STAGE = 16 * WAVES;  // tokens between barriers: a quad of them for each 16 threads
+  constexpr int BUF = STAGE * D * 2;
+  constexpr int KSCALES = STAGE * NB < 256 ? 256 : STAGE * NB;
   typedef uint32_t VRaw __attribute__((ext_vector_type(NB)));
   constexpr int LD = 33;  // floats of a row in the rows' way out
   constexpr int OUT = WAVES * 32 * LD * 4;
   __shared__ __attribute__((aligned(16))) uint8_t vbuf[2 * BUF > OUT ? 2 * BUF : OUT];
+  // (an array for each of the two stages, so that reads of one wait for no copies into the other)
+  __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[STAGE * D / 2], kbuf1[STAGE * D / 2];
+  __shared__ __attribute__((aligned(1024))) uint8_t kscale0[KSCALES], kscale1[KSCALES];
   __shared__ uint32_t over[2][WAVES];
 
   const int wave = uniform((int)(threadIdx.x >> 6)), lane = lane_id();
@@ -124,87 +134,87 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
   };
   const int last = wg_hi - 1;
 
-  // ---- values: global memory -> registers -> LDS
-  VRaw vr[PER];
-  uint32_t vs[PER];
-  const auto v_load = [&](int t0) {
+  // ---- global memory: values to registers, keys and their scale bytes to LDS.  A thread's token of
+  // each kind; its page is looked up a stage ahead.
+  const int v_run = threadIdx.x & 15, v_tok = 4 * (threadIdx.x >> 4);
+  constexpr int FRAGS = STAGE / 32 * NI, PER = (FRAGS + WAVES - 1) / WAVES;  // of keys: [32 tokens][NI]
+  constexpr int SDWORDS = STAGE * NB / 4, SCOPIES = (SDWORDS + 63) / 64;
+  const int s_dword = (64 * wave + lane) % SDWORDS, s_tok = 4 * s_dword / NB & ~(NB == 2 ? 1 : 0);
+  const auto clamped = [&](int t) { return t < last ? t : last; };
+  const auto page_at = [&](int t) { return pages[clamped(t) >> a.page_log]; };
+  int v_page, s_page, k_page[PER];
+  const auto load_pages = [&](int t0) {
+    v_page = page_at(t0 + v_tok);
+    s_page = page_at(t0 + s_tok);
+#pragma unroll
+    for (int p = 0; p < PER; ++p) k_page[p] = page_at(t0 + (wave + p * WAVES) / NI * 32 + q32);
+  };
+  VRaw vr;
+  uint32_t vs;
+  bool v_bad;
+  const auto load = [&](int t0, uint8_t* kb, uint8_t* sb) __attribute__((always_inline)) {
+    bool bad;
+    {
+      const uint8_t* at = piece_of(v_page, v_bad);
+      const int quad = (clamped(t0 + v_tok) & in_page) >> 2;
+      __builtin_memcpy(&vr, at + unit.v_codes() + (quad * 16 + v_run) * 4 * NB, 4 * NB);
+      __builtin_memcpy(&vs, at + unit.v_scales() + (quad * NB + v_run * NB / 16) * 4, 4);
+    }
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      const int id = threadIdx.x + p * THREADS, run = id & 15;
-      int t = t0 + 4 * (id >> 4);
-      t = t < last ? t : last;
-      bool bad;
-      const uint8_t* at = piece_of(pages[t >> a.page_log], bad);
-      const int quad = (t & in_page) >> 2;
-      __builtin_memcpy(&vr[p], at + unit.v_codes() + (quad * 16 + run) * 4 * NB, 4 * NB);
-      __builtin_memcpy(&vs[p], at + unit.v_scales() + (quad * NB + run * NB / 16) * 4, 4);
+      const int f = wave + p * WAVES;
+      if (FRAGS % WAVES == 0 || f < FRAGS) {
+        const uint8_t* at = piece_of(k_page[p], bad);
+        const int in = clamped(t0 + f / NI * 32 + q32) & in_page;
+        load_to_lds(at + in * (D / 2) + 32 * (f % NI) + 16 * h, kb + f * 1024, 16);
+      }
     }
+    if (wave < SCOPIES) {
+      const uint8_t* at = piece_of(s_page, bad);
+      const int in = clamped(t0 + s_tok) & in_page & ~(NB == 2 ? 1 : 0);
+      load_to_lds(at + unit.k_scales() + in * NB + (NB == 8 ? 4 * (s_dword & 1) : 0), sb + 256 * wave, 4);
+    }
+    load_pages(t0 + STAGE);
   };
   // Unit of 16 bytes: 8 tokens of a channel, [block][16 tokens][half of the lanes][32 channels].
   // Channel j of run o of its block is at place RB j + o, xor a number of the block and half, so
   // that a wave's 8-byte stores of one j spread over the banks.
-  const auto v_store = [&](int buf) {
-    uint32_t flagged = 0;
+  const auto v_store = [&](int buf) __attribute__((always_inline)) {
+    const int quad = threadIdx.x >> 4, blk = v_run * NB / 16, o = v_run % RB;
+    const int s = quad >> 2, hh = quad & 1, half = (quad >> 1) & 1;
+    const uint32_t ov = over_bytes(vs);
+    uint32_t sc = vs;
+    if (ov) {  // NaN (or, behind the last token, anything): 0 here
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const int id = threadIdx.x + p * THREADS, run = id & 15, quad = id >> 4;
-      const int blk = run * NB / 16, o = run % RB;
-      const int s = quad >> 2, hh = quad & 1, half = (quad >> 1) & 1;
-      const uint32_t ov = over_bytes(vs[p]);
-      flagged |= ov;
-      uint32_t sc = vs[p];
-      if (ov) {  // NaN (or, behind the last token, anything): 0 here
+      for (int b = 0; b < 4; ++b)
+        if (((sc >> (8 * b)) & 0xFF) > kMaxScaleByte) sc &= ~(0xFFu << (8 * b));
+    }
+    uint8_t* dst = vbuf + buf * BUF + ((blk * (STAGE / 16) + s) * 2 + hh) * 512 + half * 8;
+    const int swz = RB * ((2 * blk + hh) & (NC - 1));
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (((sc >> (8 * b)) & 0xFF) > kMaxScaleByte) sc &= ~(0xFFu << (8 * b));
-      }
-      uint8_t* dst = vbuf + buf * BUF + ((blk * (kStage / 16) + s) * 2 + hh) * 512 + half * 8;
-      const int swz = RB * ((2 * blk + hh) & (NC - 1));
+    for (int b = 0; b < NB; ++b) {
+      uint32_t x[4];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int byte = e * NB + b;
-          const uint32_t w = vr[p][byte / 4];
-          const float k = scale_byte(sc, e);
-          bf16x2 y;
-          switch (byte & 3) {
-            case 0: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 0); break;
-            case 1: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 1); break;
-            case 2: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 2); break;
-            default: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 3); break;
-          }
-          x[e] = __builtin_bit_cast(uint32_t, y);
+      for (int e = 0; e < 4; ++e) {
+        const int byte = e * NB + b;
+        const uint32_t w = vr[byte / 4];
+        const float k = scale_byte(sc, e);
+        bf16x2 y;
+        switch (byte & 3) {
+          case 0: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 0); break;
+          case 1: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 1); break;
+          case 2: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 2); break;
+          default: y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, k, 3); break;
         }
-        *(u32x2*)(dst + (((RB * 2 * b + o) ^ swz) * 16)) =
-            u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x05040100), __builtin_amdgcn_perm(x[3], x[2], 0x05040100)};
-        *(u32x2*)(dst + (((RB * (2 * b + 1) + o) ^ swz) * 16)) =
-            u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x07060302), __builtin_amdgcn_perm(x[3], x[2], 0x07060302)};
+        x[e] = __builtin_bit_cast(uint32_t, y);
       }
+      *(u32x2*)(dst + (((RB * 2 * b + o) ^ swz) * 16)) =
+          u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x05040100), __builtin_amdgcn_perm(x[3], x[2], 0x05040100)};
+      *(u32x2*)(dst + (((RB * (2 * b + 1) + o) ^ swz) * 16)) =
+          u32x2{__builtin_amdgcn_perm(x[1], x[0], 0x07060302), __builtin_amdgcn_perm(x[3], x[2], 0x07060302)};
     }
-    const bool f2 = __ballot(flagged != 0) != 0;
+    const bool f2 = __ballot(ov != 0 || v_bad) != 0;
     if (lane == 0) over[buf][wave] = f2;
-  };
-
-  // ---- keys: 64 tokens, in registers as they are
-  u32x4 kr[2][NI];
-  uint32_t ks[2][NI];
-  const auto k_load = [&](int t0) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      int t = t0 + 32 * u + q32;
-      t = t < last ? t : last;
-      bool bad;
-      const uint8_t* at = piece_of(pages[t >> a.page_log], bad);
-      const int in = t & in_page;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        __builtin_memcpy(&kr[u][i], at + in * (D / 2) + 16 * (2 * i + h), 16);
-        const uint32_t b = at[unit.k_scales() + in * NB + 2 * i + h];
-        ks[u][i] = bad || b > kMaxScaleByte ? 255u : b;
-      }
-    }
   };
 
   float m = -__builtin_inff(), l = 0.f;
@@ -217,33 +227,62 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
   const float cap_k = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
   const float unit_scale = plain ? qk_scale : 1.f;
 
-  if (wg_lo < wg_hi) {
-    v_load(wg_lo);
-    v_store(0);
-    lds_barrier();
-  }
-  int buf = 0;
-  for (int t0 = wg_lo; t0 < wg_hi; t0 += kStage, buf ^= 1) {
-    const bool more = t0 + kStage < wg_hi;
-    if (more) v_load(t0 + kStage);
+  const auto arrived = [] {  // every load and copy that this wave has started
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+    asm volatile("" ::: "memory");
+  };
+
+  // One stage: the next one's loads, this one's tokens in 64s, then the next one's values to LDS.
+  const auto pass = [&](int t0, int buf, const uint8_t* kb, const uint8_t* sb, uint8_t* next_kb,
+                        uint8_t* next_sb) __attribute__((always_inline)) {
+    const bool more = t0 + STAGE < wg_hi;
+    if (more) load(t0 + STAGE, next_kb, next_sb);
     uint32_t nan_here = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) nan_here |= over[buf][w];
+    nan_here = uniform((int)nan_here);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < STAGE / 64; ++half) {
       const int t = t0 + 64 * half;
       if (t >= hi || t + 64 <= lo || t >= wg_hi) continue;
-      k_load(t);
       // ---- scores
       f32x16 s[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         s[u] = f32x16{};
+        const int tok32 = 2 * half + u;
+        uint32_t sw[2] = {};  // the token's scale bytes, its lane's blocks 2 i + h from byte 0
+        if constexpr (NB == 2) {
+          sw[0] = *(const uint16_t*)(sb + (32 * tok32 + q32) * 2) >> (8 * h);
+        } else if constexpr (NB == 4) {
+          sw[0] = *(const uint32_t*)(sb + (32 * tok32 + q32) * 4) >> (8 * h);
+        } else {
+          const u32x2 w = *(const u32x2*)(sb + (32 * tok32 + q32) * 8);
+          sw[0] = w[0] >> (8 * h);
+          sw[1] = w[1] >> (8 * h);
+        }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const v8i32 k = {(int)kr[u][i][0], (int)kr[u][i][1], (int)kr[u][i][2], (int)kr[u][i][3], 0, 0, 0, 0};
-          s[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, qh[i], s[u], 4, 0, 0, (int)ks[u][i], 0, e0[i]);
-          s[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, ql[i], s[u], 4, 0, 0, (int)ks[u][i], 0, e1[i]);
+          const u32x4 kr = *(const u32x4*)(kb + (tok32 * NI + i) * 1024 + lane * 16);
+          const v8i32 k = {(int)kr[0], (int)kr[1], (int)kr[2], (int)kr[3], 0, 0, 0, 0};
+          if (i & 1) {
+            s[u] = scores_32<2>(k, qh[i], s[u], sw[i / 2], e0[i]);
+            s[u] = scores_32<2>(k, ql[i], s[u], sw[i / 2], e1[i]);
+          } else {
+            s[u] = scores_32<0>(k, qh[i], s[u], sw[i / 2], e0[i]);
+            s[u] = scores_32<0>(k, ql[i], s[u], sw[i / 2], e1[i]);
+          }
+        }
+      }
+      if (nan_here) {  // (among what that stands for: pages that are none)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int page = page_at(t + 32 * u + q32);
+          const uint32_t none = (uint32_t)__ballot(page < 0 || page >= a.n_pages) >> (4 * h);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (none >> (8 * (e >> 2) + (e & 3)) & 1) s[u][e] = __builtin_nanf("");
         }
       }
       if (!plain) {
@@ -306,9 +345,9 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
             for (int e = 0; e < 8; ++e) {
               int j = t + 16 * c + 8 * (e >> 2) + 4 * h + (e & 3);
               seen[e] = (__bf16)(j >= see.lo && j < see.hi ? 1.f : 0.f);
-              j = j < last ? j : last;
+              j = clamped(j);
               bool bad;
-              const uint8_t* at = piece_of(pages[j >> a.page_log], bad);
+              const uint8_t* at = piece_of(page_at(j), bad);
               const int quad = (j & in_page) >> 2;
               const uint32_t u = at[unit.v_scales() + (quad * NB + b) * 4 + (j & 3)];
               nan[e] = (__bf16)(u > kMaxScaleByte ? 1.f : 0.f);
@@ -326,12 +365,27 @@ __global__ __launch_bounds__(64 * WAVES) void attn_chunk_kernel(const AttnArgs a
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const int swz = RB * ((2 * b + h) & (NC - 1));
-          const bf16x8 v = *(const bf16x8*)(vbuf + buf * BUF + ((b * (kStage / 16) + 4 * half + c) * 2 + h) * 512 + (q32 ^ swz) * 16);
+          const bf16x8 v = *(const bf16x8*)(vbuf + buf * BUF + ((b * (STAGE / 16) + 4 * half + c) * 2 + h) * 512 +
+                                               (q32 ^ swz) * 16);
           acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[c], acc[b], 0, 0, 0);
         }
     }
-    if (more) v_store(buf ^ 1);
+    if (more) {
+      arrived();
+      v_store(buf ^ 1);
+    }
     lds_barrier();
+  };
+  if (wg_lo < wg_hi) {
+    load_pages(wg_lo);
+    load(wg_lo, kbuf0, kscale0);
+    arrived();
+    v_store(0);
+    lds_barrier();
+  }
+  for (int t0 = wg_lo; t0 < wg_hi; t0 += 2 * STAGE) {
+    pass(t0, 0, kbuf0, kscale0, kbuf1, kscale1);
+    if (t0 + STAGE < wg_hi) pass(t0 + STAGE, 1, kbuf1, kscale1, kbuf0, kscale0);
   }
   l = sum2(l);
 
