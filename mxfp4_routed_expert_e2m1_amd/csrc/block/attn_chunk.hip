@@ -218,6 +218,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
   };
 
   float m = -__builtin_inff(), l = 0.f;
+  uint32_t nan_blocks = 0;  // blocks of channels in which this row has seen a NaN
   f32x16 acc[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) acc[b] = f32x16{};
@@ -246,43 +247,68 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
     for (int half = 0; half < STAGE / 64; ++half) {
       const int t = t0 + 64 * half;
       if (t >= hi || t + 64 <= lo || t >= wg_hi) continue;
-      // ---- scores
+      // ---- scores: all operands on their way before the first product
       f32x16 s[2];
+      u32x4 kr[2][NI];
+      uint32_t sw[2][2];  // the token's scale bytes, its lane's blocks 2 i + h from byte 0
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        s[u] = f32x16{};
         const int tok32 = 2 * half + u;
-        uint32_t sw[2] = {};  // the token's scale bytes, its lane's blocks 2 i + h from byte 0
+        sw[u][1] = 0;
         if constexpr (NB == 2) {
-          sw[0] = *(const uint16_t*)(sb + (32 * tok32 + q32) * 2) >> (8 * h);
+          sw[u][0] = *(const uint16_t*)(sb + (32 * tok32 + q32) * 2) >> (8 * h);
         } else if constexpr (NB == 4) {
-          sw[0] = *(const uint32_t*)(sb + (32 * tok32 + q32) * 4) >> (8 * h);
+          sw[u][0] = *(const uint32_t*)(sb + (32 * tok32 + q32) * 4) >> (8 * h);
         } else {
           const u32x2 w = *(const u32x2*)(sb + (32 * tok32 + q32) * 8);
-          sw[0] = w[0] >> (8 * h);
-          sw[1] = w[1] >> (8 * h);
+          sw[u][0] = w[0] >> (8 * h);
+          sw[u][1] = w[1] >> (8 * h);
         }
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const u32x4 kr = *(const u32x4*)(kb + (tok32 * NI + i) * 1024 + lane * 16);
-          const v8i32 k = {(int)kr[0], (int)kr[1], (int)kr[2], (int)kr[3], 0, 0, 0, 0};
-          if (i & 1) {
-            s[u] = scores_32<2>(k, qh[i], s[u], sw[i / 2], e0[i]);
-            s[u] = scores_32<2>(k, ql[i], s[u], sw[i / 2], e1[i]);
-          } else {
-            s[u] = scores_32<0>(k, qh[i], s[u], sw[i / 2], e0[i]);
-            s[u] = scores_32<0>(k, ql[i], s[u], sw[i / 2], e1[i]);
-          }
+        for (int i = 0; i < NI; ++i) kr[u][i] = *(const u32x4*)(kb + (tok32 * NI + i) * 1024 + lane * 16);
+        s[u] = f32x16{};
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        v8i32 k[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          k[u] = v8i32{(int)kr[u][i][0], (int)kr[u][i][1], (int)kr[u][i][2], (int)kr[u][i][3], 0, 0, 0, 0};
+        if (i & 1) {
+          s[0] = scores_32<2>(k[0], qh[i], s[0], sw[0][i / 2], e0[i]);
+          s[1] = scores_32<2>(k[1], qh[i], s[1], sw[1][i / 2], e0[i]);
+          s[0] = scores_32<2>(k[0], ql[i], s[0], sw[0][i / 2], e1[i]);
+          s[1] = scores_32<2>(k[1], ql[i], s[1], sw[1][i / 2], e1[i]);
+        } else {
+          s[0] = scores_32<0>(k[0], qh[i], s[0], sw[0][i / 2], e0[i]);
+          s[1] = scores_32<0>(k[1], qh[i], s[1], sw[1][i / 2], e0[i]);
+          s[0] = scores_32<0>(k[0], ql[i], s[0], sw[0][i / 2], e1[i]);
+          s[1] = scores_32<0>(k[1], ql[i], s[1], sw[1][i / 2], e1[i]);
         }
       }
-      if (nan_here) {  // (among what that stands for: pages that are none)
+      // Values that are NaN (0 in LDS): noted for the rows that see them, a token a lane.  Pages that
+      // are none: their scores are NaN.
+      if (nan_here) {
+        bool bad;
+        const int j = clamped(t + lane);
+        const uint8_t* at = piece_of(page_at(j), bad);
+        const int in = j & in_page;
+        const uint64_t none = __ballot(bad);
+        const int lo_bit = see.lo > t ? see.lo - t : 0, hi_bit = see.hi - t;
+        uint64_t sees_here = hi_bit >= 64 ? ~(uint64_t)0 : hi_bit > 0 ? ((uint64_t)1 << hi_bit) - 1 : 0;
+        sees_here = lo_bit < 64 ? sees_here >> lo_bit << lo_bit : 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t u = at[unit.v_scales() + ((in >> 2) * NB + b) * 4 + (in & 3)];
+          if (__ballot(u > kMaxScaleByte) & sees_here) nan_blocks |= 1u << b;
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int page = page_at(t + 32 * u + q32);
-          const uint32_t none = (uint32_t)__ballot(page < 0 || page >= a.n_pages) >> (4 * h);
+          const uint32_t here = (uint32_t)(none >> (32 * u)) >> (4 * h);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (none >> (8 * (e >> 2) + (e & 3)) & 1) s[u][e] = __builtin_nanf("");
+            if (here >> (8 * (e >> 2) + (e & 3)) & 1) s[u][e] = __builtin_nanf("");
         }
       }
       if (!plain) {
@@ -306,6 +332,16 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
             s[u][e] = j >= see.lo && j < see.hi ? s[u][e] : -__builtin_inff();
           }
       }
+      // (the first values are on their way while the weights are made, the next ones while they are used)
+      bf16x8 v[2][NB];
+      const auto v_read = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int swz = RB * ((2 * b + h) & (NC - 1));
+          v[c & 1][b] = *(const bf16x8*)(vbuf + buf * BUF + ((b * (STAGE / 16) + 4 * half + c) * 2 + h) * 512 +
+                                         (q32 ^ swz) * 16);
+        }
+      };
       // ---- softmax
       float top = -__builtin_inff();
 #pragma unroll
@@ -325,6 +361,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
         m = next;
       }
       const float base = m == -__builtin_inff() ? 0.f : m;
+      v_read(0);
+      __builtin_amdgcn_sched_barrier(0);
       bf16x8 p[4];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -334,41 +372,15 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
           l += w;
           p[2 * u + (e >> 3)][e & 7] = (__bf16)w;
         }
-      // ---- values that are NaN: in the channels of the rows that see them
-      if (nan_here) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            bf16x8 nan, seen;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              int j = t + 16 * c + 8 * (e >> 2) + 4 * h + (e & 3);
-              seen[e] = (__bf16)(j >= see.lo && j < see.hi ? 1.f : 0.f);
-              j = clamped(j);
-              bool bad;
-              const uint8_t* at = piece_of(page_at(j), bad);
-              const int quad = (j & in_page) >> 2;
-              const uint32_t u = at[unit.v_scales() + (quad * NB + b) * 4 + (j & 3)];
-              nan[e] = (__bf16)(u > kMaxScaleByte ? 1.f : 0.f);
-            }
-            f32x16 n = {};
-            n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(nan, seen, n, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (n[e] > 0.f) acc[b][e] = __builtin_nanf("");
-          }
-      }
       // ---- out
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c) {
+        if (c < 3) v_read(c + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int swz = RB * ((2 * b + h) & (NC - 1));
-          const bf16x8 v = *(const bf16x8*)(vbuf + buf * BUF + ((b * (STAGE / 16) + 4 * half + c) * 2 + h) * 512 +
-                                               (q32 ^ swz) * 16);
-          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[c], acc[b], 0, 0, 0);
-        }
+        for (int b = 0; b < NB; ++b)
+          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[c & 1][b], p[c], acc[b], 0, 0, 0);
+      }
     }
     if (more) {
       arrived();
@@ -388,6 +400,12 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
     if (t0 + STAGE < wg_hi) pass(t0 + STAGE, 1, kbuf1, kscale1, kbuf0, kscale0);
   }
   l = sum2(l);
+  if (__ballot(nan_blocks != 0)) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[b][e] = nan_blocks >> b & 1 ? __builtin_nanf("") : acc[b][e];
+  }
 
   if (a.target && piece == 0 && kvh == 0 && h == 0 && real && head == 0) put_record(a, f, tok, see);
 
