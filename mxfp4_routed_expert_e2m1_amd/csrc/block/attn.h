@@ -230,6 +230,32 @@ __device__ __forceinline__ void put_record(const AttnArgs& a, const Found& f, in
   ((RowRecord*)(a.part + a.rec_at))[f.seq.row0 + token] = r;
 }
 
+// find_item for a workgroup: by its first wave, for the others through LDS (the cut's arithmetic takes
+// as long as half a step of a pass, and waves that share a SIMD would take turns at it).
+struct FoundShared {
+  int have, cut;
+  Found f;
+};
+__device__ __forceinline__ bool find_item(const AttnArgs& a, int item, Found& f, int& cut, int wave,
+                                          FoundShared& s) {
+  if (!a.target && !a.q_offsets) return find_item(a, item, f, cut);
+  if (wave == 0) {
+    const bool have = find_item(a, item, f, cut);
+    if (lane_id() == 0) s = {have, cut, f};
+  }
+  lds_barrier();
+  f = s.f;
+  cut = uniform(s.cut);
+  f.at = uniform(f.at);
+  f.pieces = uniform(f.pieces);
+  f.first_item = uniform(f.first_item);
+  f.seq.row0 = uniform(f.seq.row0);
+  f.seq.m = uniform(f.seq.m);
+  f.seq.n = uniform(f.seq.n);
+  f.seq.prefix = uniform(f.seq.prefix);
+  return uniform(s.have) != 0;
+}
+
 __device__ __forceinline__ float max16(float v) {  // over the lanes l % 16
   const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
@@ -323,6 +349,20 @@ __device__ __forceinline__ void e4m3_planes(const float (&x)[16], int e, v8i32& 
     hi[AT + i] = h;
     lo[AT + i] = l;
   }
+}
+// Largest over blocks of 8, 16 or 32 neighbouring lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+  const auto step = [&](int o) { v = (uint32_t)o > v ? (uint32_t)o : v; };
+  step(__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
+  step(__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
+  step(__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
+  if constexpr (LANES >= 16) step(__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));  // row_mirror
+  if constexpr (LANES == 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = s[0] > s[1] ? s[0] : s[1];
+  }
+  return v;
 }
 __device__ __forceinline__ uint32_t most_bits(const float (&x)[16]) {
   uint32_t most = 0;

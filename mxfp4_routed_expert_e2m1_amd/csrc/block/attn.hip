@@ -57,7 +57,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
 
   int cut;
   Found f;
-  if (!find_item(a, item, f, cut)) return;
+  __shared__ FoundShared found;
+  if (!find_item(a, item, f, cut, wave, found)) return;
   const Seq& sq = f.seq;
   const int local = item - f.first_item;
   // the last rows first: they see the most tokens
@@ -72,9 +73,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   bool real[NQ];
   Sight see[NQ];
   float slope[NQ];
-  // q on its way: channel runs of 8, [i][n]; bf16 calls have 16 g .. and 64 + 16 g .. of 128
-  // channels in a lane, f32 calls its blocks 4 i + g
-  Raw8<T> qraw[NQ][NI][4];
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) {
     real[nq] = trow0 + 16 * nq + r16 < rows_here;
@@ -84,15 +82,39 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
     see[nq] = sight_of(a, sq, tok[nq]);
     if (!real[nq]) see[nq] = {0, 0};
     slope[nq] = a.slopes && real[nq] ? a.slopes[head[nq]] * kLog2e : 0.f;
-    const T* qp = (const T*)a.q + (int64_t)(sq.row0 + tok[nq]) * a.ld_q + head[nq] * a.hs_q;
+  }
+  // q on its way: f32 calls 8 channels of each of a lane's blocks 4 i + g; bf16 calls D/64 channels of
+  // the rows that a wave prepares for the workgroup
+  constexpr int QROWS = 16 * NQ / WAVES, QCH = D / 64;
+  Raw8<float> qraw[NQ][NI][4];
+  __bf16 qmine[QROWS][QCH];
+  if constexpr (F32) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int nq = 0; nq < NQ; ++nq) {
+      const T* qp = (const T*)a.q + (int64_t)(sq.row0 + tok[nq]) * a.ld_q + head[nq] * a.hs_q;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int c = F32 ? 32 * (4 * i + g) + 8 * n : 128 * i + 64 * (n >> 1) + 16 * g + 8 * (n & 1);
-        qraw[nq][i][n] = Raw8<T>{};
-        if (real[nq] && c < D) qraw[nq][i][n] = load8(qp + c);
-      }
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int c = 32 * (4 * i + g) + 8 * n;
+          qraw[nq][i][n] = Raw8<float>{};
+          if (real[nq] && c < D) qraw[nq][i][n] = load8((const float*)qp + c);
+        }
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < QROWS; ++n) {
+      const int row = wave * QROWS + n;
+      int qt, qhd;
+      rs.at(a, row, qt, qhd);
+#pragma unroll
+      for (int c = 0; c < QCH; ++c) qmine[n][c] = (__bf16)0.f;
+      if (trow0 + row < rows_here)
+        __builtin_memcpy(qmine[n],
+                         (const __bf16*)a.q + (int64_t)(sq.row0 + qt) * a.ld_q +
+                             (int64_t)(kvh * a.group + qhd) * a.hs_q + QCH * lane,
+                         sizeof(qmine[n]));
+    }
   }
 
   // the tile's tokens: what its first row (window) and its last (causal) see, and all of them
@@ -117,7 +139,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   }
 
   const KvUnit<D> unit{1 << a.page_log};
-  const int32_t* pages = a.table + f.at * a.ld_table;
+  // (scalar loads: as vector loads their arrival would be that of every copy before them)
+  const auto* pages = (const __attribute__((address_space(4))) int32_t*)(a.table + f.at * a.ld_table);
   const bool plain = a.softcap == 0.f && !a.slopes && a.scale > 0.f;
   const float qk_scale = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
   const float cap_k = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
@@ -136,7 +159,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   uint32_t bad = 0;   // two bits a step, the latest lowest: whether its pages are none
   const auto load_pages = [&](int step) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) pg[u] = uniform(pages[sub_of(step, u) >> a.page_log]);
+    for (int u = 0; u < 2; ++u) pg[u] = pages[uniform(sub_of(step, u) >> a.page_log)];
   };
   const auto copy = [&](uint8_t* to, int step) {
     const uint8_t* at[2];
@@ -182,7 +205,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   if (n_steps) {
     load_pages(0);
 #pragma unroll
-    for (int i = 0; i < RING - 1; ++i) copy(ring[i], i);
+    for (int i = 0; i < RING - 1; ++i) {
+      if (i == 0 || i < n_steps) copy(ring[i], i);
+      else bad <<= 2;
+    }
   }
 
   // q as the matrix core takes it: bf16 calls in two E4M3 planes (128 channels an instruction), f32
@@ -190,56 +216,96 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   v8i32 qh[NQ][NI], ql[NQ][NI];
   int e0[NQ][NI], e1[NQ][NI];
   bf16x8 q[NQ][NI][4][PARTS];
+  if constexpr (F32) {
 #pragma unroll
-  for (int nq = 0; nq < NQ; ++nq)
+    for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if constexpr (F32) {
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           float v[8], x[2][4];
-          to_f32<T>(qraw[nq][i][n], v);
+          to_f32<float>(qraw[nq][i][n], v);
 #pragma unroll
           for (int e = 0; e < 8; ++e)  // (a row with an infinity has no finite score)
             x[e / 4][e % 4] = fabsf(v[e]) < __builtin_inff() ? v[e] : __builtin_nanf("");
           split8<PARTS>(x, q[nq][i][n]);
         }
-      } else {
-        int e[2];
+  } else {
+    // Each wave's rows into the last stage's memory, which has no copies yet: planes [row][D], scale
+    // bytes [row][NB].  An 8-bit operand's lane has channels 16 g .. and 64 + 16 g .. of 128, and the
+    // scale of block 4 i + g.
+    uint8_t* const qs = ring[RING - 1];
+    constexpr int ROWS = 16 * NQ;
+    static_assert(ROWS * (2 * D + NB) <= WAVES * STAGE);
+#pragma unroll
+    for (int n = 0; n < QROWS; ++n) {
+      const int row = wave * QROWS + n;
+      uint32_t most = 0;
+      float x[QCH];
+#pragma unroll
+      for (int c = 0; c < QCH; ++c) {
+        x[c] = (float)qmine[n][c];
+        const uint32_t b = __float_as_uint(x[c]) & 0x7FFFFFFFu;
+        most = b > most ? b : most;
+      }
+      most = block_max<32 / QCH>(most);
+      const int e = plane_exponent(most);
+      const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+      uint8_t hi8[QCH], lo8[QCH];
+#pragma unroll
+      for (int c = 0; c < QCH; ++c) {
+        const float r = x[c] * down;
+        const int hi = __builtin_amdgcn_cvt_pk_fp8_f32(r, r, 0, false);
+        const float rest = (r - __builtin_amdgcn_cvt_f32_fp8(hi, 0)) * 32.f;
+        hi8[c] = (uint8_t)hi;
+        lo8[c] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(rest, rest, 0, false);
+      }
+      __builtin_memcpy(qs + row * D + QCH * lane, hi8, QCH);
+      __builtin_memcpy(qs + (ROWS + row) * D + QCH * lane, lo8, QCH);
+      if (lane % (32 / QCH) == 0)  // (infinite or NaN: so are all of its products)
+        qs[2 * ROWS * D + row * NB + lane / (32 / QCH)] = (uint8_t)(most >= 0x7F800000u ? 255 : e);
+    }
+    lds_barrier();
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int row = 16 * nq + r16;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float x[16];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v[8];
-            to_f32<T>(qraw[nq][i][2 * b + k], v);
-#pragma unroll
-            for (int n = 0; n < 8; ++n) x[8 * k + n] = v[n];
+          const int c = 128 * i + 64 * b + 16 * g;
+          u32x4 hi = {}, lo = {};
+          if (c < D) {
+            hi = *(const u32x4*)(qs + row * D + c);
+            lo = *(const u32x4*)(qs + (ROWS + row) * D + c);
           }
-          const uint32_t own = most_bits(x);  // (half of block 4 i + 2 b + g / 2)
-          const auto other = __builtin_amdgcn_permlane16_swap(own, own, false, false);
-          const uint32_t most = other[0] > other[1] ? other[0] : other[1];
-          e[b] = plane_exponent(most);
-          if (b == 0) e4m3_planes<0>(x, e[b], qh[nq][i], ql[nq][i]);
-          else e4m3_planes<4>(x, e[b], qh[nq][i], ql[nq][i]);
-          if (most >= 0x7F800000u) e[b] = 255;  // infinite or NaN: so are all of its products
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            qh[nq][i][4 * b + k] = (int)hi[k];
+            ql[nq][i][4 * b + k] = (int)lo[k];
+          }
         }
-        // the scale of block 4 i + g goes with lanes g
-        const int first = __shfl(e[0], r16 + 32 * (g & 1)), second = __shfl(e[1], r16 + 32 * (g & 1));
-        e0[nq][i] = g < 2 ? first : second;
+        const int block = 4 * i + g;
+        e0[nq][i] = block < NB ? qs[2 * ROWS * D + row * NB + block] : 127;
         e1[nq][i] = e0[nq][i] == 255 ? 255 : e0[nq][i] - 5;
       }
-    }
+    lds_barrier();  // (copies into that stage start behind this)
+  }
 
-  // One step: the copies of step + RING - 1 into the stage that was read last, once those reads are
-  // done, then this step's tokens.
+  // One step: the copies of step + RING - 1, if there is one, into the stage that was read last, once
+  // those reads are done, then this step's tokens.
   const auto pass = [&](int step, const uint8_t* stage, uint8_t* to) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0
     asm volatile("" ::: "memory");
-    copy(to, step + RING - 1);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((RING - 1) * COPIES | 0xF70);  // vmcnt
+    if (step + RING - 1 < n_steps) {
+      copy(to, step + RING - 1);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt((RING - 1) * COPIES | 0xF70);  // vmcnt
+    } else {
+      bad <<= 2;
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+    }
     asm volatile("" ::: "memory");
     const int t = t_first + step * STRIDE;
     const uint8_t* mine = stage + wave * STAGE;
@@ -430,7 +496,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
       pass(step + i, ring[i], ring[(i + RING - 1) % RING]);
     }
   }
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0: no copy is on its way into the stages
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) l[nq] = sum16(l[nq]);
 
@@ -444,72 +509,76 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   const int64_t slot0 =
       (((int64_t)item * a.kv_heads + kvh) << a.tile_log) + (SHARED ? 0 : wave * 16 * NQ);
   if constexpr (SHARED) {
-    // (through the first stage's memory, half of a run's channels at a time)
+    // Through the first two stages' memory, half of a run's channels in each; rows that are none stay
+    // out of it.  The waves bring their parts to the largest base first.
     constexpr int HC = NC / 2, LD = D / 2 + 4, LANES = 4 * WAVES, PER = D / 2 / LANES;
     static_assert(16 * LD * 4 <= STAGE && PER >= 1 && HC % PER == 0);
-    __shared__ float ml[NQ][WAVES][16][2];
-    float(*joined)[LD] = (float(*)[LD])(ring0 + wave * STAGE);
+    __shared__ float bases[NQ][WAVES][16], sums[NQ][WAVES][16];
     const int row = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * PER;  // of D/2
     if (g == 0) {
 #pragma unroll
-      for (int nq = 0; nq < NQ; ++nq) {
-        ml[nq][wave][r16][0] = m[nq];
-        ml[nq][wave][r16][1] = l[nq];
-      }
+      for (int nq = 0; nq < NQ; ++nq) bases[nq][wave][r16] = m[nq];
     }
+    lds_barrier();
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, bases[nq][w][r16]);
+      // (a wave without weights has nothing to add, and its base is no number to take an exponential
+      // with)
+      const float k = l[nq] == 0.f ? 0.f : exp2_fast(m[nq] - (top == -__builtin_inff() ? 0.f : top));
+      if (g == 0) sums[nq][wave][r16] = l[nq] * k;
+      if (nq) lds_barrier();
+      if (real[nq]) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float* to = (float*)((half ? ring1 : ring0) + wave * STAGE) + r16 * LD;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < HC; j += 2)
+              *(f32x2*)(to + HC * (4 * g + e) + j) =
+                  f32x2{acc[nq][half * HC + j][e] * k, acc[nq][half * HC + j + 1][e] * k};
+        }
+      }
+      lds_barrier();
       const int r = trow0 + 16 * nq + row;
+      if (r >= rows_here) continue;
       int token, hd;
       rs.at(a, 16 * nq + row, token, hd);
       hd += kvh * a.group;
-      float top = -__builtin_inff(), sum = 0.f, k[WAVES];
+      float sum = 0.f, o[2][PER] = {};
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        sum += sums[nq][w][row];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float* from = (const float*)((half ? ring1 : ring0) + w * STAGE) + row * LD + ch;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) o[half][j] += from[j];
+        }
+      }
+      const Sight sg = sight_of(a, sq, token);
+      const bool sees = sg.lo < sg.hi;
+      const float inv = 1.f / sum;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int j = 0; j < HC; j += 2)
-            *(f32x2*)&joined[r16][HC * (4 * g + e) + j] =
-                f32x2{acc[nq][half * HC + j][e], acc[nq][half * HC + j + 1][e]};
-        __syncthreads();
-        if (half == 0) {
-#pragma unroll
-          for (int w = 0; w < WAVES; ++w) top = fmaxf(top, ml[nq][w][row][0]);
-          const float base = top == -__builtin_inff() ? 0.f : top;
-#pragma unroll
-          for (int w = 0; w < WAVES; ++w) {
-            // (a wave without weights has nothing to add, and its base is no number to take an
-            // exponential with)
-            const float lw = ml[nq][w][row][1];
-            k[w] = lw == 0.f ? 0.f : exp2_fast(ml[nq][w][row][0] - base);
-            sum += lw * k[w];
-          }
-        }
-        float o[PER] = {};
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-          const float* from = (const float*)(ring0 + w * STAGE) + row * LD + ch;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) o[j] += from[j] * k[w];
-        }
-        if (r >= rows_here) continue;
         const int c = ch / HC * NC + half * HC + ch % HC;  // channel of the first
         if (f.pieces > 1) {
           const int64_t slot = slot0 + 16 * nq + row;
-          __builtin_memcpy(a.part + slot * D + c, o, sizeof(o));
+          __builtin_memcpy(a.part + slot * D + c, o[half], sizeof(o[half]));
           if (ch == 0 && half == 0) {
-            a.part[a.ml_at + 2 * slot] = top;
+            float up = -__builtin_inff();
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) up = fmaxf(up, bases[nq][w][row]);
+            a.part[a.ml_at + 2 * slot] = up;
             a.part[a.ml_at + 2 * slot + 1] = sum;
           }
         } else {
-          const Sight sg = sight_of(a, sq, token);
-          const bool sees = sg.lo < sg.hi;
-          const float inv = 1.f / sum;
           T res[PER];
 #pragma unroll
-          for (int j = 0; j < PER; ++j) res[j] = (T)(sees ? o[j] * inv : 0.f);
+          for (int j = 0; j < PER; ++j) res[j] = (T)(sees ? o[half][j] * inv : 0.f);
           T* dst = (T*)a.out + (int64_t)(sq.row0 + token) * a.ld_out + hd * a.hs_out + c;
           __builtin_memcpy(dst, res, sizeof(res));
         }

@@ -56,7 +56,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
 
   int cut;
   Found f;
-  if (!find_item(a, item, f, cut)) return;
+  __shared__ FoundShared found;
+  if (!find_item(a, item, f, cut, wave, found)) return;
   const Seq& sq = f.seq;
   const int local = item - f.first_item;
   // the last rows first: they see the most tokens
