@@ -139,6 +139,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   }
 
   const KvUnit<D> unit{1 << a.page_log};
+  const uint32_t page_bytes = (uint32_t)unit.bytes() * a.kv_heads;  // (of all heads: < 2^27)
+  const uint8_t* pieces0 = a.data + (uint32_t)unit.bytes() * (uint32_t)kvh;
   // (scalar loads: as vector loads their arrival would be that of every copy before them)
   const auto* pages = (const __attribute__((address_space(4))) int32_t*)(a.table + f.at * a.ld_table);
   const bool plain = a.softcap == 0.f && !a.slopes && a.scale > 0.f;
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
     for (int u = 0; u < 2; ++u) {
       const bool none = pg[u] < 0 || pg[u] >= a.n_pages;
       bad = bad << 1 | none;
-      at[u] = a.data + ((int64_t)(none ? 0 : pg[u]) * a.kv_heads + kvh) * unit.bytes();
+      at[u] = pieces0 + (uint64_t)(none ? 0u : (uint32_t)pg[u]) * page_bytes;
       in[u] = sub_of(step, u) & ((1 << a.page_log) - 1);
     }
     load_pages(step + 1);

@@ -130,10 +130,12 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
   const KvUnit<D> unit{1 << a.page_log};
   const int32_t* pages = a.table + f.at * a.ld_table;
   const int in_page = (1 << a.page_log) - 1;
+  const uint32_t page_bytes = (uint32_t)unit.bytes() * a.kv_heads;  // (of all heads: < 2^27)
+  const uint8_t* pieces0 = a.data + (uint32_t)unit.bytes() * (uint32_t)kvh;
   // a token's piece of the cache; a page that is none: the first, and `bad`
   const auto piece_of = [&](int page, bool& bad) {
     bad = page < 0 || page >= a.n_pages;
-    return a.data + ((int64_t)(bad ? 0 : page) * a.kv_heads + kvh) * unit.bytes();
+    return pieces0 + (uint64_t)(bad ? 0u : (uint32_t)page) * page_bytes;
   };
   const int last = wg_hi - 1;
 
