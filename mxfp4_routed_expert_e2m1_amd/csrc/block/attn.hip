@@ -45,7 +45,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   constexpr int NB = D / 32, NC = D / 16, NI = (D + 127) / 128, PARTS = F32 ? 3 : 1;
   constexpr int STEP = 32, STRIDE = SHARED ? STEP * WAVES : STEP;
   // a wave's step in LDS: keys' codes, values' codes, scale bytes
-  constexpr int STAGE = 32 * D + 256 * NI, RING = WAVES == 16 || D == 256 ? 2 : 3;
+  constexpr int STAGE = 32 * D + 256 * NI, RING = D == 256 ? 2 : 3;
   typedef uint32_t VRaw __attribute__((ext_vector_type(NB)));
   // (an array for each stage, so that reads of one wait for no copies into the others)
   __shared__ __attribute__((aligned(1024))) uint8_t ring0[WAVES * STAGE], ring1[WAVES * STAGE],
@@ -741,14 +741,18 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
   }
   p.tiles = tiles_of(rows, group, n_seqs, p.tile_rows);
   // Cutting shortens a workgroup's pass by the chip's idle part of it, and costs the joining launch
-  // (5 us: the time of 1024 tokens for few rows, of 2048 for many, which also have more to join).
+  // (5 us: the time of 900 tokens for few rows, of 2048 for many, which also have more to join).
+  // Below, few tiles get workgroups of twice the waves.  One request of 8 key heads of 128 with 4
+  // query heads each, us with 4 waves, 8 waves, cut:
+  //   bf16   512 tokens 8.0, 7.4, 9.8   1000: 11.4, 9.3, 10.0   1500: 14.7, 11.5, 10.0
+  //   f32    512 tokens 8.9, 8.3, 9.7   768: 11.3, 9.9, 9.6     1000: 13.8, 11.7, 9.8
   const int64_t groups = p.tiles * C->n_heads;
   int64_t span = tokens;  // that a tile's rows see at most
   if (A->window > 0 && A->window + p.tile_rows / group + 1 < span)
     span = A->window + p.tile_rows / group + 1;
-  p.wide = p.shared && span <= 2048 && groups <= cus;
+  p.wide = p.shared && span > 256 && span <= (f32 ? 768 : 1024) && groups <= cus;
   const bool cut = !p.wide && groups < full &&
-                   span * (full - groups) / full >= (p.chunk_waves ? 2048 : 1024);
+                   span * (full - groups) / full >= (p.chunk_waves ? 2048 : f32 ? 700 : 900);
   p.target = cut ? (int)((full + C->n_heads - 1) / C->n_heads) : 0;
   p.items = p.tiles + p.target;
   return p;
@@ -769,8 +773,8 @@ static void attn_launch(const AttnArgs& a, const AttnPlan& p, hipStream_t stream
     attn_chunk_launch(a, D, p.chunk_waves, stream);
   } else {
     const dim3 grid = item_grid(p.items, a.kv_heads);
-    // (16 waves have 128 registers each, 8 have 256)
-    constexpr int WIDE = sizeof(T) == 4 || D != 128 ? 8 : 16, WIDE2 = D == 256 ? 4 : 8;
+    // (a tile of 32 rows and 256 channels has no room for 8 waves)
+    constexpr int WIDE = 8, WIDE2 = D == 256 ? 4 : 8;
     if constexpr (sizeof(T) == 4) {
       auto k = !p.shared  ? attn_rows_kernel<T, D, 1, 4, false>
                : p.wide   ? attn_rows_kernel<T, D, 1, WIDE, true>
