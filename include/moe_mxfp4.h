@@ -580,7 +580,8 @@ typedef struct moe_rope {
  *        with more than one axis
  *   out  of x's type (device, out); may be x itself with the same strides
  * Query and key heads that are neighbours in a fused projection take one call.
- * One rounding at the end; rows == 0 or n_heads == 0 is a no-op. */
+ * One rounding at the end.  rows * n_heads < 2^31; rows == 0 or n_heads == 0 is
+ * a no-op. */
 int moe_rope(const moe_rope_t* R, const void* x, int x_type, int64_t ld_x, int64_t hs_x,
              int rows, int n_heads, int head_dim, const int32_t* pos, int64_t ld_pos, void* out,
              int64_t ld_out, int64_t hs_out, void* stream);

@@ -67,11 +67,10 @@ def _load():
 
 def _heads(name, t, gpu, shape=None):
     """(pointer, type, row stride, head stride) of [rows][heads][head_dim] on a GPU, the channels
-    of a head contiguous."""
+    of a head contiguous; `shape` is one that has been checked."""
     kind, sh, st = _TYPES.get(t.dtype), t.shape, t.stride()
     if (kind is None or len(st) != 3 or (st[2] != 1 and sh[2] > 1) or t.get_device() != gpu
-            or gpu < 0 or sh[0] > _MOST or sh[1] > _MOST or sh[2] > _MOST
-            or (shape is not None and sh != shape)):
+            or gpu < 0 or (sh != shape if shape else max(sh) > _MOST)):
         _refuse_heads(name, t, gpu, shape)
     return t.data_ptr(), kind, st[0], st[1]
 
@@ -129,6 +128,9 @@ class Rope:
 
 def _positions(positions, rope, rows, gpu):
     sh, st = positions.shape, positions.stride()
+    if (st == (1,) and sh[0] == rows and rope.n_axes == 1 and positions.dtype == _I32
+            and positions.get_device() == gpu):
+        return positions.data_ptr(), 0
     if positions.dtype != _I32:
         raise TypeError(f"positions: {positions.dtype}, need {_I32}")
     if positions.get_device() != gpu:
@@ -154,12 +156,12 @@ def moe_rope(rope, x, positions, out=None, stream=None):
         with torch.cuda.device(gpu):
             return moe_rope(rope, x, positions, out, stream)
     xp, kind, ld_x, hs_x = _heads("x", x, gpu)
-    rows, heads, dim = x.shape
+    rows, heads, dim = shape = x.shape
     _same_gpu("rope", rope.gpu, gpu)
     pp, ld_pos = _positions(positions, rope, rows, gpu)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    op, out_kind, ld_out, hs_out = _heads("out", out, gpu, x.shape)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    op, out_kind, ld_out, hs_out = _heads("out", out, gpu, shape)
     if out_kind != kind:
         raise TypeError(f"out: {out.dtype}, x is {x.dtype}")
     rc = (_lib or _load()).moe_rope(
@@ -204,14 +206,17 @@ def moe_kv_write(cache, k, v, slots, stream=None):
     if gpu >= 0 and gpu != _current_gpu():
         with torch.cuda.device(gpu):
             return moe_kv_write(cache, k, v, slots, stream)
-    shape = torch.Size((k.shape[0], cache.n_heads, cache.head_dim))
+    rows = k.shape[0]
+    if rows > _MOST:
+        raise ValueError(f"k: {rows} is more than {_MOST} rows")
+    shape = (rows, cache.n_heads, cache.head_dim)
     kp, kind, ld_k, hs_k = _heads("k", k, gpu, shape)
     vp, v_kind, ld_v, hs_v = _heads("v", v, gpu, shape)
     if v_kind != kind:
         raise TypeError(f"v: {v.dtype}, k is {k.dtype}")
     _same_gpu("cache", cache.gpu, gpu)
     rc = (_lib or _load()).moe_kv_write(
-        cache.ref, kp, ld_k, hs_k, vp, ld_v, hs_v, kind, shape[0], _slots(slots, shape[0], gpu),
+        cache.ref, kp, ld_k, hs_k, vp, ld_v, hs_v, kind, rows, _slots(slots, rows, gpu),
         _given(stream, gpu) if stream else _raw_stream(gpu))
     if rc:
         _fail("moe_kv_write", rc)
@@ -228,7 +233,10 @@ def moe_kv_read(cache, slots, k=None, v=None, dtype=torch.bfloat16, stream=None)
     if gpu >= 0 and gpu != _current_gpu():
         with torch.cuda.device(gpu):
             return moe_kv_read(cache, slots, k, v, dtype, stream)
-    shape = torch.Size((slots.numel(), cache.n_heads, cache.head_dim))
+    rows = slots.numel()
+    if rows > _MOST:
+        raise ValueError(f"slots: {rows} is more than {_MOST}")
+    shape = (rows, cache.n_heads, cache.head_dim)
     if k is None:
         k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=slots.device)
     if v is None:
@@ -239,7 +247,7 @@ def moe_kv_read(cache, slots, k=None, v=None, dtype=torch.bfloat16, stream=None)
         raise TypeError(f"v: {v.dtype}, k is {k.dtype}")
     _same_gpu("cache", cache.gpu, gpu)
     rc = (_lib or _load()).moe_kv_read(
-        cache.ref, _slots(slots, shape[0], gpu), shape[0], kp, ld_k, hs_k, vp, ld_v, hs_v, kind,
+        cache.ref, _slots(slots, rows, gpu), rows, kp, ld_k, hs_k, vp, ld_v, hs_v, kind,
         _given(stream, gpu) if stream else _raw_stream(gpu))
     if rc:
         _fail("moe_kv_read", rc)
@@ -300,7 +308,10 @@ def moe_attn_cache(attn, cache, q, table, kv_lens, q_offsets=None, prefix=None, 
         with torch.cuda.device(gpu):
             return moe_attn_cache(attn, cache, q, table, kv_lens, q_offsets, prefix, out, ws,
                                   stream)
-    shape = torch.Size((q.shape[0], attn.n_heads, cache.head_dim))
+    rows = q.shape[0]
+    if rows > _MOST:
+        raise ValueError(f"q: {rows} is more than {_MOST} rows")
+    shape = (rows, attn.n_heads, cache.head_dim)
     qp, kind, ld_q, hs_q = _heads("q", q, gpu, shape)
     _same_gpu("cache", cache.gpu, gpu)
     _same_gpu("attn", attn.gpu, gpu)
@@ -312,10 +323,10 @@ def moe_attn_cache(attn, cache, q, table, kv_lens, q_offsets=None, prefix=None, 
     if out_kind != kind:
         raise TypeError(f"out: {out.dtype}, q is {q.dtype}")
     if ws is None:
-        ws = torch.empty(moe_attn_cache_workspace_bytes(attn, cache, shape[0], n_seqs),
+        ws = torch.empty(moe_attn_cache_workspace_bytes(attn, cache, rows, n_seqs),
                          dtype=torch.uint8, device=q.device)
     rc = (_lib or _load()).moe_attn_cache(
-        attn.ref, cache.ref, qp, kind, ld_q, hs_q, shape[0],
+        attn.ref, cache.ref, qp, kind, ld_q, hs_q, rows,
         _vec("q_offsets", q_offsets, n_seqs + 1, gpu, _I32), n_seqs,
         _vec("kv_lens", kv_lens, n_seqs, gpu, _I32), tp, ld_table, pages,
         _vec("prefix", prefix, n_seqs, gpu, _I32), op, ld_out, hs_out, *_workspace(ws, gpu),

@@ -212,7 +212,7 @@ extern "C" int moe_rope(const moe_rope_t* R, const void* x, int x_type, int64_t 
   if (!aligned(x, size) || !aligned(out, size) || !aligned(pos, 4) || !aligned(R->steps, 8))
     return MOE_ERR_ALIGNMENT;
   // (rows' groups of heads and workgroups of a launch)
-  if ((int64_t)rows * n_heads >= ((int64_t)1 << 32)) return MOE_ERR_SHAPE;
+  if ((int64_t)rows * n_heads >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
   if (x_type == MOE_TYPE_F32)
     rope_launch<float>(R, x, ld_x, hs_x, rows, n_heads, head_dim, pos, ld_pos, out, ld_out, hs_out,

@@ -378,3 +378,135 @@ def test_refused_in_the_binding():
         m.moe_attn_cache(attn, paged.cache, queries(2, 4, 64, torch.float32), table, lens)
     with pytest.raises(m.MoeError):                 # 3 query heads for 2 key heads
         m.moe_attn_cache(m.Attention(3, 0.125), paged.cache, q[:, :3].contiguous(), table, lens)
+
+
+# ------------------------------------------------- the forms for many rows and long texts
+@pytest.mark.parametrize("dim,kv,heads,rows,n", [(64, 8, 32, 2048, 2100), (128, 8, 32, 2048, 2100),
+                                                 (64, 32, 32, 1030, 1200)])
+def test_workgroups_of_256_rows(dim, kv, heads, rows, n):
+    """Enough tiles of 256 rows for every CU; some of the rows against the 64-bit form."""
+    dtype, page = torch.bfloat16, 32
+    paged = ref.Paged([n, 70], kv, dim, page, 20, dtype=dtype)
+    q = queries(rows + 1, heads, dim, dtype)
+    scale = float(np.float32(dim ** -0.5))
+    out = call(paged, q, [rows, 1], scale, window=900)
+    k, v = paged.values(0)
+    some = [0, 1, 63, 64, 65, rows // 2, rows - 2, rows - 1]
+    for r in some:
+        last = n - rows + r + 1
+        want, size, ds = ref.attention(ref.f64(q[r: r + 1]), k[:last], v[:last], scale, window=900)
+        ref.check(out[r: r + 1], want, ref.attention_error(size, ds, last, dtype), dtype)
+    ref.check_batch(out[rows:], _only(paged, 1), q[rows:], [1], dtype, scale, window=900)
+
+
+def _only(paged, s):
+    class One:
+        lens = [paged.lens[s]]
+
+        @staticmethod
+        def values(_):
+            return paged.values(s)
+    return One
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_rows_over_a_long_text_are_cut(dtype):
+    """Tiles of many rows whose tokens are cut and joined (a wave for each row's head); the heads'
+    group does not divide a tile, so that a row's heads lie in two."""
+    run([3000, 40], [300, 40], 7, 1, 64, 64, dtype)
+    run([2600], [110], 24, 1, 128, 64, dtype, window=2500, softcap=20.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new", [3, 90])
+def test_nan_blocks_and_bad_pages_in_cut_calls(new, dtype):
+    """NaN keys, NaN values and a page that is none, in a text that is cut, for few and many rows."""
+    n, heads = 4000, 4
+    paged = ref.Paged([n], 1, 64, 16, 21, dtype=dtype)
+    paged.v[0][1000, 0, 40] = float("nan")
+    paged.k[0][n - new + 1, 0, 2] = float("nan")
+    m.moe_kv_write(paged.cache, paged.k[0].cuda(), paged.v[0].cuda(), paged.slots[0].cuda())
+    q = queries(new, heads, 64, dtype)
+    out = call(paged, q, [new], 0.125)
+    ref.check_batch(out, paged, q, [new], dtype, 0.125)
+    bad = torch.isnan(out)
+    assert bad[0, :, 32:].all() and not bad[0, :, :32].any() and bad[1:].all()
+    paged.table[0, 5] = -7                       # tokens 80 .. 95
+    out = call(paged, q, [new], 0.125)
+    assert torch.isnan(out).all()
+    out = call(paged, q, [new], 0.125, window=n - 200)   # (sees 1000 and not 95)
+    assert torch.equal(torch.isnan(out), bad)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_out_of_range_lengths_with_many_rows(dtype):
+    lens = [256, 200]
+    paged = ref.Paged(lens, 1, 64, 16, 22, wide=16, dtype=dtype)
+    q = queries(160, 2, 64, dtype)
+    attn = m.Attention(2, 0.125)
+    table = paged.table.cuda()
+
+    def go(lens, off):
+        out = torch.full_like(q, 3.0)
+        m.moe_attn_cache(attn, paged.cache, q, table, i32(lens), q_offsets=i32(off), out=out)
+        return out
+    good = go(lens, [0, 80, 160])
+    ref.check_batch(good, paged, q, [80, 80], dtype, 0.125)
+    assert torch.equal(go([10**9, 200], [0, 80, 160]), good)
+    assert torch.equal(go(lens, [0, 80, 10**6]), good)
+    out = go([-1, 200], [0, 80, 160])
+    assert not out[:80].any() and torch.equal(out[80:], good[80:])
+    for off in ([0, 160, 80], [160, 0, 160], [80, 80, 20], [-9, -3, 0]):
+        go(lens, off)
+    # a row whose place is below 0 sees nothing
+    out = go([30, 200], [0, 80, 160])
+    assert not out[:50].any() and out[50:80].any()
+
+
+def test_a_cache_past_4_gib():
+    """Pages at both ends of a cache of more than 4 GiB, for few and many rows."""
+    kv, dim, page = 32, 128, 256
+    per = kv * page * (dim + dim // 16)
+    n_pages = 2**32 // per + 5
+    cache = m.KVCache(n_pages, page, kv, dim)
+    g = torch.Generator().manual_seed(3)
+    pages = torch.tensor([n_pages - 1, 0, n_pages - 3], dtype=torch.int32)
+    n = 600
+    t = torch.arange(n)
+    slots = (pages.long()[t // page] * page + t % page).int().cuda()
+    k, v = torch.randn(2, n, kv, dim, generator=g).bfloat16()
+    m.moe_kv_write(cache, k.cuda(), v.cuda(), slots)
+    kk, vv = ref.stored(ref.f64(k)), ref.stored(ref.f64(v))
+    scale = float(np.float32(dim ** -0.5))
+    attn = m.Attention(kv, scale)
+    for new in (1, 80):
+        q = queries(new, kv, dim, torch.bfloat16)
+        out = m.moe_attn_cache(attn, cache, q, pages.cuda()[None], i32([n]), q_offsets=i32([0, new]))
+        want, size, ds = ref.attention(ref.f64(q), kk, vv, scale)
+        ref.check(out, want, ref.attention_error(size, ds, n, torch.bfloat16), torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_scales_that_are_not_positive(scale, dtype):
+    scale = float(np.float32(scale))
+    paged = ref.Paged([200], 1, 64, 16, 23, dtype=dtype)
+    for new in (2, 100):
+        q = queries(new, 2, 64, dtype)
+        ref.check_batch(call(paged, q, [new], scale), paged, q, [new], dtype, scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scores_that_grow_along_the_text(dtype):
+    """Each stretch of tokens outweighs all before it, and then falls: bases are raised again and
+    again, and what came before leaves the sums."""
+    n, dim = 700, 64
+    paged = ref.Paged([n], 1, dim, 16, 24, dtype=dtype)
+    t = torch.arange(n)
+    height = 3.0 * torch.floor(t / 16) * (t < 500) - 40.0 * (t >= 500)
+    paged.k[0][:, 0, :32] = (height[:, None] / 8).to(dtype)
+    m.moe_kv_write(paged.cache, paged.k[0].cuda(), paged.v[0].cuda(), paged.slots[0].cuda())
+    for new in (1, 5, 120):
+        q = queries(new, 2, dim, dtype)
+        q[:, :, :32] = 0.5
+        ref.check_batch(call(paged, q, [new], 1.0), paged, q, [new], dtype, 1.0)
