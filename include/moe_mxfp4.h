@@ -666,10 +666,11 @@ size_t moe_attn_cache_workspace_bytes(const moe_attn_t* A, const moe_kv_cache_t*
  * they hold is kept within the arguments: offsets within 0..rows, lengths within
  * 0..max_pages * page; a token whose table entry is no page of the cache counts as
  * NaN.  Masked tokens change nothing, whatever the cache holds there.
- * Scores, softmax and sums are fp32; q is exact (f32: in three bf16 parts), as
- * the cache's values are; softmax weights enter the second product as bf16 (f32:
- * in three parts).  rows * (n_heads / cache heads) < 2^28, max_pages * page <
- * 2^30, n_seqs <= 2^24; rows == 0 or n_seqs == 0 is a no-op. */
+ * Scores, softmax and sums are fp32, the cache's values exact.  q: bf16 calls keep
+ * all 8 bits of a channel's number, less what lies below 2^-22 of the largest of its
+ * 32 channels, f32 calls all 24.  Softmax weights enter the second product as bf16
+ * (f32 calls: with all 24 bits).  rows * (n_heads / cache heads) < 2^28, max_pages *
+ * page < 2^30, n_seqs <= 2^24; rows == 0 or n_seqs == 0 is a no-op. */
 int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, const void* q, int type,
                    int64_t ld_q, int64_t hs_q, int rows, const int32_t* q_offsets, int n_seqs,
                    const int32_t* kv_lens, const int32_t* table, int64_t ld_table, int max_pages,

@@ -114,13 +114,15 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int item, Found& f)
   return item >= f.first_item && item - f.first_item < f.seq.tiles(a);
 }
 
-__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_incl_scan(v), 63); }
+__device__ __forceinline__ int wave_sum(int v) {
+  return __builtin_amdgcn_readlane(wave_incl_scan(v), 63);
+}
 
 // Cut calls (few tiles, so few sequences): a piece has `cut` tokens, as many for every sequence, and
 // items are counted over the sequences.  The cut is the batch's work over `target` pieces where
 // that makes no more than `target` of them (a sequence's last piece is a whole one there), or over
-// fewer pieces by half a piece, or a whole one, for each tile.  (Counts of one sequence are kept below 2^24 or 2^25, so that offsets
-// that overlap cannot make a sum of 64 overflow.)
+// fewer pieces by half a piece, or a whole one, for each tile.  (Counts of one sequence are kept below
+// 2^24 or 2^25, so that offsets that overlap cannot make a sum of 64 overflow.)
 __device__ __forceinline__ bool find_piece(const AttnArgs& a, int item, Found& f, int& cut) {
   const int lane = lane_id();
   Seq q = {0, 0, 0, 0};
@@ -224,7 +226,8 @@ __device__ __forceinline__ Sight sight_of(const AttnArgs& a, const Seq& s, int t
 struct RowRecord {
   int first_item, pieces, tiles, row0;  // pieces negative: the row sees nothing
 };
-__device__ __forceinline__ void put_record(const AttnArgs& a, const Found& f, int token, const Sight& see) {
+__device__ __forceinline__ void put_record(const AttnArgs& a, const Found& f, int token,
+                                           const Sight& see) {
   RowRecord r = {f.first_item, see.lo < see.hi ? f.pieces : -f.pieces, f.seq.tiles(a), f.seq.row0};
   if (f.pieces == 1) r.pieces = 1;
   ((RowRecord*)(a.part + a.rec_at))[f.seq.row0 + token] = r;
@@ -271,19 +274,33 @@ __device__ __forceinline__ float sum16(float v) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// softcap * tanh(s / softcap); k = 2 log2(e) / softcap.  For bf16
-// calls cap - 2 cap / (1 + e^2x); for f32 ones (1 - e^-2x) / (1 + e^-2x), the reciprocal refined:
-// off by at most 2^-24 of the cap, which is what a score near it is rounded to.
+// softcap * tanh(x), x = s / softcap; k = 2 log2(e) / softcap.  Caps up to kNearCap: bf16 calls
+// cap - 2 cap / (1 + e^2x), f32 ones cap (1 - e^-2x) / (1 + e^-2x) with the reciprocal refined, off by
+// at most 2^-23 and 2^-24 of the cap, which is what scores near it are rounded to.  Wider caps leave
+// most scores far below them, where that would be much: below x = 1/4 the series of tanh x / x, whose
+// first dropped term is 2^-26, and the quotient from there on.
+constexpr float kNearCap = 64.f;
+__device__ __forceinline__ float cap_factor(float cap) {
+  return cap > 0.f ? fminf(2.f * kLog2e / cap, 3.4e38f) : 0.f;
+}
+__device__ __forceinline__ float capped_quotient(float s, float cap, float k) {
+  const float e = exp2_fast(-k * fabsf(s)), d = 1.f + e;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = fmaf(fmaf(-d, r, 1.f), r, r);
+  return copysignf(cap * ((1.f - e) * r), s);
+}
 template <bool F32>
 __device__ __forceinline__ float capped(float s, float cap, float k) {
-  if constexpr (!F32) {
-    return fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + exp2_fast(s * k)), cap);
-  } else {
-    const float e = exp2_fast(-k * fabsf(s)), d = 1.f + e;
-    float r = __builtin_amdgcn_rcpf(d);
-    r = fmaf(fmaf(-d, r, 1.f), r, r);
-    return copysignf(cap * ((1.f - e) * r), s);
-  }
+  if constexpr (F32) return capped_quotient(s, cap, k);
+  else return fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + exp2_fast(s * k)), cap);
+}
+__device__ __forceinline__ float capped_wide(float s, float cap, float k) {
+  const float x = s * (k * (0.5f / kLog2e)), z = x * x;
+  float p = 2.1869489e-2f;  // 62/2835, -17/315, 2/15, -1/3
+  p = fmaf(p, z, -5.3968254e-2f);
+  p = fmaf(p, z, 1.3333333e-1f);
+  p = fmaf(p, z, -3.3333333e-1f);
+  return z < 0.0625f ? fmaf(s * z, p, s) : capped_quotient(s, cap, k);
 }
 
 // 4 scale bytes, any above kMaxScaleByte (253..255)?
@@ -291,7 +308,8 @@ __device__ __forceinline__ uint32_t over_bytes(uint32_t x) {
   return ((x & 0x7F7F7F7Fu) + 0x03030303u) & x & 0x80808080u;
 }
 __device__ __forceinline__ float scale_byte(uint32_t word, int b) {
-  return __uint_as_float((b == 0 ? word << 23 : b == 3 ? word >> 1 : word >> (8 * b) << 23) & 0x7F800000u);
+  const uint32_t at = b == 0 ? word << 23 : b == 3 ? word >> 1 : word >> (8 * b) << 23;
+  return __uint_as_float(at & 0x7F800000u);
 }
 
 // Eight numbers as sums of PARTS bf16 numbers.  Three hold every fp32 bit: the upper 8 bits of the
@@ -357,7 +375,8 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v) {
   step(__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
   step(__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
   step(__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
-  if constexpr (LANES >= 16) step(__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));  // row_mirror
+  if constexpr (LANES >= 16)
+    step(__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));  // row_mirror
   if constexpr (LANES == 32) {
     const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
     v = s[0] > s[1] ? s[0] : s[1];

@@ -1,29 +1,39 @@
 // attn.hip -- attention of a ragged batch's rows over a 4-bit cache.
 //
-// One pass over the tokens with the running maximum and sum of a softmax: for 64 tokens at a time
+// One pass over the tokens with the running maximum and sum of a softmax, 32 tokens a step:
 //   S^T = K Q^T          (matrix core, tokens x rows)
 //   m' = max(m, max S),  P = 2^(S - m'),  l = l 2^(m - m') + sum P
 //   O^T = O^T 2^(m - m') + V^T P^T
 // with S in units of log2.  A tile's rows are (token, query head of the key head's group) pairs,
 // row r = token r / G, head r % G, so one pass over a key head's tokens serves its whole group.
+// Here are tiles of 16 or 32 rows a wave: few new rows a sequence, and every f32 call.  Tiles of 128 and
+// 256 rows are in attn_chunk.hip.
 //
-// Operands without a detour through LDS.  E2M1 values times a power of two are exact in bf16, and
-// the converter makes two of them in one instruction.  Lane l of a wave holds row l % 16 of an
-// operand and 8 elements of the contraction, group l / 16; which 8 is free, as long as both
-// operands agree:
-//   scores: group g has the channels g D/4 .. + D/4, which lie side by side in the cache, 8 at a
-//           time, so one load fetches a lane's part of a token;
+// Operands.  bf16 calls: keys' E2M1 codes and their scale bytes go into the scaled 8-bit matrix
+// instruction as they are in the cache, against q in two E4M3 planes.  f32 calls, and V in all: E2M1
+// values times a power of two are exact in bf16, and the converter makes two in one instruction.  Lane
+// l of a wave holds row l % 16 of an operand and a part of the contraction, group l / 16; which part
+// is free, as long as both operands agree:
+//   scores: group g has block g of 32 channels (of 4 at a time), which lie side by side in the cache;
 //   out:    group g has the tokens 4g .. 4g+3 and 16 + 4g .. + 3 of 32, since that is what it
 //           holds of S^T as the matrix core leaves it: P goes from one product into the next in
 //           the registers where it was made.  V's order in the cache makes these 4 tokens of
 //           D/16 channels one load.
-// Rounding: q, K and V are exact.  P is rounded to bf16 (relative 2^-9, of either sign, averaged
-// over the tokens); f32 calls split q and P into three bf16 parts each, which hold all 24 bits.
+// Rounding.  K and V are exact.  q in bf16 calls: all 8 bits, less what is below 2^-22 of the largest of
+// its block of 32 channels.  P is rounded to bf16 (relative 2^-9, of either sign, averaged over the
+// tokens).  f32 calls split q and P into three bf16 parts each, which hold all 24 bits.
 //
 // Work.  A call's tiles (sequence, rows) times key heads fill the chip or not; where they do not, a
 // sequence's tokens are cut into pieces of equal length, as many over all sequences as fill it,
-// and a second launch joins them.  Lengths are on the GPU alone, so every wave works out the
-// same cut from them.
+// and a second launch joins them.  Lengths are on the GPU alone, so a workgroup finds its tile and the
+// cut from them when it starts.
+//
+// What bounds it: the cache's bytes, read once for each tile, for few rows of long contexts; the
+// latency of the chain lengths -> page -> tokens -> softmax -> join for short ones; f32 calls the six
+// products for the scores and the weights.  32 query heads on 8 of 128 channels, one new row a request:
+//   64 requests of 4096 tokens  55 us (3.9 TB/s)     16 of 2048 to 8192   29 us with its join of 5
+//   one of 1003 tokens          9.3 us               one of 65536         25 us
+// and 5 new rows of 3 requests of up to 100001 tokens, 24 heads on 8: bf16 77 us (4.0 TB/s), f32 97 us.
 #include "attn.h"
 
 namespace moe {
@@ -31,16 +41,18 @@ namespace moe {
 // ------------------------------------------------------------------- the pass
 // SHARED: the waves of a workgroup have one tile of 16 NQ rows and take its tokens in turn, 32 each,
 // joined in LDS at the end; otherwise each wave has a tile of its own among the workgroup's.
-// A wave's next keys are on their way from memory while it has the scores, its next values when they
-// are used up: registers for one step's codes, which leaves room for more waves.
-// Workgroups of 4 waves that a CU holds (by their registers and LDS).
+// Each wave copies the tokens of its next two steps straight into LDS (one step for D 256, by the
+// room) while it has the current ones.  16 requests of 2048 to 8192 tokens took 53 us with codes loaded
+// into registers just before their use, 31 with copies into LDS.
+// Workgroups of 4 waves that a CU holds (by their registers and LDS):
 constexpr int resident(bool f32, int dim, int nq) {
   if (dim == 256) return nq == 1 ? 2 : 1;
   if (dim == 128) return nq == 1 ? 3 : 2;
   return f32 || nq == 2 ? 3 : 4;
 }
 template <typename T, int D, int NQ, int WAVES, bool SHARED>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D, NQ) : 1) void attn_rows_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D, NQ) : 1)
+void attn_rows_kernel(const AttnArgs a) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int NB = D / 32, NC = D / 16, NI = (D + 127) / 128, PARTS = F32 ? 3 : 1;
   constexpr int STEP = 32, STRIDE = SHARED ? STEP * WAVES : STEP;
@@ -145,7 +157,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
   const auto* pages = (const __attribute__((address_space(4))) int32_t*)(a.table + f.at * a.ld_table);
   const bool plain = a.softcap == 0.f && !a.slopes && a.scale > 0.f;
   const float qk_scale = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
-  const float cap_k = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
+  const float cap_k = cap_factor(a.softcap);
   const float unit_scale = plain ? qk_scale : 1.f;
 
   // ---- tokens: a wave's steps of 32, copied straight into its part of LDS, RING - 1 steps ahead.  16
@@ -204,11 +216,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
     }
   };
   constexpr int COPIES = D == 64 ? 3 : 5 * NI;
+  // Tiles of many rows copy their last tokens again for the steps past the end, so that nothing
+  // depends on how many are left: 1024 new rows of a request of 2048 tokens, 32 query heads on 8 of
+  // 128, f32: 103 -> 98 us.  For a single row the copies themselves count: 1003 tokens in bf16 take
+  // 9.3 us without them, 10.0 with them.
+  constexpr bool PAST_END = !SHARED;
   if (n_steps) {
     load_pages(0);
 #pragma unroll
     for (int i = 0; i < RING - 1; ++i) {
-      if (i == 0 || i < n_steps) copy(ring[i], i);
+      if (PAST_END || i == 0 || i < n_steps) copy(ring[i], i);
       else bad <<= 2;
     }
   }
@@ -300,7 +317,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0
     asm volatile("" ::: "memory");
-    if (step + RING - 1 < n_steps) {
+    if (PAST_END || step + RING - 1 < n_steps) {
       copy(to, step + RING - 1);
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt((RING - 1) * COPIES | 0xF70);  // vmcnt
@@ -351,8 +368,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
           const v8i32 k = {(int)kk[0], (int)kk[1], (int)kk[2], (int)kk[3], 0, 0, 0, 0};
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq) {
-            c[nq] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, qh[nq][i], c[nq], 4, 0, 0, (int)sb, 0, e0[nq][i]);
-            c[nq] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, ql[nq][i], c[nq], 4, 0, 0, (int)sb, 0, e1[nq][i]);
+            c[nq] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                k, qh[nq][i], c[nq], 4, 0, 0, (int)sb, 0, e0[nq][i]);
+            c[nq] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                k, ql[nq][i], c[nq], 4, 0, 0, (int)sb, 0, e1[nq][i]);
           }
         }
       }
@@ -362,18 +381,31 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
         for (int e = 0; e < 4; ++e) s[nq][u][e] = c[nq][e];
     }
     if (!plain) {
+      const auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int nq = 0; nq < NQ; ++nq)
+        for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = s[nq][u][e] * qk_scale;
-            if (a.softcap > 0.f) x = capped<F32>(x, a.softcap, cap_k) * kLog2e;
-            const int j = t + 16 * u + 4 * g + e;
-            if (a.slopes) x -= slope[nq] * (float)abs(sq.n - sq.m + tok[nq] - j);
-            s[nq][u][e] = x;
-          }
+            for (int e = 0; e < 4; ++e) s[nq][u][e] = f(s[nq][u][e] * qk_scale);
+      };
+      if (a.softcap > kNearCap)
+        each([&](float x) { return capped_wide(x, a.softcap, cap_k) * kLog2e; });
+      else if (a.softcap > 0.f)
+        each([&](float x) { return capped<F32>(x, a.softcap, cap_k) * kLog2e; });
+      else
+        each([](float x) { return x; });
+      if (a.slopes) {
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = t + 16 * u + 4 * g + e;
+              s[nq][u][e] -= slope[nq] * (float)abs(sq.n - sq.m + tok[nq] - j);
+            }
+      }
     }
     if (t < all_lo || t + STEP > all_hi) {
 #pragma unroll
@@ -498,6 +530,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
       pass(step + i, ring[i], ring[(i + RING - 1) % RING]);
     }
   }
+  if constexpr (PAST_END) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+    asm volatile("" ::: "memory");
+  }
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) l[nq] = sum16(l[nq]);
 
@@ -618,7 +655,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D
 }
 
 // Pieces into rows: WAVES waves for each (row, head).  A lane has a piece's base and sum, then D/64
-// channels of pieces w, w + WAVES, ..
+// channels of pieces w, w + WAVES, ..  A launch of its own, 5 us, most of them its start and its chain
+// record -> bases -> parts: the pieces' bytes are few.
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
   constexpr int PER = D / 64, BATCH = 8;

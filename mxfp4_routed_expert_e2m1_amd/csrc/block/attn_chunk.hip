@@ -230,7 +230,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
 
   const bool plain = a.softcap == 0.f && !a.slopes && a.scale > 0.f;
   const float qk_scale = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
-  const float cap_k = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
+  const float cap_k = cap_factor(a.softcap);
   const float unit_scale = plain ? qk_scale : 1.f;
 
   const auto arrived = [] {  // every load and copy that this wave has started
@@ -328,16 +328,27 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
         }
       }
       if (!plain) {
+        const auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x = s[u][e] * qk_scale;
-            if (a.softcap > 0.f) x = capped<false>(x, a.softcap, cap_k) * kLog2e;
-            const int j = t + 32 * u + 8 * (e >> 2) + 4 * h + (e & 3);
-            if (a.slopes) x -= slope * (float)abs(place - j);
-            s[u][e] = x;
-          }
+            for (int e = 0; e < 16; ++e) s[u][e] = f(s[u][e] * qk_scale);
+        };
+        if (a.softcap > kNearCap)
+          each([&](float x) { return capped_wide(x, a.softcap, cap_k) * kLog2e; });
+        else if (a.softcap > 0.f)
+          each([&](float x) { return capped<false>(x, a.softcap, cap_k) * kLog2e; });
+        else
+          each([](float x) { return x; });
+        if (a.slopes) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int j = t + 32 * u + 8 * (e >> 2) + 4 * h + (e & 3);
+              s[u][e] -= slope * (float)abs(place - j);
+            }
+        }
       }
       if (t < all_lo || t + 64 > all_hi) {
 #pragma unroll

@@ -102,6 +102,16 @@ def test_capped_scores(grow, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("cap", [1e-39, 70.0, 1e4, 1e30, 3e38])
+def test_caps_far_from_the_scores(cap, dtype):
+    """Caps that hardly bend the scores (where a tanh times its cap loses what is small against it),
+    that bend some, and one below the normal numbers, under which all tokens weigh the same."""
+    run([300, 40], [130, 1], 4, 2, 64, 16, dtype, softcap=float(np.float32(cap)), grow=8.0)
+    run([300, 40], None, 4, 2, 128, 16, dtype, softcap=float(np.float32(cap)), grow=8.0)
+    run([300], [100], 4, 2, 64, 16, dtype, softcap=float(np.float32(cap)), grow=8.0, slopes=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_bias_by_distance(dtype):
     run([200, 700], [50, 3], 6, 2, 64, 16, dtype, slopes=True)
     run([200, 700], [50, 3], 6, 2, 64, 16, dtype, slopes=True, softcap=20.0, window=100,
