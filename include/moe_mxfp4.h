@@ -580,8 +580,9 @@ typedef struct moe_rope {
  *        with more than one axis
  *   out  of x's type (device, out); may be x itself with the same strides
  * Query and key heads that are neighbours in a fused projection take one call.
- * One rounding at the end.  rows * n_heads < 2^31; rows == 0 or n_heads == 0 is
- * a no-op. */
+ * One rounding at the end.  rows * n_heads < 2^31, in fewer than 2^32 threads (of 8
+ * pairs, or 8 channels to copy, of up to 8 heads); rows == 0 or n_heads == 0 is a
+ * no-op. */
 int moe_rope(const moe_rope_t* R, const void* x, int x_type, int64_t ld_x, int64_t hs_x,
              int rows, int n_heads, int head_dim, const int32_t* pos, int64_t ld_pos, void* out,
              int64_t ld_out, int64_t hs_out, void* stream);
@@ -614,7 +615,8 @@ size_t moe_kv_cache_bytes(const moe_kv_cache_t* C);
  *   slots  int32 [rows] (device); a row whose slot is negative or past the cache is
  *          skipped.  Two rows of one call with the same slot leave a mix of both
  *          in it.
- * Other slots are left as they are. */
+ * Other slots are left as they are.  rows * n_heads * head_dim < 2^35 (also to read);
+ * rows == 0 is a no-op. */
 int moe_kv_write(const moe_kv_cache_t* C, const void* k, int64_t ld_k, int64_t hs_k,
                  const void* v, int64_t ld_v, int64_t hs_v, int type, int rows,
                  const int32_t* slots, void* stream);

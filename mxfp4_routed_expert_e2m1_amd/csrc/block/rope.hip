@@ -6,7 +6,9 @@
 // frequency's own rounding; its two top bits (rounded) are the quadrant, the rest an angle within
 // +-pi/4, where Taylor's series to x^9 (sine) and x^10 (cosine) are off by 2e-9 and 1e-10.
 //
-// Bound by memory: each element is read and written once, 16 bytes a lane.  A thread holds the
+// Bound by memory: each element is read and written once, 16 bytes a lane (4096 rows of 40 heads of
+// 128, bf16: 17.0 us, 4.9 TB/s; through the L2s 20.8); a row or some hundreds by the chain position ->
+// sine -> row (4.0 and 6.5 us).  A thread holds the
 // sines and cosines of 8 pairs and takes several heads with them where there are rows enough to
 // fill the chip without splitting heads.
 #include "block.h"
@@ -160,30 +162,39 @@ __global__ __launch_bounds__(256) void rope_kernel(
   }
 }
 
-template <typename T>
-static void rope_launch(const moe_rope_t* R, const void* x, int64_t ld_x, int64_t hs_x, int rows,
-                        int n_heads, int dim, const int32_t* pos, int64_t ld_pos, void* out,
-                        int64_t ld_out, int64_t hs_out, hipStream_t stream) {
-  const int half = R->rot_dim / 2, pair_chunks = (half + 7) / 8;
-  const bool in_place = x == out;
-  const int chunks = pair_chunks + (in_place ? 0 : (dim - R->rot_dim + 7) / 8);
+// How a call's threads lie.
+struct RopePlan {
+  int pair_chunks, chunks, chunk_log, hpt, groups;
+  int64_t threads;
+};
+static RopePlan rope_plan(const moe_rope_t* R, int rows, int n_heads, int dim, bool in_place) {
+  RopePlan p;
+  p.pair_chunks = (R->rot_dim / 2 + 7) / 8;
+  p.chunks = p.pair_chunks + (in_place ? 0 : (dim - R->rot_dim + 7) / 8);
   // a head per thread until there are two workgroups for each CU, then up to 8 (4096 rows of 40 heads
   // of 128, bf16: 17.0 us; 4 heads 18.1, 2 heads 28.5)
-  const int64_t full = (int64_t)256 * 512;
-  int hpt = (int)((int64_t)rows * n_heads * chunks / full);
-  hpt = hpt < 1 ? 1 : hpt > 8 ? 8 : hpt;
-  const int groups = (n_heads + hpt - 1) / hpt;
-  int chunk_log = 0;
-  while ((1 << chunk_log) < chunks) ++chunk_log;
-  const int64_t threads = ((int64_t)rows * groups) << chunk_log;
-  const dim3 grid((unsigned)((threads + 255) / 256));
+  const int64_t hpt = (int64_t)rows * n_heads * p.chunks / (256 * 512);
+  p.hpt = hpt < 1 ? 1 : hpt > 8 ? 8 : (int)hpt;
+  p.groups = (n_heads + p.hpt - 1) / p.hpt;
+  p.chunk_log = 0;
+  while ((1 << p.chunk_log) < p.chunks) ++p.chunk_log;
+  p.threads = ((int64_t)rows * p.groups) << p.chunk_log;
+  return p;
+}
+
+template <typename T>
+static void rope_launch(const moe_rope_t* R, const RopePlan& p, const void* x, int64_t ld_x,
+                        int64_t hs_x, int rows, int n_heads, int dim, const int32_t* pos,
+                        int64_t ld_pos, void* out, int64_t ld_out, int64_t hs_out,
+                        hipStream_t stream) {
+  const dim3 grid((unsigned)((p.threads + 255) / 256));
   // (results of a call that fills the chip leave past the L2s)
-  const bool past = hpt > 1;
+  const bool past = p.hpt > 1;
   auto k = R->interleaved ? (past ? rope_kernel<T, true, true> : rope_kernel<T, true, false>)
                           : (past ? rope_kernel<T, false, true> : rope_kernel<T, false, false>);
   hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, (const T*)x, ld_x, hs_x, rows, n_heads, dim,
-                     half, pair_chunks, chunks, chunk_log, hpt, groups, pos, ld_pos, R->steps,
-                     R->axes, R->n_axes, R->scale, (T*)out, ld_out, hs_out);
+                     R->rot_dim / 2, p.pair_chunks, p.chunks, p.chunk_log, p.hpt, p.groups, pos,
+                     ld_pos, R->steps, R->axes, R->n_axes, R->scale, (T*)out, ld_out, hs_out);
 }
 
 }  // namespace moe
@@ -211,14 +222,16 @@ extern "C" int moe_rope(const moe_rope_t* R, const void* x, int x_type, int64_t 
   const size_t size = type_size(x_type);
   if (!aligned(x, size) || !aligned(out, size) || !aligned(pos, 4) || !aligned(R->steps, 8))
     return MOE_ERR_ALIGNMENT;
-  // (rows' groups of heads and workgroups of a launch)
+  // (rows' groups of heads and the threads of a launch)
   if ((int64_t)rows * n_heads >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
+  const RopePlan p = rope_plan(R, rows, n_heads, head_dim, x == out);
+  if (p.threads > 0xFFFFFF00) return MOE_ERR_SHAPE;
   if (!device_is_gfx950()) return MOE_ERR_UNSUPPORTED_ARCH;
   if (x_type == MOE_TYPE_F32)
-    rope_launch<float>(R, x, ld_x, hs_x, rows, n_heads, head_dim, pos, ld_pos, out, ld_out, hs_out,
+    rope_launch<float>(R, p, x, ld_x, hs_x, rows, n_heads, head_dim, pos, ld_pos, out, ld_out, hs_out,
                        (hipStream_t)stream);
   else
-    rope_launch<__bf16>(R, x, ld_x, hs_x, rows, n_heads, head_dim, pos, ld_pos, out, ld_out,
+    rope_launch<__bf16>(R, p, x, ld_x, hs_x, rows, n_heads, head_dim, pos, ld_pos, out, ld_out,
                         hs_out, (hipStream_t)stream);
   return launch_status();
 }

@@ -51,6 +51,8 @@ def test_rope_validation():
     assert call(ldo=512) == INVALID
     assert call(hs=256, ld=64, hso=64, ldo=256) == INVALID
     assert call(rows=2**31 - 1, heads=2**20, hs=64, ld=64 * 2**20, ldo=64 * 2**20) == SHAPE
+    # 32 pairs in 4 threads of one head, 2^32 of them
+    assert call(rows=2**30, heads=1, ld=64, ldo=64) == SHAPE
 
 
 def cache(heads=4, dim=64, page=16, pages=8, data=0x100000):
@@ -93,6 +95,8 @@ def test_write_and_read_validation(write):
         assert call(**{k: MIS4}) == ALIGN
     for kw in (dict(ldk=63), dict(ldk=255), dict(hsk=63), dict(ldv=255), dict(hsv=63)):
         assert call(**kw) == STRIDE, kw
+    assert call(rows=2**27) == SHAPE
+    assert call(rows=2**31 - 1) == SHAPE
 
 
 def attn(heads=8, window=0, scale=1.0, softcap=0.0, slopes=0):
