@@ -31,8 +31,8 @@
 // What bounds it: the cache's bytes, read once for each tile, for few rows of long contexts; the
 // latency of the chain lengths -> page -> tokens -> softmax -> join for short ones; f32 calls the six
 // products for the scores and the weights.  32 query heads on 8 of 128 channels, one new row a request:
-//   64 requests of 4096 tokens  55 us (3.9 TB/s)     16 of 2048 to 8192   29 us with its join of 5
-//   one of 1003 tokens          9.3 us               one of 65536         25 us
+//   64 requests of 2048 to 4096 tokens  55 us (3.9 TB/s)   16 of 2048 to 8192  29 us with its join of 5
+//   one of 1003 tokens  9.3 us                             one of 65536  25 us
 // and 5 new rows of 3 requests of up to 100001 tokens, 24 heads on 8: bf16 77 us (4.0 TB/s), f32 97 us.
 #include "attn.h"
 

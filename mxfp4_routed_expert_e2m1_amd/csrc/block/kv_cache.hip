@@ -4,9 +4,9 @@
 // threads a block of 32, whose largest magnitude is a maximum over the quad in registers.  The
 // scale is a power of two, so dividing by it is exact and the only rounding is the converter's,
 // to the nearest E2M1 value with ties to the even code.  Both kernels are bound by the rows in
-// memory (8 heads of 128, bf16: 4096 rows written 12.7 us, 3.3 TB/s; 65536 read 55 us, 6.1 TB/s, past
-// the L2s; a row of either 3 to 4), 32 times the scales and 4 to 8 times the codes; V's order (kv_cache.h) puts a token's
-// codes at 4-byte pieces, which meet in L2 with those of the 3 tokens beside it.
+// memory (8 heads of 128, bf16: 4096 rows written 7.1 us, read 6.2; 65536 read 55 us, 6.1 TB/s, past
+// the L2s; 16 rows 2.8), 32 times the scales and 4 to 8 times the codes; V's order (kv_cache.h)
+// puts a token's codes at 4-byte pieces, which meet in L2 with those of the 3 tokens beside it.
 #include "kv_cache.h"
 
 namespace moe {
