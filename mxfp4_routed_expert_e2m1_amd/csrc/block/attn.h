@@ -394,6 +394,6 @@ __device__ __forceinline__ uint32_t most_bits(const float (&x)[16]) {
 }
 
 // 256 rows or fewer of a sequence and one key head at a time, bf16 (attn_chunk.hip).
-void attn_chunk_launch(const AttnArgs& a, int head_dim, int waves, hipStream_t stream);
+void attn_chunk_launch(const AttnArgs& a, int head_dim, int tile_rows, bool halves, hipStream_t stream);
 
 }  // namespace moe

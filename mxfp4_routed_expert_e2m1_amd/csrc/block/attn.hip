@@ -746,9 +746,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
 // ------------------------------------------------------------------ the host side
 // How a call runs: the kernel and the rows of its tiles, the pieces to cut into.
 struct AttnPlan {
-  int chunk_waves; // 0: attn_rows_kernel
-  int nq;          // of attn_rows_kernel
-  bool shared, wide;
+  bool chunk;  // attn_chunk_kernel, or attn_rows_kernel
+  int nq;      // of attn_rows_kernel
+  bool shared, wide, halves;
   int tile_rows, quantum;
   int64_t tiles;   // at most, over all sequences
   int target;      // 0: tokens are not cut
@@ -766,17 +766,17 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
   const int64_t each = (rows * group + n_seqs - 1) / n_seqs;  // rows of a sequence, on average
   p.shared = each <= 64;
   p.nq = f32 || each <= 16 ? 1 : 2;
-  p.chunk_waves = f32 || p.shared ? 0 : 4;
+  p.chunk = !f32 && !p.shared;
   p.tile_rows = p.shared ? 16 * p.nq : f32 ? 64 : 128;
   p.quantum = p.shared ? 128 : 64;
   // workgroups that the chip holds at once
-  int64_t full = (p.chunk_waves ? 2 : resident(f32, C->head_dim, p.nq)) * cus;
-  if (p.chunk_waves && C->head_dim < 256 &&
-      tiles_of(rows, group, n_seqs, 256) * C->n_heads >= cus) {
-    p.chunk_waves = 8;
+  int64_t full = (p.chunk ? 2 : resident(f32, C->head_dim, p.nq)) * cus;
+  const auto tiles_of_256 = [&] {
     p.tile_rows = 256;
     full = cus;
-  }
+  };
+  if (p.chunk && C->head_dim < 256 && tiles_of(rows, group, n_seqs, 256) * C->n_heads >= cus)
+    tiles_of_256();
   p.tiles = tiles_of(rows, group, n_seqs, p.tile_rows);
   // Cutting shortens a workgroup's pass by the chip's idle part of it, and costs the joining launch
   // (5 us: the time of 900 tokens for few rows, of 2048 for many, which also have more to join).
@@ -784,13 +784,25 @@ static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
   // query heads each, us with 4 waves, 8 waves, cut:
   //   bf16   512 tokens 8.0, 7.4, 9.8   1000: 11.4, 9.3, 10.0   1500: 14.7, 11.5, 10.0
   //   f32    512 tokens 8.9, 8.3, 9.7   768: 11.3, 9.9, 9.6     1000: 13.8, 11.7, 9.8
-  const int64_t groups = p.tiles * C->n_heads;
+  int64_t groups = p.tiles * C->n_heads;
   int64_t span = tokens;  // that a tile's rows see at most
   if (A->window > 0 && A->window + p.tile_rows / group + 1 < span)
     span = A->window + p.tile_rows / group + 1;
   p.wide = p.shared && span > 256 && span <= (f32 ? 768 : 1024) && groups <= cus;
   const bool cut = !p.wide && groups < full &&
-                   span * (full - groups) / full >= (p.chunk_waves ? 2048 : f32 ? 700 : 900);
+                   span * (full - groups) / full >= (p.chunk ? 2048 : f32 ? 700 : 900);
+  // Tiles of 256 rows once there is work for all CUs, by their number or since they are cut: 200 and
+  // 512 new rows over 8192 tokens, 32 query heads on 8 of 128, 61.0 and 96.6 us in tiles of 128, 55.7
+  // and 89.5 in those.
+  if (cut && p.chunk && C->head_dim < 256 && each > 128 && p.tile_rows == 128) {
+    tiles_of_256();
+    p.tiles = tiles_of(rows, group, n_seqs, 256);
+    groups = p.tiles * C->n_heads;
+  }
+  // Few tiles: two waves for each 32 rows (512 new rows, 32 query heads on 8 of 128: 20.4 us with one,
+  // 19.4 with two; 500, 16 heads on 4 of 64: 14.9, 13.3; four prompts of 100, 32 on 8 of 128: 11.4, 13.2).
+  p.halves = p.chunk && !cut && C->head_dim < 256 && p.tile_rows == 128 && groups <= cus &&
+             span > 256;
   p.target = cut ? (int)((full + C->n_heads - 1) / C->n_heads) : 0;
   p.items = p.tiles + p.target;
   return p;
@@ -807,8 +819,8 @@ static bool attn_sizes_ok(const moe_attn_t* A, const moe_kv_cache_t* C) {
 
 template <typename T, int D>
 static void attn_launch(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  if (p.chunk_waves) {
-    attn_chunk_launch(a, D, p.chunk_waves, stream);
+  if (p.chunk) {
+    attn_chunk_launch(a, D, p.tile_rows, p.halves, stream);
   } else {
     const dim3 grid = item_grid(p.items, a.kv_heads);
     // (a tile of 32 rows and 256 channels has no room for 8 waves)

@@ -13,7 +13,10 @@
 //     LDS, in the order in which the lanes read them as operands.  The reads take half of LDS's
 //     rate, where the keys the same way would fill it.
 // A row's base of the exponential is raised when its maximum has grown by 2^8 (or is the first):
-// weights of up to 2^8 are as exact as those up to 1, and the accumulators are rarely rescaled.  (To do
+// weights of up to 2^8 are as exact as those up to 1, and the accumulators are rarely rescaled.  Bound by
+// the matrix core at the clock that the power limit leaves: 4096 new rows over 8192 tokens, 32 query
+// heads on 8 of 128, take 351 us, 1170 TF/s, what a large library product reaches.  Chunks with heads of
+// 64 are bound by their exponentials, short prompts by the chain before the first product.  (To do
 // without the maximum as long as the weights' sum stays small was slower, 477 us: the sum has to be
 // known before the products.)  The sum that divides is that of the rounded weights.
 #include "attn.h"
@@ -35,8 +38,11 @@ __device__ __forceinline__ f32x16 scores_32(v8i32 k, v8i32 q, f32x16 s, uint32_t
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, q, s, 4, 0, J, (int)scales, 0, e);
 }
 
-template <int D, int WAVES>
+// HALVES: two waves for the same 32 rows, each with 64 of a stage's 128 tokens, joined in LDS at the
+// end: for tiles that leave CUs idle, where a stage's time is its chain of steps and not its work.
+template <int D, int WAVES, bool HALVES>
 __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kernel(const AttnArgs a) {
+  constexpr int ROW_WAVES = HALVES ? WAVES / 2 : WAVES;
   constexpr int NB = D / 32, NI = NB / 2, NC = D / 16, RB = 32 / NC;
   constexpr int STAGE = 16 * WAVES;  // tokens between barriers: a quad of them for each 16 threads
   constexpr int BUF = STAGE * D * 2;
@@ -51,6 +57,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
   __shared__ uint32_t over[2][WAVES];
 
   const int wave = uniform((int)(threadIdx.x >> 6)), lane = lane_id();
+  const int rw = HALVES ? wave % ROW_WAVES : wave;  // rows 32 rw ..
   const int q32 = lane & 31, h = lane >> 5;
   const int item = block_item(), kvh = blockIdx.x;
 
@@ -64,14 +71,14 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
   const int up = f.pieces == 1 ? local : local / f.pieces, piece = local - up * f.pieces;
   const int tile = sq.tiles(a) - 1 - up;
   const int rows_here = sq.m * a.group;
-  const int tile0 = tile << a.tile_log, row0 = tile0 + 32 * wave;
+  const int tile0 = tile << a.tile_log, row0 = tile0 + 32 * rw;
   const RowSplit rs(a, tile0);
 
   // this lane's row, and what it sees
   const int r = row0 + q32;
   const bool real = r < rows_here;
   int tok, head;
-  rs.at(a, 32 * wave + q32, tok, head);
+  rs.at(a, 32 * rw + q32, tok, head);
   if (!real) tok = head = 0;
   head += kvh * a.group;
   Sight see = sight_of(a, sq, tok);
@@ -79,37 +86,18 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
   const float slope = a.slopes && real ? a.slopes[head] * kLog2e : 0.f;
   const int place = sq.n - sq.m + tok;
 
-  v8i32 qh[NI], ql[NI];
-  int e0[NI], e1[NI];
+  // q on its way: an 8-bit operand's lane has channels 16 h .. of both of its blocks, 32 (2i) + and
+  // 32 (2i + 1) +
+  Raw8<__bf16> qraw[NB][2];
   {
-    // an 8-bit operand's lane has channels 16 h .. of both of its blocks, 32 (2i) + and 32 (2i + 1) +
     const __bf16* qp = (const __bf16*)a.q + (int64_t)(sq.row0 + tok) * a.ld_q + head * a.hs_q + 16 * h;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      int e[2];
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float x[16] = {};
-        if (real) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v[8];
-            to_f32<__bf16>(load8(qp + 32 * (2 * i + b) + 8 * k), v);
-#pragma unroll
-            for (int n = 0; n < 8; ++n) x[8 * k + n] = v[n];
-          }
-        }
-        const uint32_t own = most_bits(x);
-        const auto other = __builtin_amdgcn_permlane32_swap(own, own, false, false);
-        const uint32_t most = other[0] > other[1] ? other[0] : other[1];
-        e[b] = plane_exponent(most);
-        if (b == 0) e4m3_planes<0>(x, e[b], qh[i], ql[i]);
-        else e4m3_planes<4>(x, e[b], qh[i], ql[i]);
-        if (most >= 0x7F800000u) e[b] = 255;  // infinite or NaN: so are all of its products
+      for (int k = 0; k < 2; ++k) {
+        qraw[b][k] = Raw8<__bf16>{};
+        if (real) qraw[b][k] = load8(qp + 32 * b + 8 * k);
       }
-      e0[i] = h ? e[1] : e[0];
-      e1[i] = e0[i] == 255 ? 255 : e0[i] - 5;
-    }
   }
 
   // the tokens of the workgroup's rows, of this wave's, and those that all of the wave's rows see
@@ -119,11 +107,11 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
     return sight_of(a, sq, uniform(t < sq.m - 1 ? t : sq.m - 1));
   };
   const int64_t p0 = sq.first(a) + (int64_t)piece * cut;
-  const int wg_lo0 = row_sight(0).lo, wg_hi0 = row_sight(32 * WAVES - 1).hi;
+  const int wg_lo0 = row_sight(0).lo, wg_hi0 = row_sight(32 * ROW_WAVES - 1).hi;
   const int wg_lo = p0 > wg_lo0 ? (int)p0 : wg_lo0 & ~(kStep - 1);
   const int wg_hi = p0 + cut < wg_hi0 ? (int)(p0 + cut) : wg_hi0;
   const bool any = row0 < rows_here;
-  const Sight s0 = row_sight(32 * wave), s1 = row_sight(32 * wave + 31);
+  const Sight s0 = row_sight(32 * rw), s1 = row_sight(32 * rw + 31);
   const int lo = s0.lo, hi = any ? s1.hi : 0;
   const int all_lo = s1.lo, all_hi = s0.hi;
 
@@ -222,6 +210,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
     if (lane == 0) over[buf][wave] = f2;
   };
 
+  v8i32 qh[NI], ql[NI];
+  int e0[NI], e1[NI];
   float m = -__builtin_inff(), l = 0.f;
   uint32_t nan_blocks = 0;  // blocks of channels in which this row has seen a NaN
   f32x16 acc[NB];
@@ -259,7 +249,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
     for (int w = 0; w < WAVES; ++w) nan_here |= over[buf][w];
     nan_here = uniform((int)nan_here);
 #pragma unroll
-    for (int half = 0; half < STAGE / 64; ++half) {
+    for (int part = 0; part < (HALVES ? 1 : STAGE / 64); ++part) {
+      const int half = HALVES ? wave / ROW_WAVES : part;
       const int t = t0 + 64 * half;
       if (t >= hi || t + 64 <= lo || t >= wg_hi) continue;
       // ---- scores: all operands on their way before the first product
@@ -426,6 +417,33 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
   if (wg_lo < wg_hi) {
     load_pages(wg_lo);
     load(wg_lo, kbuf0, kscale0);
+  }
+  // (while the first tokens are on their way)
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    int e[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float v[8];
+        to_f32<__bf16>(qraw[2 * i + b][k], v);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) x[8 * k + n] = v[n];
+      }
+      const uint32_t own = most_bits(x);
+      const auto other = __builtin_amdgcn_permlane32_swap(own, own, false, false);
+      const uint32_t most = other[0] > other[1] ? other[0] : other[1];
+      e[b] = plane_exponent(most);
+      if (b == 0) e4m3_planes<0>(x, e[b], qh[i], ql[i]);
+      else e4m3_planes<4>(x, e[b], qh[i], ql[i]);
+      if (most >= 0x7F800000u) e[b] = 255;  // infinite or NaN: so are all of its products
+    }
+    e0[i] = h ? e[1] : e[0];
+    e1[i] = e0[i] == 255 ? 255 : e0[i] - 5;
+  }
+  if (wg_lo < wg_hi) {
     arrived();
     v_store(0);
     lds_barrier();
@@ -435,6 +453,37 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
     if (t0 + STAGE < wg_hi) pass(t0 + STAGE, 1, kbuf1, kscale1, kbuf0, kscale0);
   }
   l = sum2(l);
+  if constexpr (HALVES) {
+    // (every wave is past its last read of the stages)
+    static_assert(WAVES == 8 && 4 * 64 * NB * 64 <= 2 * BUF);
+    __shared__ float others[3][ROW_WAVES][64];
+    float* const theirs = (float*)vbuf + rw * (NB * 16 * 64) + lane;
+    if (wave >= ROW_WAVES) {
+      others[0][rw][lane] = m;
+      others[1][rw][lane] = l;
+      others[2][rw][lane] = __uint_as_float(nan_blocks);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) theirs[(16 * b + e) * 64] = acc[b][e];
+    }
+    lds_barrier();
+    if (wave < ROW_WAVES) {
+      const float m2 = others[0][rw][lane], l2 = others[1][rw][lane];
+      nan_blocks |= __float_as_uint(others[2][rw][lane]);
+      const float up = fmaxf(m, m2), base = up == -__builtin_inff() ? 0.f : up;
+      // (a wave without weights has nothing to add)
+      const float k1 = l == 0.f ? 0.f : exp2_fast(m - base), k2 = l2 == 0.f ? 0.f : exp2_fast(m2 - base);
+      l = l * k1 + l2 * k2;
+      m = up;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[b][e] = acc[b][e] * k1 + theirs[(16 * b + e) * 64] * k2;
+    }
+    lds_barrier();  // (the rows' way out goes through the same memory)
+    if (wave >= ROW_WAVES) return;
+  }
   if (__ballot(nan_blocks != 0)) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -448,16 +497,16 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
   const bool sees = see.lo < see.hi;
   const bool part = f.pieces > 1;
   const float inv = part ? 1.f : sees ? 1.f / l : 0.f;
-  const int64_t slot0 = (((int64_t)item * a.kv_heads + kvh) << a.tile_log) + 32 * wave;
+  const int64_t slot0 = (((int64_t)item * a.kv_heads + kvh) << a.tile_log) + 32 * rw;
   if (part && real && h == 0) {
     a.part[a.ml_at + 2 * (slot0 + q32)] = m;
     a.part[a.ml_at + 2 * (slot0 + q32) + 1] = l;
   }
-  float* mine = (float*)vbuf + wave * 32 * LD;
+  float* mine = (float*)vbuf + rw * 32 * LD;
   const int orow = lane >> 1, oc = (lane & 1) * 16;
   const int orr = row0 + orow;
   int otok, ohead;
-  rs.at(a, 32 * wave + orow, otok, ohead);
+  rs.at(a, 32 * rw + orow, otok, ohead);
   __bf16* dst = (__bf16*)a.out + (int64_t)(sq.row0 + otok) * a.ld_out +
                 (int64_t)(kvh * a.group + ohead) * a.hs_out + oc;
 #pragma unroll
@@ -486,17 +535,23 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attn_chunk_kerne
   }
 }
 
-template <int D, int WAVES>
+template <int D, int WAVES, bool HALVES>
 static void launch_one(const AttnArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_chunk_kernel<D, WAVES>), item_grid(a.items, a.kv_heads),
+  hipLaunchKernelGGL((attn_chunk_kernel<D, WAVES, HALVES>), item_grid(a.items, a.kv_heads),
                      dim3(64 * WAVES), 0, stream, a);
 }
+template <int D>
+static void launch_dim(const AttnArgs& a, int tile_rows, bool halves, hipStream_t stream) {
+  if (halves) launch_one<D, 8, true>(a, stream);
+  else if (tile_rows == 256) launch_one<D, 8, false>(a, stream);
+  else launch_one<D, 4, false>(a, stream);
+}
 
-void attn_chunk_launch(const AttnArgs& a, int head_dim, int waves, hipStream_t stream) {
+void attn_chunk_launch(const AttnArgs& a, int head_dim, int tile_rows, bool halves, hipStream_t stream) {
   switch (head_dim) {
-    case 64: waves == 8 ? launch_one<64, 8>(a, stream) : launch_one<64, 4>(a, stream); break;
-    case 128: waves == 8 ? launch_one<128, 8>(a, stream) : launch_one<128, 4>(a, stream); break;
-    default: launch_one<256, 4>(a, stream); break;
+    case 64: launch_dim<64>(a, tile_rows, halves, stream); break;
+    case 128: launch_dim<128>(a, tile_rows, halves, stream); break;
+    default: launch_one<256, 4, false>(a, stream); break;
   }
 }
 

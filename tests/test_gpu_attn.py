@@ -419,6 +419,23 @@ def _only(paged, s):
     return One
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,n", [(1100, 1100), (1100, 1301)])
+def test_more_tiles_than_cus(rows, n, dim):
+    """Tiles of 128 rows that leave no CU idle, and are too few for those of 256."""
+    run([n], [rows], 32, 32, dim, 64, torch.bfloat16, window=150)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", [257, 319, 321, 383, 385, 400, 513])
+def test_two_waves_for_the_same_rows(n, dim):
+    """Few tiles: a stage's 128 tokens in two halves, of which one may be empty for a row, a wave or
+    all; from the text's start and behind a window."""
+    run([n], [70], 4, 2, dim, 16, torch.bfloat16)
+    run([n, 70, 127, 129, 200], [70, 70, 100, 65, 33], 4, 2, dim, 16, torch.bfloat16)
+    run([n, 5], [70, 3], 8, 2, dim, 32, torch.bfloat16, window=40, prefix=[90, 0], softcap=8.0)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_many_rows_over_a_long_text_are_cut(dtype):
     """Tiles of many rows whose tokens are cut and joined (a wave for each row's head); the heads'
