@@ -95,8 +95,8 @@ _TURN = ((10**70 << 192) + _PI_70) // (2 * _PI_70)
 def _step(frequency):
     """Turns per position in units of 2^-64 of a frequency in radians per position, rounded once
     and modulo a turn."""
-    num, den = float(frequency).as_integer_ratio()
-    return ((num * _TURN * 2 + (den << 128)) // (den << 129)) % 2**64
+    num, den = float(frequency).as_integer_ratio()  # (den is a power of two)
+    return ((num * _TURN >> den.bit_length() + 126) + 1 >> 1) % 2**64
 
 
 class Rope:
