@@ -2,6 +2,7 @@
 // of its work, what a row sees, scores beyond the product, reductions.
 #pragma once
 
+#include "attn_plan.h"
 #include "kv_cache.h"
 
 namespace moe {
@@ -9,7 +10,6 @@ namespace moe {
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kStep = 64;  // tokens to which pieces and the start of a pass are aligned
 
 struct AttnArgs {
   const void* q;
@@ -118,11 +118,15 @@ __device__ __forceinline__ int wave_sum(int v) {
   return __builtin_amdgcn_readlane(wave_incl_scan(v), 63);
 }
 
-// Cut calls (few tiles, so few sequences): a piece has `cut` tokens, as many for every sequence, and
-// items are counted over the sequences.  The cut is the batch's work over `target` pieces where
-// that makes no more than `target` of them (a sequence's last piece is a whole one there), or over
-// fewer pieces by half a piece, or a whole one, for each tile.  (Counts of one sequence are kept below
-// 2^24 or 2^25, so that offsets that overlap cannot make a sum of 64 overflow.)
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {  // of numbers below 2^48
+  const int low = wave_sum((int)(v & 0xFFFFFF));
+  return ((int64_t)wave_sum((int)(v >> 24)) << 24) + low;
+}
+
+// Cut calls (few tiles, so few sequences): a piece has `cut` tokens (choose_cut), as many for every
+// sequence, and items are counted over the sequences.  (A sequence's rows are below 2^28, so its tiles
+// below 2^24, and its pieces are kept below 2^24, so that offsets that overlap cannot make a sum of 64
+// overflow.)
 __device__ __forceinline__ bool find_piece(const AttnArgs& a, int item, Found& f, int& cut) {
   const int lane = lane_id();
   Seq q = {0, 0, 0, 0};
@@ -133,41 +137,29 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, int item, Found& f
     if (s0 + lane < a.n_seqs) {
       q.load(a, s0 + lane);
       tiles = q.tiles(a);
-      tiles = tiles < (1 << 24) ? tiles : 1 << 24;
       span = q.n - q.first(a);
     }
-  };
-  const auto steps = [&] {
-    const int64_t w = (int64_t)tiles * ((span + kStep - 1) / kStep);
-    return w < (1 << 25) ? (int)w : (1 << 25) - 1;
   };
   const auto items_of = [&](int pieces) {
     const int64_t n = (int64_t)tiles * pieces;
     return n < (1 << 24) ? (int)n : 1 << 24;
   };
   take(0);
-  int64_t work = wave_sum(steps()), all = wave_sum(tiles);
+  int64_t work = wave_sum(steps_of(tiles, span)), all = wave_sum(tiles);
   const bool one = a.n_seqs <= 64;
   if (!one) {
     for (int s0 = 64; s0 < a.n_seqs; s0 += 64) {
       take(s0);
-      work += wave_sum(steps());
+      work += wave_sum(steps_of(tiles, span));
       all += wave_sum(tiles);
     }
     take(0);
   }
-  for (int k = one ? 0 : 2;; ++k) {
-    int over = all < a.target ? a.target - (int)all * k / 2 : 0;
-    over = over > a.target / 2 ? over : (a.target + 1) / 2;
-    const uint32_t w = work < 0x7FFFFFFF ? (uint32_t)work : 0x7FFFFFFFu;
-    const int64_t c = (int64_t)((w + over - 1) / (uint32_t)over) * kStep;
-    const int64_t up = (c + a.quantum - 1) & ~(int64_t)(a.quantum - 1);
-    cut = uniform((int)(up < a.quantum ? a.quantum : up > 0x40000000 ? 0x40000000 : up));
-    if (k == 2 || wave_sum(items_of(span <= cut ? 1 : (span + cut - 1) / cut)) <= a.target) break;
-  }
+  cut = uniform(choose_cut(work, all, a.target, a.quantum, one,
+                           [&](int c) { return wave_sum(items_of(pieces_of(span, c))); }));
   int64_t before = 0;
   for (int s0 = 0;;) {
-    const int pieces = span <= cut ? 1 : (span + cut - 1) / cut;
+    const int pieces = pieces_of(span, cut);
     const int items = items_of(pieces), scan = wave_incl_scan(items);
     const int64_t end = before + scan;
     const bool mine = item < end && item >= end - items;

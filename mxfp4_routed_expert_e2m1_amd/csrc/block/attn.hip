@@ -44,12 +44,6 @@ namespace moe {
 // Each wave copies the tokens of its next two steps straight into LDS (one step for D 256, by the
 // room) while it has the current ones.  16 requests of 2048 to 8192 tokens took 53 us with codes loaded
 // into registers just before their use, 31 with copies into LDS.
-// Workgroups of 4 waves that a CU holds (by their registers and LDS):
-constexpr int resident(bool f32, int dim, int nq) {
-  if (dim == 256) return nq == 1 ? 2 : 1;
-  if (dim == 128) return nq == 1 ? 3 : 2;
-  return f32 || nq == 2 ? 3 : 4;
-}
 template <typename T, int D, int NQ, int WAVES, bool SHARED>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? resident(sizeof(T) == 4, D, NQ) : 1)
 void attn_rows_kernel(const AttnArgs a) {
@@ -744,75 +738,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
 }
 
 // ------------------------------------------------------------------ the host side
-// How a call runs: the kernel and the rows of its tiles, the pieces to cut into.
-struct AttnPlan {
-  bool chunk;  // attn_chunk_kernel, or attn_rows_kernel
-  int nq;      // of attn_rows_kernel
-  bool shared, wide, halves;
-  int tile_rows, quantum;
-  int64_t tiles;   // at most, over all sequences
-  int target;      // 0: tokens are not cut
-  int64_t items;   // of the grid
-};
-
-static int64_t tiles_of(int64_t rows, int64_t group, int64_t n_seqs, int tile_rows) {
-  return (rows * group + tile_rows - 1) / tile_rows + n_seqs;
-}
-
-static AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32, int64_t rows,
-                          int64_t n_seqs, int64_t tokens, int cus) {
-  AttnPlan p;
-  const int64_t group = A->n_heads / C->n_heads;
-  const int64_t each = (rows * group + n_seqs - 1) / n_seqs;  // rows of a sequence, on average
-  p.shared = each <= 64;
-  p.nq = f32 || each <= 16 ? 1 : 2;
-  p.chunk = !f32 && !p.shared;
-  p.tile_rows = p.shared ? 16 * p.nq : f32 ? 64 : 128;
-  p.quantum = p.shared ? 128 : 64;
-  // workgroups that the chip holds at once
-  int64_t full = (p.chunk ? 2 : resident(f32, C->head_dim, p.nq)) * cus;
-  const auto tiles_of_256 = [&] {
-    p.tile_rows = 256;
-    full = cus;
-  };
-  if (p.chunk && C->head_dim < 256 && tiles_of(rows, group, n_seqs, 256) * C->n_heads >= cus)
-    tiles_of_256();
-  p.tiles = tiles_of(rows, group, n_seqs, p.tile_rows);
-  // Cutting shortens a workgroup's pass by the chip's idle part of it, and costs the joining launch
-  // (5 us: the time of 900 tokens for few rows, of 2048 for many, which also have more to join).
-  // Below, few tiles get workgroups of twice the waves.  One request of 8 key heads of 128 with 4
-  // query heads each, us with 4 waves, 8 waves, cut:
-  //   bf16   512 tokens 8.0, 7.4, 9.8   1000: 11.4, 9.3, 10.0   1500: 14.7, 11.5, 10.0
-  //   f32    512 tokens 8.9, 8.3, 9.7   768: 11.3, 9.9, 9.6     1000: 13.8, 11.7, 9.8
-  int64_t groups = p.tiles * C->n_heads;
-  int64_t span = tokens;  // that a tile's rows see at most
-  if (A->window > 0 && A->window + p.tile_rows / group + 1 < span)
-    span = A->window + p.tile_rows / group + 1;
-  p.wide = p.shared && span > 256 && span <= (f32 ? 768 : 1024) && groups <= cus;
-  const bool cut = !p.wide && groups < full &&
-                   span * (full - groups) / full >= (p.chunk ? 2048 : f32 ? 700 : 900);
-  // Tiles of 256 rows once there is work for all CUs, by their number or since they are cut: 200 and
-  // 512 new rows over 8192 tokens, 32 query heads on 8 of 128, 61.0 and 96.6 us in tiles of 128, 55.7
-  // and 89.5 in those.
-  if (cut && p.chunk && C->head_dim < 256 && each > 128 && p.tile_rows == 128) {
-    tiles_of_256();
-    p.tiles = tiles_of(rows, group, n_seqs, 256);
-    groups = p.tiles * C->n_heads;
-  }
-  // Few tiles: two waves for each 32 rows (512 new rows, 32 query heads on 8 of 128: 20.4 us with one,
-  // 19.4 with two; 500, 16 heads on 4 of 64: 14.9, 13.3; four prompts of 100, 32 on 8 of 128: 11.4, 13.2).
-  p.halves = p.chunk && !cut && C->head_dim < 256 && p.tile_rows == 128 && groups <= cus &&
-             span > 256;
-  p.target = cut ? (int)((full + C->n_heads - 1) / C->n_heads) : 0;
-  p.items = p.tiles + p.target;
-  return p;
-}
-
-// Floats of a cut call's workspace: the pieces' rows, their bases and sums, the rows' records.
-static int64_t part_floats(const moe_kv_cache_t* C, int64_t items, int64_t tile_rows, int64_t rows) {
-  return items * C->n_heads * tile_rows * (C->head_dim + 2) + 4 * rows;
-}
-
 static bool attn_sizes_ok(const moe_attn_t* A, const moe_kv_cache_t* C) {
   return A->n_heads >= 1 && A->n_heads <= 16384 && A->n_heads % C->n_heads == 0;
 }
@@ -856,21 +781,7 @@ extern "C" size_t moe_attn_cache_workspace_bytes(const moe_attn_t* A, const moe_
   if (!A || !C || !kv_sizes_ok(C) || !attn_sizes_ok(A, C) || rows <= 0 || n_seqs <= 0) return 0;
   int cus = device_cu_count();
   if (cus <= 0) cus = 256;
-  // Cut calls have fewer than `full` tiles over all heads, so at most that many and their target
-  // pieces: no fewer rows or sequences need more.
-  const int64_t heads = C->n_heads;
-  const int64_t group = A->n_heads / heads;
-  int64_t most = 0;
-  for (int tile_rows : {16, 32, 64, 128, 256}) {
-    const int64_t full = (tile_rows <= 64 ? 4 : tile_rows == 128 ? 2 : 1) * cus;
-    const int64_t target = (full + heads - 1) / heads;
-    int64_t tiles = tiles_of(rows, group, n_seqs, tile_rows);
-    tiles = tiles < target ? tiles : target;
-    const int64_t most_rows = target * tile_rows;
-    const int64_t n = part_floats(C, tiles + target, tile_rows, rows < most_rows ? rows : most_rows);
-    most = n > most ? n : most;
-  }
-  return (size_t)most * 4;
+  return (size_t)attn_workspace(A, C, rows, n_seqs, cus);
 }
 
 extern "C" int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, const void* q,
