@@ -20,8 +20,11 @@
 //           the registers where it was made.  V's order in the cache makes these 4 tokens of
 //           D/16 channels one load.
 // Rounding.  K and V are exact.  q in bf16 calls: all 8 bits, less what is below 2^-22 of the largest of
-// its block of 32 channels.  P is rounded to bf16 (relative 2^-9, of either sign, averaged over the
-// tokens).  f32 calls split q and P into three bf16 parts each, which hold all 24 bits.
+// its block of 32 channels.  P is rounded to bf16 (by 2^-8 of a weight at most; the second product at this
+// rate has no more bits), and l is the sum of the rounded weights, by the matrix core: they are exact
+// weights of an average, so equal values are its result however they round (the sum of unrounded ones
+// left a row 2^-8 short where all rounded down, in the same time).  f32 calls split q and P into three
+// bf16 parts each, which hold all 24 bits.
 //
 // Work.  A call's tiles (sequence, rows) times key heads fill the chip or not; where they do not, a
 // sequence's tokens are cut into pieces of equal length, as many over all sequences as fill it,
@@ -135,9 +138,10 @@ void attn_rows_kernel(const AttnArgs a) {
   const int all_lo = s1.lo, all_hi = s0.hi;
 
   float m[NQ], l[NQ];
-  f32x4 acc[NQ][NC];
+  f32x4 acc[NQ][NC], lsum[NQ];  // (lsum: bf16 calls' l, in every register and group alike)
 #pragma unroll
   for (int nq = 0; nq < NQ; ++nq) {
+    lsum[nq] = f32x4{0.f, 0.f, 0.f, 0.f};
     m[nq] = -__builtin_inff();
     l[nq] = 0.f;
 #pragma unroll
@@ -460,6 +464,7 @@ void attn_rows_kernel(const AttnArgs a) {
         const float up = fmaxf(m[nq], top);
         const float old = exp2_fast(m[nq] - (up == -__builtin_inff() ? 0.f : up));
         l[nq] *= old;
+        lsum[nq] *= old;
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -472,7 +477,7 @@ void attn_rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float w = exp2_fast(fmaf(s[nq][u][e], unit_scale, -base));
-          l[nq] += w;
+          if constexpr (F32) l[nq] += w;
           s[nq][u][e] = w;
         }
       split8<PARTS>(s[nq], p[nq]);
@@ -516,6 +521,14 @@ void attn_rows_kernel(const AttnArgs a) {
               __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[nq][k], acc[nq][2 * b + 1], 0, 0, 0);
         }
     }
+    if constexpr (!F32) {
+      bf16x8 one;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) one[e] = (__bf16)1.f;
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq)
+        lsum[nq] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, p[nq][0], lsum[nq], 0, 0, 0);
+    }
   };
   for (int step = 0; step < n_steps; step += RING) {
 #pragma unroll
@@ -530,7 +543,7 @@ void attn_rows_kernel(const AttnArgs a) {
     asm volatile("" ::: "memory");
   }
 #pragma unroll
-  for (int nq = 0; nq < NQ; ++nq) l[nq] = sum16(l[nq]);
+  for (int nq = 0; nq < NQ; ++nq) l[nq] = F32 ? sum16(l[nq]) : lsum[nq][0];
 
   if (a.target && piece == 0 && kvh == 0 && g == 0 && (!SHARED || wave == 0)) {
 #pragma unroll
