@@ -67,7 +67,7 @@ inline bool head_strides_ok(int64_t ld, int64_t hs, int rows, int heads, int dim
   if (rows > 1 && (ld < dim || ld > kMost)) return false;
   if (heads > 1 && (hs < dim || hs > kMost)) return false;
   if (rows <= 1 || heads <= 1) return true;
-  return ld >= hs * (heads - 1) + dim || hs >= ld * (rows - 1) + dim;
+  return (ld - dim) / (heads - 1) >= hs || (hs - dim) / (rows - 1) >= ld;
 }
 
 }  // namespace moe
