@@ -654,9 +654,9 @@ size_t moe_attn_cache_workspace_bytes(const moe_attn_t* A, const moe_kv_cache_t*
                                       int n_seqs);
 
 /*   q         f32/bf16 [rows][n_heads][head_dim] (device)
- *   q_offsets int32 [n_seqs + 1] (device): sequence s has rows q_offsets[s] ..
- *             q_offsets[s+1] - 1; rows in no sequence are left as they are in
- *             out.  NULL: one row per sequence, rows == n_seqs.
+ *   q_offsets int32 [n_seqs + 1] (device), none less than the one before: sequence s
+ *             has rows q_offsets[s] .. q_offsets[s+1] - 1; rows in no sequence are
+ *             left as they are in out.  NULL: one row per sequence, rows == n_seqs.
  *   kv_lens   int32 [n_seqs] (device): cached tokens, the new rows among them
  *   table     int32 [n_seqs][ld_table] (device): a sequence's pages in order,
  *             max_pages <= ld_table of them readable (NULL with 0).  Entries past a
@@ -667,12 +667,17 @@ size_t moe_attn_cache_workspace_bytes(const moe_attn_t* A, const moe_kv_cache_t*
  * Lengths are read on the GPU, so a captured call replays with others.  What
  * they hold is kept within the arguments: offsets within 0..rows, lengths within
  * 0..max_pages * page; a token whose table entry is no page of the cache counts as
- * NaN.  Masked tokens change nothing, whatever the cache holds there.
+ * NaN.  Where offsets go back, the rows of any sequence may hold anything; rows in none
+ * are left.  Masked tokens change nothing, whatever the cache holds there.
  * Scores, softmax and sums are fp32, the cache's values exact.  q: bf16 calls keep
  * all 8 bits of a channel's number, less what lies below 2^-22 of the largest of its
  * 32 channels, f32 calls all 24.  Softmax weights enter the second product as bf16
- * (f32 calls: with all 24 bits).  rows * (n_heads / cache heads) < 2^28, max_pages *
- * page < 2^30, n_seqs <= 2^24; rows == 0 or n_seqs == 0 is a no-op. */
+ * (f32 calls: with all 24 bits) and are divided by the sum of what entered it.
+ * Kernel and tiles are chosen for the call as a whole, from rows / n_seqs and
+ * max_pages * page, which the host knows: chunks of a prompt and single tokens are
+ * faster in calls of their own, and so is a table of no more columns than the
+ * longest text needs.  rows * (n_heads / cache heads) < 2^28, max_pages * page <
+ * 2^30, n_seqs <= 2^24; rows == 0 or n_seqs == 0 is a no-op. */
 int moe_attn_cache(const moe_attn_t* A, const moe_kv_cache_t* C, const void* q, int type,
                    int64_t ld_q, int64_t hs_q, int rows, const int32_t* q_offsets, int n_seqs,
                    const int32_t* kv_lens, const int32_t* table, int64_t ld_table, int max_pages,

@@ -298,7 +298,8 @@ def moe_attn_cache(attn, cache, q, table, kv_lens, q_offsets=None, prefix=None, 
       kv_lens   int32 [n_seqs]: its cached tokens
       q_offsets int32 [n_seqs + 1]: its rows, q_offsets[s] .. q_offsets[s+1] - 1; None: one each
       prefix    int32 [n_seqs] or None: so many first tokens are seen by all of its rows
-    Returns out, of q's type."""
+    Chunks of a prompt and single tokens are faster in calls of their own, and with a table of no
+    more columns than the longest text needs.  Returns out, of q's type."""
     gpu = q.get_device()
     if stream is not None and (out is None or ws is None):
         _given(stream, gpu)

@@ -85,7 +85,9 @@ inline AttnPlan attn_plan(const moe_attn_t* A, const moe_kv_cache_t* C, bool f32
   //   bf16   512 tokens 8.0, 7.4, 9.8   1000: 11.4, 9.3, 10.0   1500: 14.7, 11.5, 10.0
   //   f32    512 tokens 8.9, 8.3, 9.7   768: 11.3, 9.9, 9.6     1000: 13.8, 11.7, 9.8
   int64_t groups = p.tiles * C->n_heads;
-  int64_t span = tokens;  // that a tile's rows see at most
+  // Tokens that a tile's rows see at most, as far as the window goes.  (With a prefix, rows in front of
+  // its end see up to it, so a window and a long prefix are planned as shorter than they are.)
+  int64_t span = tokens;
   if (A->window > 0 && A->window + p.tile_rows / group + 1 < span)
     span = A->window + p.tile_rows / group + 1;
   p.wide = p.shared && span > 256 && span <= (f32 ? 768 : 1024) && groups <= cus;
